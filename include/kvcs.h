@@ -1,5 +1,7 @@
 /*
- * kvcs.h -- C ABI of the GB300 (sm_103a) KV-cache block checksum library.
+ * kvcs.h -- C ABI of the GB300 (sm_103a) KV-cache block checksum library,
+ * with the operators that write, read (attention) and thin out (eviction)
+ * the same paged caches.
  *
  * What it computes (page "vllm.distributed.kv_transfer.kv_checksum.checksum",
  * vLLM API docs, module docstring items 1 and 2):
@@ -406,6 +408,157 @@ int kvcs_write_kv(const kvcs_cache *caches, int32_t num_caches, int32_t block_si
                   const int64_t *positions, uint64_t *block_sums, uint32_t *status,
                   void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over paged caches, and eviction from them
+ * ------------------------------------------------------------------------- */
+
+/* Element types of queries, outputs and cached K and V. */
+#define KVCS_DTYPE_BF16 0
+#define KVCS_DTYPE_FP16 1
+#define KVCS_DTYPE_FP8_E4M3 2 /* caches only */
+
+/*
+ * One attention (or attention-mass) call over one layer's cache, for the new
+ * tokens of a batch of requests.  Pointers are DEVICE pointers unless stated.
+ *
+ * Request r's new tokens are rows new_offsets[r] .. new_offsets[r+1] of q,
+ * and they are the last tokens of its num_tokens (their K and V are already
+ * in the cache: kvcs_write_kv).  So with n new tokens, new token i is at
+ * request position num_tokens[r] - n + i.  It sees cached tokens up to and
+ * including its own position, with a window only the last `window` of them;
+ * of these, those in the request's listed blocks (positions first_position
+ * on) and below num_tokens.  One token a request is a decode step, many are
+ * a prefill chunk; both may share a call.
+ *
+ * Query head h reads KV head h / (q_heads / num_heads).  The score of query i
+ * and token j is s = scale * k_scale * (q_i . k_j), with a softcap
+ * softcap * tanh(s / softcap) instead; the weights are its softmax over the
+ * visible tokens, and
+ *     out_i = v_scale * sum_j w_ij v_j,   lse_i = log sum_j exp(score_ij).
+ * A row that sees nothing has out 0 and lse -infinity.  Nothing in slots
+ * past num_tokens, nor in tokens that a row does not see, reaches the row,
+ * whatever the bytes there are (NaN and infinities included).
+ */
+typedef struct kvcs_attention {
+  const void *q;        /* [total_new][q_heads][head_dim], 16-byte aligned */
+  int64_t q_stride;     /* elements between rows of q, a multiple of 8;
+                           0 = q_heads * head_dim */
+  const int64_t *new_offsets; /* [R + 1], non-decreasing, within [0, total_new] */
+  int64_t total_new;    /* rows of q and out; rows no request owns are left
+                           as they were */
+  int64_t max_new;      /* most new tokens a request has, as known to the host
+                           (a request with more is flagged and its rows are
+                           left as they were); 0 = total_new */
+  int32_t q_heads;      /* a multiple of the cache's num_heads */
+  int32_t q_dtype;      /* KVCS_DTYPE_BF16 or _FP16; out has the same */
+  int32_t kv_dtype;     /* q_dtype, or KVCS_DTYPE_FP8_E4M3 */
+  float scale;          /* commonly head_dim ** -0.5 */
+  float softcap;        /* 0 = none */
+  float k_scale;        /* what a stored K value of 1 stands for; 1 unless quantised */
+  float v_scale;
+  int64_t window;       /* 0 = none */
+  void *out;            /* attention: [total_new][q_heads][head_dim], 16-byte aligned */
+  float *lse;           /* [total_new][q_heads], natural log.  Attention: written,
+                           or NULL.  Mass: read */
+  void *workspace;      /* attention: kvcs_attention_workspace bytes, 16-byte
+                           aligned; scratch of this call alone while it runs
+                           (calls that may overlap, and graphs that may run at
+                           the same time, need one each); needs no clearing */
+  int64_t workspace_bytes;
+  int64_t observe;      /* mass: only the last `observe` new tokens of each
+                           request count; 0 = all */
+} kvcs_attention;
+
+/*
+ * kvcs_attention_workspace -- bytes of workspace kvcs_paged_attention needs
+ * for a call of num_requests requests with these sizes (*att's pointers are
+ * not looked at).  num_sms as in kvcs_plan.  Returns its error codes.
+ */
+int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_t num_requests,
+                             const kvcs_attention *att, int32_t num_sms, int64_t *bytes);
+
+/*
+ * kvcs_paged_attention -- attention of a batch's new tokens over one layer's
+ * paged cache (NHD, HND with or without kernel sub-blocks, or XSPLIT; any
+ * strides).  Arguments as in kvcs_block_checksums, with *att (HOST) above;
+ * block_ids may repeat a block within and between requests (shared prefixes).
+ *
+ *   status  KVCS_STATUS_BAD_BLOCK_ID: a needed block id is outside the pool;
+ *           its tokens are left out, as if masked.  KVCS_STATUS_BAD_REQUESTS:
+ *           inconsistent tables (also more than 2^30 cached tokens in one
+ *           request): the request's rows see nothing (or, where its
+ *           new_offsets are at fault, are left as they were).
+ *
+ * Results do not depend on timing: the same call gives the same bits.
+ * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a
+ * STATE cache, types that do not go together, q_heads not a multiple of
+ * num_heads, a negative or non-finite size or scale, missing or misaligned
+ * pointers, or a short workspace; KVCS_EUNSUPPORTED for a LATENT cache, a
+ * head that is not 8 to 256 elements (a multiple of 8), a page of 2 GiB or
+ * more, or 2^31 or more query rows.
+ */
+int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs_requests *reqs,
+                         int64_t total_positions, const kvcs_attention *att, uint32_t *status,
+                         void *stream);
+
+/*
+ * kvcs_attention_mass -- adds to each cached token, per KV head, the weights
+ * it gets from the observed new tokens under all query heads of the head:
+ *     mass[block][head][slot] += sum_i exp(score_ij - lse_i).
+ * q, scores, visibility and errors as in kvcs_paged_attention; lse is that
+ * call's (read), out and the workspace are not used.
+ *   mass  float[num_blocks][num_heads][block_size], zeroed by the caller when
+ *         a block is allocated.  Tokens that no observed row sees are not
+ *         written.  Where requests share a block, the order in which their
+ *         sums are added is not fixed.
+ */
+int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_requests *reqs,
+                        int64_t total_positions, const kvcs_attention *att, float *mass,
+                        uint32_t *status, void *stream);
+
+/*
+ * One eviction.  A request's cached tokens are those of its listed blocks
+ * below num_tokens; N of them, and a budget B = min(keep[r], N).  Per cache
+ * and KV head (each with a choice of its own) the first min(sinks, B) tokens
+ * stay, the last min(recent, B - sinks) too, and of the others those with
+ * the greatest scores, as many as the budget leaves; equal scores go to the
+ * lowest index, and NaN counts as the greatest score.
+ */
+typedef struct kvcs_eviction {
+  float *const *scores; /* HOST array of num_caches DEVICE pointers, each
+                           [num_blocks][num_heads][block_size] as
+                           kvcs_attention_mass keeps it; moved along */
+  const int64_t *keep;  /* DEVICE [R]: tokens to keep */
+  int64_t sinks, recent;
+  const int32_t *new_block_ids; /* DEVICE [total_positions], or NULL = in place.
+                           The kept tokens of request r go to blocks
+                           new_block_ids[pos_offsets[r] ...], of which the
+                           first ceil(B / block_size) are used and must not
+                           be blocks that the call reads */
+  uint64_t *block_sums; /* DEVICE words, one per block, or NULL.  The words of
+                           the filled blocks become the checksums of their
+                           kept tokens (kvcs_write_kv's running words) over
+                           the caches of this call; in place, the words of
+                           the request's emptied blocks become 0 */
+} kvcs_eviction;
+
+/*
+ * kvcs_evict -- thins out the caches of a batch: the kept tokens' K, V (or
+ * latent rows) and scores move, in order, to the first B slots of the
+ * request's blocks, after which the request holds first_position *
+ * block_size + B tokens (the caller lowers num_tokens and frees blocks).
+ * Slots from B on keep their bytes.  All layouts but STATE; caches and other
+ * arguments as in kvcs_block_checksums.
+ *
+ * Blocks that the call writes must belong to one request alone (in place:
+ * all its blocks), listed once.  A request with a bad block id
+ * (KVCS_STATUS_BAD_BLOCK_ID), inconsistent tables or a negative keep
+ * (KVCS_STATUS_BAD_REQUESTS) is left untouched.
+ */
+int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
+               const kvcs_requests *reqs, int64_t total_positions, const kvcs_eviction *ev,
+               uint32_t *status, void *stream);
+
 /* Which kernel and launch shape kvcs_block_checksums would use.  Filled by
  * kvcs_plan and kvcs_plan_requests; no CUDA work is enqueued. */
 typedef struct kvcs_plan_info {
@@ -490,7 +643,9 @@ uint64_t kvcs_launch_count(void);
  * Minor 3 added kvcs_outputs.workspace, read only when flags has
  * KVCS_OUT_WORKSPACE (callers built against minor 2 never set it).
  * Minor 4 added kvcs_plan_requests and kvcs_plan_info.slot_launches (the
- * struct grew: callers pass the minor-4 layout). */
+ * struct grew: callers pass the minor-4 layout).  Minor 5 added
+ * kvcs_paged_attention, kvcs_attention_workspace, kvcs_attention_mass and
+ * kvcs_evict. */
 int32_t kvcs_version(void);
 
 #ifdef __cplusplus

@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) KV-cache block checksums.
+"""GB300 (sm_103a) KV-cache block checksums, and the operators around the same
+paged caches: writes, attention, attention mass and eviction.
 
 The checksum of page "vllm.distributed.kv_transfer.kv_checksum.checksum"
 (vLLM API docs): per block position, over every (layer, KV head) slice,
@@ -21,4 +22,7 @@ from ._binding import (  # noqa: F401
     workload_checksums, Checksummer, workload_checksummer, kvcs_outputs,
     group_checksums, block_checksum_tags, write_kv, KVWriter,
     KVCS_ETOOLARGE, KVCS_NOALLOC_MAX_CACHES, block_checksums_noalloc,
-    kvcs_block_checksums_noalloc)
+    kvcs_block_checksums_noalloc, KVCS_DTYPE_BF16, KVCS_DTYPE_FP16, KVCS_DTYPE_FP8_E4M3,
+    kvcs_attention, kvcs_eviction)
+from ._attention import (  # noqa: F401
+    attention_mass, attention_workspace_bytes, evict, paged_attention)

@@ -35,6 +35,10 @@ KVCS_OUT_WORKSPACE = 2
 KVCS_WORKSPACE_WORDS = 16
 KVCS_NOALLOC_MAX_CACHES = 1024
 
+KVCS_DTYPE_BF16 = 0
+KVCS_DTYPE_FP16 = 1
+KVCS_DTYPE_FP8_E4M3 = 2
+
 
 class kvcs_cache(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
@@ -59,6 +63,24 @@ class kvcs_requests(ctypes.Structure):
                 ("first_position", ctypes.c_void_p),
                 ("num_tokens", ctypes.c_void_p),
                 ("block_ids", ctypes.c_void_p)]
+
+
+class kvcs_attention(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("new_offsets", ctypes.c_void_p), ("total_new", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("q_dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("window", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64), ("observe", ctypes.c_int64)]
+
+
+class kvcs_eviction(ctypes.Structure):
+    _fields_ = [("scores", ctypes.POINTER(ctypes.c_void_p)), ("keep", ctypes.c_void_p),
+                ("sinks", ctypes.c_int64), ("recent", ctypes.c_int64),
+                ("new_block_ids", ctypes.c_void_p), ("block_sums", ctypes.c_void_p)]
 
 
 class kvcs_plan_info(ctypes.Structure):
@@ -95,6 +117,20 @@ SIGNATURES = {
         ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
         ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvcs_attention_workspace": (ctypes.c_int, [
+        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int64,
+        ctypes.POINTER(kvcs_attention), ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
+    "kvcs_paged_attention": (ctypes.c_int, [
+        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.POINTER(kvcs_requests),
+        ctypes.c_int64, ctypes.POINTER(kvcs_attention), ctypes.c_void_p, ctypes.c_void_p]),
+    "kvcs_attention_mass": (ctypes.c_int, [
+        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.POINTER(kvcs_requests),
+        ctypes.c_int64, ctypes.POINTER(kvcs_attention), ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p]),
+    "kvcs_evict": (ctypes.c_int, [
+        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int32,
+        ctypes.POINTER(kvcs_requests), ctypes.c_int64, ctypes.POINTER(kvcs_eviction),
+        ctypes.c_void_p, ctypes.c_void_p]),
     "kvcs_plan": (ctypes.c_int, [
         ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int32,
         ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(kvcs_plan_info)]),

@@ -1,7 +1,8 @@
 """Build the CUDA library ``_build/libkvcs.so`` for sm_103a with nvcc.
 
-One translation unit, one ``-gencode``; the CUDA runtime is linked
-statically so the library needs nothing but the driver at run time.
+One ``-gencode``; the translation units compile in parallel (the attention
+kernels once per cache type) and link into one library, with the CUDA
+runtime linked statically so that it needs nothing but the driver at run time.
 """
 
 from __future__ import annotations
@@ -9,6 +10,8 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -17,8 +20,11 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 OUT_DIR = PKG / "_build"
 LIB = OUT_DIR / "libkvcs.so"
-SOURCES = [CSRC / "kvcs.cu"]
-DEPS = SOURCES + sorted(CSRC.glob("*.cuh")) + [INCLUDE / "kvcs.h"]
+# (source, defines) of each object
+UNITS = [("kvcs.cu", ()), ("kvcs_attend.cu", ())] + [
+    ("kvcs_attend_type.cu", (f"-DKVCS_KV_TYPE={t}",)) for t in range(3)]
+DEPS = (sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h"))
+        + [INCLUDE / "kvcs.h"])
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -35,13 +41,22 @@ def build(force: bool = False, verbose: bool = False) -> Path:
             and LIB.stat().st_mtime >= max(p.stat().st_mtime for p in DEPS)):
         return LIB
     OUT_DIR.mkdir(exist_ok=True)
+    flags = [ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+             f"-I{INCLUDE}", f"-I{CSRC}", *(["-Xptxas", "-v"] if verbose else [])]
+
     tmp = OUT_DIR / f"libkvcs.so.tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared",
-           "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
-           "-cudart", "static", f"-I{INCLUDE}", f"-I{CSRC}",
-           *(["-Xptxas", "-v"] if verbose else []),
-           *map(str, SOURCES), "-o", str(tmp)]
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory(dir=OUT_DIR) as objects_dir:
+        def compile_unit(i: int) -> str:
+            source, defines = UNITS[i]
+            obj = str(Path(objects_dir) / f"unit{i}.o")
+            subprocess.run([nvcc(), *flags, *defines, "-c", str(CSRC / source), "-o", obj],
+                           check=True)
+            return obj
+
+        with ThreadPoolExecutor(len(UNITS)) as ex:
+            objects = list(ex.map(compile_unit, range(len(UNITS))))
+        subprocess.run([nvcc(), ARCH, "-shared", "-cudart", "static", *objects, "-o", str(tmp)],
+                       check=True)
     os.replace(tmp, LIB)
     return LIB
 

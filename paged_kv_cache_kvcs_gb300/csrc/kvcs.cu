@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "kvcs.h"
+#include "kvcs_attend_host.h"
 #include "kvcs_bulk.cuh"
 #include "kvcs_direct.cuh"
 #include "kvcs_slots.cuh"
@@ -826,6 +827,14 @@ int columns_of(const kvcs_cache *caches, int32_t num_caches) {
 }
 
 }  // namespace
+
+// What kvcs_attend.cu shares with this file.
+int check_caches(const kvcs_cache *caches, int32_t num_caches, int32_t block_size) {
+  return validate_caches(caches, num_caches, block_size, 1);
+}
+cudaError_t device_sms(int *sms) { return device_setup(sms); }
+void count_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
+
 }  // namespace kvcs
 
 using namespace kvcs;
@@ -1070,8 +1079,9 @@ const char *kvcs_strerror(int code) {
     case KVCS_OK: return "success";
     case KVCS_EINVAL: return "invalid argument";
     case KVCS_EUNSUPPORTED:
-      return "unsupported geometry (global heads past 65536 per layer, or a token row of 1 GiB "
-             "or more in a write)";
+      return "unsupported geometry (global heads past 65536 per layer, a token row of 1 GiB "
+             "or more in a write, or an attention call over latent rows or heads that are not "
+             "8 to 256 elements, a multiple of 8)";
     case KVCS_ECUDA: return "CUDA error";
     case KVCS_ETOOLARGE:
       return "beyond the fixed limit of kvcs_block_checksums_noalloc (more than "
@@ -1082,6 +1092,6 @@ const char *kvcs_strerror(int code) {
 
 uint64_t kvcs_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
-int32_t kvcs_version(void) { return (1 << 16) | 4; }
+int32_t kvcs_version(void) { return (1 << 16) | 5; }
 
 }  // extern "C"

@@ -1,0 +1,360 @@
+// kvcs_attend.cu -- host side of the operators that read and thin out paged
+// caches: attention of new tokens, attention mass, and eviction (kvcs.h).
+// As in kvcs.cu, host arguments are checked before any CUDA call, nothing is
+// allocated, and all work goes to the caller's stream.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <vector>
+
+#include "kvcs.h"
+#include "kvcs_attend_host.h"
+#include "kvcs_evict.cuh"
+
+namespace kvcs {
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int element_bytes(int kv_dtype) { return kv_dtype == KVCS_DTYPE_FP8_E4M3 ? 1 : 2; }
+
+PageMap page_map(const kvcs_cache &c, int block_size) {
+  PageMap m;
+  std::memset(&m, 0, sizeof(m));
+  const long long hb = c.head_bytes, heads = c.num_heads;
+  const long long page = block_size * heads * hb;
+  m.base = static_cast<const unsigned char *>(c.base);
+  m.num_blocks = c.num_blocks;
+  m.half_stride = c.half_stride ? c.half_stride : c.num_blocks * page;
+  m.block_stride = c.block_stride ? c.block_stride : page;
+  m.block_size = block_size;
+  m.kbs = block_size;
+  m.halves = c.layout == KVCS_LAYOUT_LATENT ? 1 : 2;
+  m.chunk_stride = 16;
+  switch (c.layout) {
+    case KVCS_LAYOUT_HND:
+      if (c.kernel_block_size > 0) m.kbs = c.kernel_block_size;
+      m.sub_stride = heads * m.kbs * hb;
+      m.slot_stride = static_cast<int>(hb);
+      m.head_stride = m.kbs * hb;
+      break;
+    case KVCS_LAYOUT_XSPLIT:
+      m.slot_stride = 16;
+      m.head_stride = block_size * hb;
+      m.chunk_stride = block_size * 16;
+      break;
+    default:  // NHD, latent
+      m.slot_stride = static_cast<int>(heads * hb);
+      m.head_stride = hb;
+      break;
+  }
+  return m;
+}
+
+// Copies of 16 bytes need every piece of every token on a 16-byte boundary.
+bool needs_8(const kvcs_cache &c) {
+  return !aligned(c.base, 16) || c.half_stride % 16 || c.block_stride % 16 || c.head_bytes % 16;
+}
+
+int check_tables(const kvcs_requests *reqs, int64_t total_positions) {
+  if (!reqs || total_positions < 0 || reqs->num_requests < 0) return KVCS_EINVAL;
+  if (reqs->num_requests == 0) return KVCS_OK;
+  if (!reqs->pos_offsets || !reqs->first_position || !reqs->num_tokens) return KVCS_EINVAL;
+  if (total_positions > 0 && !reqs->block_ids) return KVCS_EINVAL;
+  return KVCS_OK;
+}
+
+// Checks shared by attention and attention mass.
+int check_attention(const kvcs_cache *cache, int32_t block_size, const kvcs_attention *a) {
+  if (!cache || !a) return KVCS_EINVAL;
+  kvcs_cache plain = *cache;
+  plain.column = 0;
+  const int rc = check_caches(&plain, 1, block_size);
+  if (rc != KVCS_OK) return rc;
+  if (cache->layout == KVCS_LAYOUT_STATE) return KVCS_EINVAL;
+  if (a->kv_dtype < KVCS_DTYPE_BF16 || a->kv_dtype > KVCS_DTYPE_FP8_E4M3) return KVCS_EINVAL;
+  if (a->q_dtype != KVCS_DTYPE_BF16 && a->q_dtype != KVCS_DTYPE_FP16) return KVCS_EINVAL;
+  if (a->kv_dtype != KVCS_DTYPE_FP8_E4M3 && a->kv_dtype != a->q_dtype) return KVCS_EINVAL;
+  if (a->q_heads < 1 || a->q_heads % cache->num_heads) return KVCS_EINVAL;
+  if (a->total_new < 0 || a->max_new < 0 || a->max_new > a->total_new || a->window < 0 ||
+      a->observe < 0 || a->q_stride < 0)
+    return KVCS_EINVAL;
+  if (!std::isfinite(a->scale) || !std::isfinite(a->k_scale) || !std::isfinite(a->v_scale) ||
+      !std::isfinite(a->softcap) || a->softcap < 0.0f)
+    return KVCS_EINVAL;
+  if (cache->layout == KVCS_LAYOUT_LATENT) return KVCS_EUNSUPPORTED;
+  const int es = element_bytes(a->kv_dtype);
+  if (cache->head_bytes % (8 * es) || cache->head_bytes / es > 256) return KVCS_EUNSUPPORTED;
+  const int64_t dim = cache->head_bytes / es;
+  if (a->q_stride && (a->q_stride % 8 || a->q_stride < a->q_heads * dim)) return KVCS_EINVAL;
+  if (static_cast<double>(a->total_new) * a->q_heads >= 2147483648.0) return KVCS_EUNSUPPORTED;
+  if (static_cast<double>(block_size) * cache->num_heads * cache->head_bytes >= 2147483648.0)
+    return KVCS_EUNSUPPORTED;
+  return KVCS_OK;
+}
+
+AttnParams attn_params(const kvcs_cache *cache, int32_t block_size, const kvcs_requests *reqs,
+                       int64_t total_positions, const kvcs_attention *a, uint32_t *status) {
+  AttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.tab.pos_offsets = reinterpret_cast<const long long *>(reqs->pos_offsets);
+  p.tab.first_position = reinterpret_cast<const long long *>(reqs->first_position);
+  p.tab.num_tokens = reinterpret_cast<const long long *>(reqs->num_tokens);
+  p.tab.block_ids = reinterpret_cast<const int *>(reqs->block_ids);
+  p.tab.new_offsets = reinterpret_cast<const long long *>(a->new_offsets);
+  p.tab.num_requests = reqs->num_requests;
+  p.tab.total_positions = total_positions;
+  p.tab.total_new = a->total_new;
+  p.tab.max_new = a->max_new > 0 ? a->max_new : a->total_new;
+  p.tab.status = status;
+  p.map = page_map(*cache, block_size);
+  p.head_dim = cache->head_bytes / element_bytes(a->kv_dtype);
+  p.q = a->q;
+  p.q_stride = a->q_stride ? a->q_stride : static_cast<long long>(a->q_heads) * p.head_dim;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.kv_heads = cache->num_heads;
+  p.group = a->q_heads / cache->num_heads;
+  p.q_bf16 = a->q_dtype == KVCS_DTYPE_BF16;
+  p.window = static_cast<int>(a->window < kMaxRequestTokens ? a->window : 0);
+  p.observe = static_cast<int>(std::min<int64_t>(a->observe, kMaxRequestTokens));
+  p.unit8 = needs_8(*cache) ? 1 : 0;
+  p.row_lo = 1;
+  p.row_hi = 0x7fffffff;
+  const float s = a->scale * a->k_scale;
+  p.scale = s * kLog2e;
+  if (a->softcap > 0.0f) {
+    p.cap = a->softcap * kLog2e;
+    p.inv_cap = s / a->softcap;
+  }
+  p.v_scale = a->v_scale;
+  return p;
+}
+
+// The launches of one attention call: requests of up to 16 rows (new tokens
+// times query heads per KV head) go to the narrow kernel, the others to the
+// wide one.  max_new bounds the rows, so a decode step launches only the
+// narrow kernel; when total_new = num_requests * max_new every request has
+// max_new tokens and only one kernel is needed either way.
+struct AttendPlan {
+  bool narrow, wide;
+  int narrow_grid, wide_grid;
+  long long part_floats;
+};
+constexpr int kNarrowRows = 16;
+
+AttendPlan plan_attend(const AttnParams &p, int kv_dtype, int sms) {
+  AttendPlan pl;
+  const long long rows = p.tab.max_new * p.group;
+  pl.wide = rows > kNarrowRows;
+  pl.narrow = !pl.wide || (p.tab.total_new != p.tab.num_requests * p.tab.max_new &&
+                           p.group <= kNarrowRows);
+  long long nf = 0, wf = 0;
+  auto shape = kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::shape
+               : kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::shape
+                                             : &AttendLaunch<kKvFp8>::shape;
+  shape(p.head_dim, false, sms, &pl.narrow_grid, &nf);
+  shape(p.head_dim, true, sms, &pl.wide_grid, &wf);
+  pl.part_floats = std::max(pl.narrow ? nf : 0, pl.wide ? wf : 0);
+  return pl;
+}
+
+// Counters first (two launches' worth), then the partial results.
+int64_t attend_workspace(const AttendPlan &pl) {
+  const int64_t tickets = (static_cast<int64_t>(pl.narrow_grid) + pl.wide_grid) * 4;
+  return (tickets + 255) / 256 * 256 + pl.part_floats * 4;
+}
+
+__global__ void __launch_bounds__(1024) kvcs_tickets_kernel(u32 *tickets, int n) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) tickets[i] = 0;
+}
+
+}  // namespace
+}  // namespace kvcs
+
+using namespace kvcs;
+
+extern "C" {
+
+int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_t num_requests,
+                             const kvcs_attention *att, int32_t num_sms, int64_t *bytes) {
+  if (!bytes || num_requests < 0) return KVCS_EINVAL;
+  const int rc = check_attention(cache, block_size, att);
+  if (rc != KVCS_OK) return rc;
+  int sms = num_sms;
+  if (sms <= 0 && device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
+  kvcs_requests reqs;
+  std::memset(&reqs, 0, sizeof(reqs));
+  reqs.num_requests = num_requests;
+  const AttnParams p = attn_params(cache, block_size, &reqs, 0, att, nullptr);
+  *bytes = attend_workspace(plan_attend(p, att->kv_dtype, sms));
+  return KVCS_OK;
+}
+
+int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs_requests *reqs,
+                         int64_t total_positions, const kvcs_attention *att, uint32_t *status,
+                         void *stream) {
+  int rc = check_attention(cache, block_size, att);
+  if (rc != KVCS_OK) return rc;
+  rc = check_tables(reqs, total_positions);
+  if (rc != KVCS_OK) return rc;
+  if (att->total_new == 0 || reqs->num_requests == 0) return KVCS_OK;
+  if (!att->q || !att->out || !att->new_offsets || !aligned(att->q, 16) ||
+      !aligned(att->out, 16) || !aligned(att->lse, 4) || !att->workspace ||
+      !aligned(att->workspace, 16))
+    return KVCS_EINVAL;
+  int sms = 0;
+  if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
+  AttnParams p = attn_params(cache, block_size, reqs, total_positions, att, status);
+  const AttendPlan pl = plan_attend(p, att->kv_dtype, sms);
+  if (att->workspace_bytes < attend_workspace(pl)) return KVCS_EINVAL;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  u32 *tickets = static_cast<u32 *>(att->workspace);
+  const int n_tickets = pl.narrow_grid + pl.wide_grid;
+  p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(att->workspace) +
+                                     (n_tickets * 4ll + 255) / 256 * 256);
+  {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kvcs_tickets_kernel, tickets, n_tickets) != cudaSuccess)
+      return KVCS_ECUDA;
+  }
+  auto attend = att->kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::attend
+                : att->kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::attend
+                                                   : &AttendLaunch<kKvFp8>::attend;
+  bool after_zero = true;
+  if (pl.narrow) {
+    p.row_lo = 1;
+    p.row_hi = kNarrowRows;
+    p.tickets = tickets;
+    if (attend(p, false, pl.narrow_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;
+    after_zero = false;
+  }
+  if (pl.wide) {
+    p.row_lo = pl.narrow ? kNarrowRows + 1 : 1;
+    p.row_hi = 0x7fffffff;
+    p.tickets = tickets + pl.narrow_grid;
+    if (attend(p, true, pl.wide_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;
+  }
+  if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+  count_launches(1 + (pl.narrow ? 1 : 0) + (pl.wide ? 1 : 0));
+  return KVCS_OK;
+}
+
+int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_requests *reqs,
+                        int64_t total_positions, const kvcs_attention *att, float *mass,
+                        uint32_t *status, void *stream) {
+  int rc = check_attention(cache, block_size, att);
+  if (rc != KVCS_OK) return rc;
+  rc = check_tables(reqs, total_positions);
+  if (rc != KVCS_OK) return rc;
+  if (att->total_new == 0 || reqs->num_requests == 0) return KVCS_OK;
+  if (!att->q || !att->lse || !att->new_offsets || !mass || !aligned(att->q, 16) ||
+      !aligned(att->lse, 4) || !aligned(mass, 4))
+    return KVCS_EINVAL;
+  int sms = 0;
+  if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
+  AttnParams p = attn_params(cache, block_size, reqs, total_positions, att, status);
+  p.mass = mass;
+  auto run = att->kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::mass
+             : att->kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::mass
+                                                : &AttendLaunch<kKvFp8>::mass;
+  if (run(p, 4 * sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVCS_ECUDA;
+  count_launches(1);
+  return KVCS_OK;
+}
+
+int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
+               const kvcs_requests *reqs, int64_t total_positions, const kvcs_eviction *ev,
+               uint32_t *status, void *stream) {
+  if (!caches || num_caches < 1 || !ev) return KVCS_EINVAL;
+  std::vector<kvcs_cache> plain(caches, caches + num_caches);
+  for (kvcs_cache &c : plain) c.column = 0;
+  int rc = check_caches(plain.data(), num_caches, block_size);
+  if (rc != KVCS_OK) return rc;
+  rc = check_tables(reqs, total_positions);
+  if (rc != KVCS_OK) return rc;
+  if (ev->sinks < 0 || ev->recent < 0 || !ev->scores) return KVCS_EINVAL;
+  for (int32_t i = 0; i < num_caches; ++i) {
+    if (caches[i].layout == KVCS_LAYOUT_STATE) return KVCS_EINVAL;
+    if (!ev->scores[i] || !aligned(ev->scores[i], 4)) return KVCS_EINVAL;
+    if (static_cast<double>(block_size) * caches[i].num_heads * caches[i].head_bytes >=
+        2147483648.0)
+      return KVCS_EUNSUPPORTED;
+  }
+  if (!aligned(ev->new_block_ids, 4) || !aligned(ev->block_sums, 8)) return KVCS_EINVAL;
+  if (reqs->num_requests == 0 || total_positions == 0) return KVCS_OK;
+  if (!ev->keep || !aligned(ev->keep, 8)) return KVCS_EINVAL;
+  int sms = 0;
+  if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.tab.pos_offsets = reinterpret_cast<const long long *>(reqs->pos_offsets);
+  p.tab.first_position = reinterpret_cast<const long long *>(reqs->first_position);
+  p.tab.num_tokens = reinterpret_cast<const long long *>(reqs->num_tokens);
+  p.tab.block_ids = reinterpret_cast<const int *>(reqs->block_ids);
+  p.tab.num_requests = reqs->num_requests;
+  p.tab.total_positions = total_positions;
+  p.tab.status = status;
+  p.keep = reinterpret_cast<const long long *>(ev->keep);
+  p.new_block_ids = reinterpret_cast<const int *>(ev->new_block_ids);
+  p.block_sums = reinterpret_cast<u64 *>(ev->block_sums);
+  p.block_size = block_size;
+  p.sinks = static_cast<int>(std::min<int64_t>(ev->sinks, kMaxRequestTokens));
+  p.recent = static_cast<int>(std::min<int64_t>(ev->recent, kMaxRequestTokens));
+  p.num_blocks = caches[0].num_blocks;
+  for (int32_t i = 1; i < num_caches; ++i)
+    p.num_blocks = std::min<long long>(p.num_blocks, caches[i].num_blocks);
+  int launches = 0;
+  if (p.block_sums) {
+    const unsigned grid =
+        static_cast<unsigned>(std::min<int64_t>(reqs->num_requests, 4ll * sms));
+    kvcs_evict_zero_kernel<<<grid, 256, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+    ++launches;
+  }
+  for (int32_t lo = 0; lo < num_caches;) {
+    // as many caches as a launch holds and its grid can number
+    int n = 0;
+    long long rows = 0;
+    while (lo + n < num_caches && n < kMaxCachesPerLaunch) {
+      const kvcs_cache &c = caches[lo + n];
+      if ((rows + c.num_heads) * static_cast<double>(reqs->num_requests) >= 2147483648.0) break;
+      EvictCache &e = p.c[n];
+      e.map = page_map(c, block_size);
+      e.scores = ev->scores[lo + n];
+      e.m0 = 2ull * (static_cast<u64>(c.layer) * KVCS_MAX_KV_HEADS_PER_LAYER + c.head_offset) + 1;
+      e.heads = c.num_heads;
+      e.head_bytes = c.head_bytes;
+      e.first_row = static_cast<int>(rows);
+      e.unit8 = needs_8(c) ? 1 : 0;
+      rows += c.num_heads;
+      ++n;
+    }
+    if (n == 0) return KVCS_EUNSUPPORTED;
+    p.num_caches = n;
+    p.rows = static_cast<int>(rows);
+    kvcs_evict_kernel<<<static_cast<unsigned>(rows * reqs->num_requests), kEvictThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+    ++launches;
+    lo += n;
+  }
+  count_launches(launches);
+  return KVCS_OK;
+}
+
+}  // extern "C"

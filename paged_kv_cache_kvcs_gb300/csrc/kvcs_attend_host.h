@@ -1,0 +1,28 @@
+// kvcs_attend_host.h -- host-side seams between the library's translation
+// units: shared argument checks, device setup, the launch counter, and the
+// launchers of each cache type's attention kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "kvcs.h"
+#include "kvcs_attn_common.cuh"
+
+namespace kvcs {
+
+// kvcs.cu
+int check_caches(const kvcs_cache *caches, int32_t num_caches, int32_t block_size);
+cudaError_t device_sms(int *sms);
+void count_launches(int n);
+
+// kvcs_attend_type.cu, once per cache type
+template <int kType>
+struct AttendLaunch {
+  // floats of workspace a launch's partial results take, and its grid
+  static void shape(int dim, bool wide, int sms, int *grid, long long *part_floats);
+  static cudaError_t attend(const AttnParams &p, bool wide, int grid, bool after_zero,
+                            cudaStream_t st);
+  static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st);
+};
+
+}  // namespace kvcs

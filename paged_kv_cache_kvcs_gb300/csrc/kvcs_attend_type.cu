@@ -1,0 +1,87 @@
+// kvcs_attend_type.cu -- the attention and attention-mass kernels of one
+// cache type (KVCS_KV_TYPE), compiled once per type.
+
+#include "kvcs_attend.cuh"
+#include "kvcs_attend_host.h"
+#include "kvcs_mass.cuh"
+
+namespace kvcs {
+
+constexpr int kThisType = KVCS_KV_TYPE;
+
+// Everything is a template over the type: the three objects share one
+// namespace.
+template <int kType>
+struct TypeLaunch {
+  // Heads narrower than the compiled width are filled up with zeros.
+  static int width_of(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+  // CTAs per SM by shared memory (228 KB an SM, 1 KB of it reserved per CTA).
+  template <int kDim>
+  static constexpr int ctas_per_sm() {
+    return 228 * 1024 / (AttendShape<kType, kDim>::kSmemBytes + 2048) >= 2 ? 2 : 1;
+  }
+
+  template <int kDim, bool kWide>
+  static cudaError_t attend(const AttnParams &p, int grid, bool after_zero, cudaStream_t st) {
+    constexpr int smem = AttendShape<kType, kDim>::kSmemBytes;
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void *>(kvcs_attend_kernel<kType, kDim, kWide>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kAttendThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_zero ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kvcs_attend_kernel<kType, kDim, kWide>, p);
+  }
+
+  template <int kDim>
+  static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st) {
+    kvcs_mass_kernel<kType, kDim><<<static_cast<unsigned>(grid), kMassThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+};
+
+using This = TypeLaunch<kThisType>;
+
+template <>
+void AttendLaunch<kThisType>::shape(int dim, bool wide, int sms, int *grid, long long *part_floats) {
+  const int w = This::width_of(dim);
+  const int per = w == 64 ? This::ctas_per_sm<64>() : w == 128 ? This::ctas_per_sm<128>() : This::ctas_per_sm<256>();
+  *grid = per * sms;
+  *part_floats = static_cast<long long>(*grid) * 2 * attend_rows(wide) * (w + 2);
+}
+
+template <>
+cudaError_t AttendLaunch<kThisType>::attend(const AttnParams &p, bool wide, int grid, bool after_zero,
+                                        cudaStream_t st) {
+  switch (This::width_of(p.head_dim)) {
+    case 64:
+      return wide ? This::attend<64, true>(p, grid, after_zero, st)
+                  : This::attend<64, false>(p, grid, after_zero, st);
+    case 128:
+      return wide ? This::attend<128, true>(p, grid, after_zero, st)
+                  : This::attend<128, false>(p, grid, after_zero, st);
+    default:
+      return wide ? This::attend<256, true>(p, grid, after_zero, st)
+                  : This::attend<256, false>(p, grid, after_zero, st);
+  }
+}
+
+template <>
+cudaError_t AttendLaunch<kThisType>::mass(const AttnParams &p, int grid, cudaStream_t st) {
+  switch (This::width_of(p.head_dim)) {
+    case 64: return This::mass<64>(p, grid, st);
+    case 128: return This::mass<128>(p, grid, st);
+    default: return This::mass<256>(p, grid, st);
+  }
+}
+
+}  // namespace kvcs

@@ -218,7 +218,7 @@ struct PosInfo {
 
 // Request r with pos_offsets[r] <= pos < pos_offsets[r+1], or -1.  Reads
 // only pos_offsets[0 .. R], whatever the array holds.
-__device__ long long find_request(const Params &p, long long pos) {
+__device__ inline long long find_request(const Params &p, long long pos) {
   long long lo = 0, hi = p.num_requests;
   while (lo < hi) {
     long long mid = (lo + hi) >> 1;
@@ -306,7 +306,7 @@ __device__ __forceinline__ void req_seek(const Params &p, ReqCursor &c, long lon
 
 // Block position, block and valid slots of global position `pos` (request
 // cursor `c` on it, block id `b`); bad tables set status bits when `report`.
-__device__ PosInfo position_info_quiet(const Params &p, long long pos, const ReqCursor &c,
+__device__ inline PosInfo position_info_quiet(const Params &p, long long pos, const ReqCursor &c,
                                        long long b, bool report) {
   PosInfo pi;
   pi.whole = false;

@@ -1,0 +1,215 @@
+// kvcs_mass.cuh -- attention mass of cached tokens: for every cached token j
+// of every KV head, the weights it gets from the observed queries,
+//     mass_j += sum_i 2^(z_ij - lse_i / ln 2),
+// with z and the visible (i, j) as in the attention, and lse from it.
+//
+// Bound: one product per (query row, token) and a read of K, so a decode
+// step is bound by the read of K.  A warp owns 16 tokens of one head and
+// keeps their K fragments in registers while the query rows pass, so every
+// token's sum is made by one warp in row order and added to memory once: the
+// result does not depend on timing (unless requests share the block).
+#pragma once
+
+#include "kvcs_attend.cuh"
+
+namespace kvcs {
+
+constexpr int kMassThreads = 128;
+
+// A request's chunks of 16 tokens that some observed query may see.
+struct MassSpan {
+  int lo;            // first chunk
+  int chunks;
+  int first;         // first observed new token
+  long long total;
+};
+
+__device__ __forceinline__ MassSpan mass_span(const AttnParams &p, const Request &q) {
+  MassSpan s;
+  s.lo = s.chunks = 0;
+  s.first = p.observe > 0 ? max(0, q.n - p.observe) : 0;
+  s.total = 0;
+  const long long r = static_cast<long long>(q.n - s.first) * p.group;
+  if (r < p.row_lo || r > p.row_hi) return s;
+  const int first = p.window > 0 ? max(0, q.at + s.first - p.window + 1) : 0;
+  const int end = min(q.keys, max(0, q.at + q.n));
+  s.lo = first / kChunkKeys;
+  s.chunks = max(0, (end + kChunkKeys - 1) / kChunkKeys - s.lo);
+  s.total = static_cast<long long>(s.chunks) * p.kv_heads;
+  return s;
+}
+
+template <int kType, int kDim>
+__global__ void __launch_bounds__(kMassThreads)
+    kvcs_mass_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kElem = kType == kKvFp8 ? 1 : 2;
+  constexpr bool kBf16 = kType == kKvBf16;
+  constexpr int kWords = kDim * kElem / 64;   // 16-byte pieces of a key per lane
+  __shared__ long long s_scan[4];
+  __shared__ long long s_req[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int pg = (g >> 1) | ((g & 1) << 2);
+  const long long R = p.tab.num_requests;
+  long long sum = 0;
+  for (long long r = tid; r < R; r += kMassThreads)
+    sum += mass_span(p, read_request(p.tab, r, p.map.block_size, blockIdx.x == 0)).total;
+  long long total;
+  block_scan(sum, &total, s_scan);
+  const long long a_cta = total * blockIdx.x / gridDim.x, b_cta = total * (blockIdx.x + 1ll) / gridDim.x;
+  if (a_cta >= b_cta) return;
+  long long before = 0, r = 0;
+  for (long long c = 0;; c += kMassThreads) {
+    const long long rr = c + tid;
+    const long long v =
+        rr < R ? mass_span(p, read_request(p.tab, rr, p.map.block_size, false)).total : 0;
+    long long all;
+    const long long ex = before + block_scan(v, &all, s_scan);
+    if (before + all > a_cta) {
+      if (v > 0 && ex <= a_cta && a_cta < ex + v) {
+        s_req[0] = rr;
+        s_req[1] = ex;
+      }
+      __syncthreads();
+      r = s_req[0];
+      before = s_req[1];
+      break;
+    }
+    before += all;
+  }
+  Request q = read_request(p.tab, r, p.map.block_size, false);
+  MassSpan sp = mass_span(p, q);
+  // the CTA's run goes round its warps
+  for (long long x = a_cta + warp; x < b_cta; x += kMassThreads / 32) {
+    while (x >= before + sp.total) {
+      before += sp.total;
+      ++r;
+      q = read_request(p.tab, r, p.map.block_size, false);
+      sp = mass_span(p, q);
+    }
+    const long long w = x - before;
+    const int head = static_cast<int>(w / sp.chunks);
+    const int key0 = (sp.lo + static_cast<int>(w % sp.chunks)) * kChunkKeys;
+    // this lane's two keys, j * 8 + pg
+    uint4 k[2][kWords];
+    u32 valid = 0;
+    {
+      const int key = key0 + (lane & 15);
+      bool ok = key < q.keys;
+      long long off = 0;
+      if (ok) {
+        const int pos = key / p.map.block_size;
+        const int block = p.tab.block_ids[q.pos0 + pos];
+        if (block < 0 || block >= p.map.num_blocks) {
+          ok = false;
+          raise(p.tab, kStatusBadBlockId);
+        } else {
+          off = token_offset(p.map, block, key - pos * p.map.block_size, head);
+        }
+      }
+      valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const int row_bytes = p.head_dim * kElem;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const long long o = __shfl_sync(0xffffffffu, off, j * 8 + pg);
+        const bool live = valid >> (j * 8 + pg) & 1u;
+        const unsigned char *src = p.map.base + o;
+#pragma unroll
+        for (int b = 0; b < kWords; ++b) {
+          const int c = 4 * b + t;
+          const unsigned char *at = src + static_cast<long long>(c) * p.map.chunk_stride;
+          k[j][b] = make_uint4(0, 0, 0, 0);
+          if (live && c * 16 < row_bytes) {
+            if (!p.unit8) {
+              k[j][b] = __ldg(reinterpret_cast<const uint4 *>(at));
+            } else {
+              const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(at));
+              k[j][b].x = lo.x;
+              k[j][b].y = lo.y;
+              if (c * 16 + 8 < row_bytes) {
+                const uint2 hi = __ldg(reinterpret_cast<const uint2 *>(at + 8));
+                k[j][b].z = hi.x;
+                k[j][b].w = hi.y;
+              }
+            }
+          }
+        }
+      }
+    }
+    float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};   // tokens j * 8 + t + 4 i
+    // observed tokens that see some key of the chunk
+    const int i0 = max(sp.first, key0 - q.at);
+    int i1 = q.n;
+    if (p.window > 0)
+      i1 = static_cast<int>(min(static_cast<long long>(i1),
+                                static_cast<long long>(key0) + kChunkKeys - 1 + p.window - q.at));
+    const int rows_end = i1 * p.group;
+#pragma unroll 1
+    for (int row0 = i0 * p.group; row0 < rows_end; row0 += 16) {
+      int row[2], at[2];
+      bool has[2];
+      float lse[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = row0 + g + 8 * i;
+        has[i] = rr < rows_end;
+        row[i] = has[i] ? rr : row0;
+        at[i] = has[i] ? q.at + row[i] / p.group : -1;   // spare rows see nothing
+        const long long tok = q.q0 + row[i] / p.group;
+        lse[i] = kLog2e * __ldg(p.lse + tok * (p.group * p.kv_heads) + head * p.group +
+                                row[i] % p.group);
+      }
+      u32 qf[kDim / 8][2];
+      float rs[2];
+      load_queries<kType, kDim>(p, q, head, row, has, qf, rs);
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int b = 0; b < kWords; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (kType == kKvFp8) {
+            const u32 kw[4] = {k[j][b].x, k[j][b].y, k[j][b].z, k[j][b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              u32 lo, hi;
+              fp8x4_to_half(kw[i], lo, hi);
+              const int step = 4 * b + i;
+              mma16816<false>(s[j], qf[2 * step][0], qf[2 * step][1], qf[2 * step + 1][0],
+                              qf[2 * step + 1][1], lo, hi);
+            }
+          } else {
+            mma16816<kBf16>(s[j], qf[4 * b][0], qf[4 * b][1], qf[4 * b + 1][0], qf[4 * b + 1][1],
+                            k[j][b].x, k[j][b].y);
+            mma16816<kBf16>(s[j], qf[4 * b + 2][0], qf[4 * b + 2][1], qf[4 * b + 3][0],
+                            qf[4 * b + 3][1], k[j][b].z, k[j][b].w);
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + j * 8 + t + 4 * (i & 1);
+          const int a = at[i >> 1];
+          if (key <= a && (p.window == 0 || key > a - p.window))
+            acc[j][i & 1] += ex2(score_of(p, s[j][i], rs[i >> 1]) - lse[i >> 1]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = acc[j][i];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        const int kk = j * 8 + t + 4 * i;
+        if (g == 0 && (valid >> kk & 1u)) {
+          const int key = key0 + kk, pos = key / p.map.block_size;
+          const long long block = p.tab.block_ids[q.pos0 + pos];
+          atomicAdd(p.mass + (block * p.kv_heads + head) * p.map.block_size +
+                        (key - pos * p.map.block_size), v);
+        }
+      }
+  }
+}
+
+}  // namespace kvcs

@@ -1,0 +1,356 @@
+"""kvcs_paged_attention and kvcs_attention_mass against the 64-bit forms in
+attention_ref, whose error bounds are derived there."""
+
+import math
+
+import pytest
+import torch
+
+import attention_ref as A
+import paged_kv_cache_kvcs_gb300 as K
+from paged_kv_cache_kvcs_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+NHD, HND, XS = W.LAYOUT_NHD, W.LAYOUT_HND, W.LAYOUT_XSPLIT
+
+
+def run(case, **kw):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = K.paged_attention(case.cache, case.bs, *case.table, case.q, case.new_offsets,
+                                 kv_dtype=case.kv, status=status, **kw)
+    torch.cuda.synchronize()
+    return out, lse, int(status.item())
+
+
+def check(case, max_new="known", blocked=None, want_status=0, **kw):
+    m = {"max_new": max(case.new)} if max_new == "known" else {}
+    out, lse, status = run(case, **kw, **m)
+    ref = A.attention(case, blocked=blocked, **kw)
+    assert status == want_status
+    A.close(out, ref[0], ref[2])
+    A.close(lse, ref[1], ref[3])
+    return out, lse
+
+
+GEOMETRIES = [
+    dict(dim=128, heads=2, group=4, bs=16),
+    dict(dim=64, heads=3, group=1, bs=16),
+    dict(dim=128, heads=1, group=8, bs=64),
+    dict(dim=80, heads=2, group=5, bs=48),
+    dict(dim=256, heads=1, group=2, bs=32),
+    dict(dim=8, heads=2, group=3, bs=7),
+    dict(dim=96, heads=1, group=16, bs=1),
+    dict(dim=128, heads=1, group=24, bs=16),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("geo", GEOMETRIES, ids=lambda g: "-".join(map(str, g.values())))
+def test_decode(kv, geo):
+    """One new token a request, lengths around tile and block borders."""
+    check(A.Case(kv=kv, lengths=[1, 2, 15, 16, 17, 63, 64, 65, 127, 400, 1025],
+                 new=[1] * 11, seed=3, **geo), k_scale=0.5, v_scale=2.0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("geo", GEOMETRIES, ids=lambda g: "-".join(map(str, g.values())))
+def test_chunks(kv, geo):
+    """Chunks of new tokens, with and without earlier tokens; none at all."""
+    check(A.Case(kv=kv, lengths=[5, 33, 200, 77, 300, 130], new=[5, 33, 17, 0, 129, 70], seed=4,
+                 **geo))
+
+
+@pytest.mark.parametrize("layout,kw", [
+    (HND, {}), (HND, dict(kbs=4)), (XS, {}), (NHD, dict(interleaved=True)),
+    (NHD, dict(pad=16)), (NHD, dict(pad=8)), (HND, dict(offset=8)), (XS, dict(offset=8)),
+    (HND, dict(interleaved=True, pad=48))], ids=str)
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_layouts(layout, kw, kv, dim):
+    check(A.Case(kv=kv, layout=layout, dim=dim, lengths=[70, 1, 259, 90], new=[1, 1, 80, 40],
+                 seed=5, **kw))
+
+
+@pytest.mark.parametrize("window", [0, 1, 16, 100])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("new", [[1, 1, 1], [150, 3, 61]])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_window_and_softcap(window, softcap, new, dim):
+    check(A.Case(lengths=[600, 90, 61], new=new, seed=6, dim=dim, scale=2.0),
+          window=window, softcap=softcap, scale=0.3)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [40, 1, 170, 64]])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_empty_rows(new, dim):
+    """Requests with no cached tokens, fewer cached than new ones, or whose
+    listed blocks start past what a row may see."""
+    check(A.Case(lengths=[0, 0, 30, 100], new=new, first=[0, 3, 0, 2], seed=7, dim=dim), window=33)
+
+
+def test_first_position_and_extra_positions():
+    case = A.Case(lengths=[200, 64, 130], new=[3, 1, 66], first=[5, 1, 0], extra=2, seed=8, dim=128)
+    check(case)
+    check(case, max_new="unknown")
+
+
+@pytest.mark.parametrize("new", [1, 4, 100])
+def test_long_and_split(new):
+    """One request over the whole GPU: groups split between CTAs and joined."""
+    check(A.Case(heads=1, group=4, dim=128, lengths=[30011], new=[new], bs=32, seed=9))
+
+
+@pytest.mark.parametrize("new,group", [([1] * 40, 4), ([1, 300, 2, 0, 5, 90, 1, 1], 4),
+                                       ([16, 17, 4, 5], 2), ([8, 8, 8], 8)])
+def test_mixed_batches(new, group):
+    """max_new known or not, and batches on both sides of the row limits."""
+    g = torch.Generator().manual_seed(10)
+    lengths = [n + int(torch.randint(0, 700, (1,), generator=g)) for n in new]
+    case = A.Case(dim=64, group=group, lengths=lengths, new=new, seed=10)
+    a = check(case)
+    b = check(case, max_new="unknown")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("dim,new", [(64, [1, 1]), (128, [1, 1]), (128, [70, 200]), (64, [5, 12])])
+def test_nonfinite_values_in_masked_places(kv, dim, new):
+    """Values that a row does not see never reach it: later tokens' NaN and
+    infinite K and V, and those before the window."""
+    case = A.Case(kv=kv, dim=dim, lengths=[150, 300], new=new, seed=11)
+    bad = [float("nan")] if kv == "fp8" else [float("nan"), float("inf"), -float("inf")]
+    for i, b in enumerate(bad):
+        for r in (0, 1):
+            T = case.lengths[r]
+            case.put(r, 1, 3 + i, torch.full((1, dim), b))          # before every window
+            case.put(r, 0, 7 + i, torch.full((1, dim), b))
+    # the last token's V: only the last row sees it
+    if new[0] > 1:
+        case.put(0, 1, 149, torch.full((1, dim), float("nan")))
+        case.put(1, 1, 290, torch.full((1, dim), float("nan")))
+    out, lse, _ = run(case, window=20, max_new=max(new))
+    ref = A.attention(case, window=20)
+    keep = torch.isfinite(ref[0]).all(-1).all(-1)
+    seen_k = torch.ones(len(keep), dtype=torch.bool)
+    for r in (0, 1):      # rows that see a bad K are NaN: leave them out here
+        see = A.visible(case, r, 20)
+        lo = case.starts[r]
+        seen_k[lo:lo + new[r]] = ~see[:, 7:7 + len(bad)].any(1)
+    assert (keep & seen_k).sum() > 0
+    sel = keep & seen_k
+    A.close(out[sel.cuda()], ref[0][sel], ref[2][sel])
+    A.close(lse[sel.cuda()], ref[1][sel], ref[3][sel])
+    # and the rows that see a NaN value have it
+    assert torch.isnan(out.cpu()[~keep & seen_k]).any(-1).all()
+
+
+def test_scores_of_equal_and_extreme_size():
+    """Scores far apart (one token takes all weight) and all equal."""
+    case = A.Case(dim=128, lengths=[200, 200], new=[1, 90], seed=12, scale=30.0)
+    check(case, scale=1.0)
+    check(case, scale=0.0)
+    check(case, scale=-1.0)
+
+
+def test_strided_queries_and_given_outputs():
+    case = A.Case(dim=64, lengths=[50, 400], new=[3, 100], seed=13)
+    n, hq, d = case.q.shape
+    fused = torch.randn((n, hq * d + 2 * 2 * d), device="cuda").to(case.q.dtype)
+    fused[:, :hq * d] = case.q.reshape(n, -1)
+    q = fused[:, :hq * d].view(n, hq, d)
+    assert q.stride(0) != hq * d
+    out = torch.empty_like(case.q)
+    lse = torch.empty((n, hq), device="cuda")
+    ws = torch.full((K.attention_workspace_bytes(case.cache, case.bs, 2, q, max_new=100),), 255,
+                    dtype=torch.uint8, device="cuda")
+    got = K.paged_attention(case.cache, case.bs, *case.table, q, case.new_offsets, out=out, lse=lse,
+                            workspace=ws, max_new=100)
+    assert got[0] is out and got[1] is lse
+    ref = A.attention(case)
+    A.close(out, ref[0], ref[2])
+    A.close(lse, ref[1], ref[3])
+
+
+def test_rows_no_request_owns_are_left():
+    case = A.Case(dim=128, lengths=[50, 90], new=[2, 70], seed=14)
+    n = case.q.shape[0]
+    q = torch.cat([case.q[:1], case.q, case.q[:2]])
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    K.paged_attention(case.cache, case.bs, *case.table, q, case.new_offsets + 1, out=out, lse=lse,
+                      max_new=70)
+    ref = A.attention(case)
+    A.close(out[1:1 + n], ref[0], ref[2])
+    for x in (out, lse):
+        assert (x[:1] == 7).all() and (x[1 + n:] == 7).all()
+
+
+@pytest.mark.parametrize("new", [[1, 1], [33, 100]])
+def test_bad_block_ids_are_left_out(new):
+    case = A.Case(dim=128, lengths=[100, 300], new=new, seed=15)
+    case.table[3][case.offsets[0] + 2] = -1
+    case.table[3][case.offsets[1] + 5] = case.nb
+    case.table[3][case.offsets[1] + 6] = 2 ** 31 - 1
+    check(case, blocked={0: (2,), 1: (5, 6)}, want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
+
+
+def test_bad_tables_are_flagged():
+    """Rows of requests with inconsistent tables see nothing; a request of
+    more than max_new new tokens is left as it was."""
+    base = dict(dim=64, lengths=[100, 60, 80], new=[1, 1, 1], seed=16)
+
+    def outcome(change, **kw):
+        case = A.Case(**base)
+        change(case)
+        out = torch.full(case.q.shape, 7.0, dtype=case.q.dtype, device="cuda")
+        _, lse, status = run(case, out=out, **kw)
+        ref = A.attention(A.Case(**base))
+        return case, out, lse, status, ref
+
+    def negative_first(c):
+        c.table[1][1] = -4
+
+    def decreasing(c):
+        c.table[0][1] = c.total + 9
+
+    for change, hit in ((negative_first, [1]), (decreasing, [0, 1])):
+        case, out, lse, status, ref = outcome(change, max_new=1)
+        assert status == K.KVCS_STATUS_BAD_REQUESTS
+        for r in range(3):
+            if r in hit:
+                assert (out[r] == 0).all() and torch.isneginf(lse[r]).all()
+            else:
+                A.close(out[r:r + 1], ref[0][r:r + 1], ref[2][r:r + 1])
+
+    def too_many(c):
+        c.new_offsets.copy_(torch.tensor([0, 0, 2, 3]))
+    case, out, lse, status, ref = outcome(too_many, max_new=1)
+    assert status == K.KVCS_STATUS_BAD_REQUESTS and (out[:2] == 7).all()
+    A.close(out[2:], ref[0][2:], ref[2][2:])
+
+
+def test_shared_prefix_blocks():
+    """Two requests listing the same blocks read the same tokens."""
+    case = A.Case(dim=128, lengths=[96, 96], new=[2, 40], seed=17)
+    lo, hi = case.offsets[1], case.offsets[2]
+    case.table[3][lo:hi] = case.table[3][:hi - lo].clone()
+    case.values[1] = case.values[0]
+    check(case)
+
+
+@pytest.mark.parametrize("new", [[1] * 9, [200, 90, 1]])
+def test_graph_replay_streams_and_determinism(new):
+    """Captured and replayed over refilled inputs, on another stream, and
+    twice: the same bits."""
+    lengths = [1000 + 137 * i for i in range(len(new))]
+    case = A.Case(dim=128, lengths=lengths, new=new, seed=18)
+    m = max(new)
+    first = run(case, max_new=m)
+    assert torch.equal(first[0], run(case, max_new=m)[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = K.paged_attention(case.cache, case.bs, *case.table, case.q, case.new_offsets,
+                                 max_new=m, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    g = torch.cuda.CUDAGraph()
+    q = case.q.clone()
+    with torch.cuda.graph(g):
+        out, lse = K.paged_attention(case.cache, case.bs, *case.table, q, case.new_offsets,
+                                     max_new=m, total_positions=case.total)
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2):
+        out2, _ = K.paged_attention(case.cache, case.bs, *case.table, q, case.new_offsets,
+                                    max_new=m, total_positions=case.total)
+    for s in (1.0, 0.5, 1.0):
+        q.copy_(case.q * s)
+        g.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, out2)
+        if s == 1.0:
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+# ---------------------------------------------------------------------------
+# attention mass
+# ---------------------------------------------------------------------------
+
+def check_mass(case, blocked=None, want_status=0, observe=0, max_new=True, **kw):
+    lse = A.attention(case, blocked=blocked, **kw)[1].float().cuda()
+    before = torch.rand((case.nb, case.heads, case.bs), device="cuda")
+    got = before.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m = {"max_new": max(case.new)} if max_new else {}
+    K.attention_mass(case.cache, case.bs, *case.table, case.q, case.new_offsets, lse, got,
+                     observe=observe, kv_dtype=case.kv, status=status, **kw, **m)
+    torch.cuda.synchronize()
+    want, tol = A.mass(case, lse, before, observe=observe, blocked=blocked, **kw)
+    assert int(status.item()) == want_status
+    A.close(got, want, tol)
+    return got
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("geo", GEOMETRIES, ids=lambda g: "-".join(map(str, g.values())))
+@pytest.mark.parametrize("new", [[1, 1, 1, 1, 1, 1], [5, 33, 17, 0, 129, 70]], ids=["one", "many"])
+def test_mass(kv, geo, new):
+    check_mass(A.Case(kv=kv, lengths=[5, 33, 200, 77, 300, 130], new=new, seed=20, **geo),
+               k_scale=0.5)
+
+
+@pytest.mark.parametrize("layout,kw", [
+    (HND, {}), (HND, dict(kbs=4)), (XS, {}), (NHD, dict(interleaved=True)),
+    (NHD, dict(pad=8)), (HND, dict(offset=8)), (XS, dict(offset=8))], ids=str)
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [1, 1, 80, 40]], ids=["one", "many"])
+def test_mass_layouts(layout, kw, kv, new):
+    check_mass(A.Case(kv=kv, layout=layout, dim=128, lengths=[70, 1, 259, 90], new=new, seed=21,
+                      **kw))
+
+
+@pytest.mark.parametrize("observe", [0, 1, 16, 500])
+@pytest.mark.parametrize("window,softcap", [(0, 0.0), (33, 0.0), (33, 15.0)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [150, 3, 61]], ids=["one", "many"])
+def test_mass_observed_window_softcap(observe, window, softcap, new):
+    check_mass(A.Case(lengths=[600, 90, 61], new=new, seed=22, dim=128), observe=observe,
+               window=window, softcap=softcap)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [40, 1, 170, 64]], ids=["one", "many"])
+def test_mass_empty_rows_and_first_positions(new):
+    check_mass(A.Case(lengths=[0, 0, 30, 100], new=new, first=[0, 3, 0, 2], seed=23, dim=64),
+               window=33, max_new=False)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [33, 100]])
+def test_mass_bad_block_ids(new):
+    case = A.Case(dim=128, lengths=[100, 300], new=new, seed=24)
+    case.table[3][case.offsets[0] + 2] = -1
+    case.table[3][case.offsets[1] + 5] = case.nb
+    case.ids[case.offsets[0] + 2] = 0
+    check_mass(case, blocked={0: (2,), 1: (5,)}, want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
+
+
+def test_mass_sums_to_the_observed_weight():
+    """Every row's weights sum to 1, so a head's mass grows by rows seen."""
+    case = A.Case(dim=128, lengths=[500, 90], new=[100, 1], seed=25)
+    _, lse, _ = run(case, max_new=100)
+    mass = torch.zeros((case.nb, case.heads, case.bs), device="cuda")
+    K.attention_mass(case.cache, case.bs, *case.table, case.q, case.new_offsets, lse, mass,
+                     max_new=100)
+    total = mass.double().sum((0, 2)).cpu()
+    assert torch.allclose(total, torch.full((case.heads,), 101.0 * case.group, dtype=torch.float64),
+                          rtol=1e-4)
+
+
+@pytest.mark.parametrize("new", [[1] * 9, [200, 90, 1]])
+def test_mass_repeats_bit_for_bit(new):
+    case = A.Case(dim=128, lengths=[1000 + 137 * i for i in range(len(new))], new=new, seed=26)
+    _, lse, _ = run(case, max_new=max(new))
+    got = []
+    for _ in range(2):
+        mass = torch.zeros((case.nb, case.heads, case.bs), device="cuda")
+        K.attention_mass(case.cache, case.bs, *case.table, case.q, case.new_offsets, lse, mass,
+                         max_new=max(new))
+        got.append(mass)
+    assert torch.equal(*got)
