@@ -471,11 +471,11 @@ typedef struct kvcs_attention {
 
 /*
  * kvcs_attention_workspace -- bytes of workspace kvcs_paged_attention needs
- * for a call of num_requests requests with these sizes (*att's pointers are
+ * for a call of num_requests requests and total_positions with these sizes (*att's pointers are
  * not looked at).  num_sms as in kvcs_plan.  Returns its error codes.
  */
 int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_t num_requests,
-                             const kvcs_attention *att, int32_t num_sms, int64_t *bytes);
+                             int64_t total_positions, const kvcs_attention *att, int32_t num_sms, int64_t *bytes);
 
 /*
  * kvcs_paged_attention -- attention of a batch's new tokens over one layer's

@@ -87,17 +87,19 @@ def _scores(a, dim, scale, softcap, window, k_scale, v_scale, max_new) -> None:
     a.max_new = min(max_new, a.total_new) if max_new is not None else 0
 
 
-def attention_workspace_bytes(cache, block_size: int, num_requests: int, q, *, max_new=None,
-                              kv_dtype=None) -> int:
+def attention_workspace_bytes(cache, block_size: int, num_requests: int, total_positions: int, q,
+                              *, max_new=None, kv_dtype=None) -> int:
     """Bytes of workspace ``paged_attention`` needs for ``num_requests``
-    requests and queries like ``q`` (``kvcs_attention_workspace``)."""
+    requests of ``total_positions`` blocks and queries like ``q``
+    (``kvcs_attention_workspace``)."""
     dev = B._current_device()
     offsets = torch.empty(num_requests + 1, dtype=torch.int64, device=dev)
     a = _queries(cache, q, offsets, num_requests, kv_dtype, dev)
     _scores(a, q.shape[2], None, 0.0, 0, 1.0, 1.0, max_new)
     n = ctypes.c_int64()
     _raise(B.load_library().kvcs_attention_workspace(
-        B.cache_array([cache]), block_size, num_requests, ctypes.byref(a), 0, ctypes.byref(n)),
+        B.cache_array([cache]), block_size, num_requests, total_positions, ctypes.byref(a), 0,
+        ctypes.byref(n)),
         "kvcs_attention_workspace")
     return n.value
 
@@ -144,7 +146,7 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     arr = B.cache_array([cache])
     n = ctypes.c_int64()
     a_ref = ctypes.byref(a)
-    _raise(lib.kvcs_attention_workspace(arr, block_size, R, a_ref, 0, ctypes.byref(n)),
+    _raise(lib.kvcs_attention_workspace(arr, block_size, R, total_positions, a_ref, 0, ctypes.byref(n)),
            "kvcs_attention_workspace")
     handle = _stream_handle(stream, dev)
     if workspace is None:

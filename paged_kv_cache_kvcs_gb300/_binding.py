@@ -118,7 +118,7 @@ SIGNATURES = {
         ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p,
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "kvcs_attention_workspace": (ctypes.c_int, [
-        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int64,
+        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
         ctypes.POINTER(kvcs_attention), ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
     "kvcs_paged_attention": (ctypes.c_int, [
         ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.POINTER(kvcs_requests),

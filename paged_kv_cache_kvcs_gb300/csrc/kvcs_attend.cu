@@ -18,6 +18,8 @@
 namespace kvcs {
 namespace {
 
+constexpr u64 kAttendTimeoutNs = 2000000000ull;  // 2 s per wait
+
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 int element_bytes(int kv_dtype) { return kv_dtype == KVCS_DTYPE_FP8_E4M3 ? 1 : 2; }
@@ -135,38 +137,125 @@ AttnParams attn_params(const kvcs_cache *cache, int32_t block_size, const kvcs_r
   return p;
 }
 
-// The launches of one attention call: requests of up to 16 rows (new tokens
-// times query heads per KV head) go to the narrow kernel, the others to the
-// wide one.  max_new bounds the rows, so a decode step launches only the
-// narrow kernel; when total_new = num_requests * max_new every request has
-// max_new tokens and only one kernel is needed either way.
+// Slots a TMA box takes: runs of consecutive slots that lie in one page and
+// one tile.  Below 8 the boxes would not start on the swizzle's 1 KiB period.
+int tc_box(const kvcs_cache &c, int block_size) {
+  const int run = c.layout == KVCS_LAYOUT_HND && c.kernel_block_size > 0 ? c.kernel_block_size
+                                                                        : block_size;
+  int box = kTcKeys;
+  while (run % box) box /= 2;
+  return box;
+}
+
+// Whether the tensor-memory kernel takes the cache: 16-bit heads of 64 or
+// 128 in token rows, everything on 16-byte boundaries, and extents and
+// strides a tensor map can hold.
+bool tc_takes(const kvcs_cache &c, int block_size, const kvcs_attention &a) {
+  const PageMap m = page_map(c, block_size);
+  return a.kv_dtype != KVCS_DTYPE_FP8_E4M3 && (c.head_bytes == 128 || c.head_bytes == 256) &&
+         (c.layout == KVCS_LAYOUT_NHD || c.layout == KVCS_LAYOUT_HND) && !needs_8(c) &&
+         tc_box(c, block_size) >= 8 && c.num_blocks > 0 && c.num_blocks < (1ll << 31) &&
+         m.block_stride < (1ll << 40);
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// One half (K or V) of a pool as a tensor [block][sub-block][head][slot][element],
+// read in boxes of `box` slots by 64 elements.
+bool half_map(CUtensorMap *map, const PageMap &m, int half, int heads, int dim, bool bf16, int box) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const long long subs = m.block_size / m.kbs;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(m.kbs),
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(subs),
+                              static_cast<cuuint64_t>(m.num_blocks)};
+  const cuuint64_t strides[4] = {
+      static_cast<cuuint64_t>(m.slot_stride), static_cast<cuuint64_t>(m.head_stride),
+      static_cast<cuuint64_t>(subs > 1 ? m.sub_stride : m.block_stride),
+      static_cast<cuuint64_t>(m.block_stride)};
+  const cuuint32_t boxes[5] = {64, static_cast<cuuint32_t>(box), 1, 1, 1};
+  const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                const_cast<unsigned char *>(m.base) + half * m.half_stride, dims, strides, boxes,
+                steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The launches of one attention call.  A request's rows are its new tokens
+// times the query heads per KV head: up to 16 rows go to the narrow kernel,
+// more to the tensor-memory kernel, or to the wide one where that does not
+// take the cache or no request can have more than 64 rows.  max_new bounds
+// the rows, so a decode step launches only the narrow kernel; when total_new
+// = num_requests * max_new every request has max_new tokens and one kernel
+// is enough either way.
+constexpr int kNarrowRows = 16;
+constexpr int kWideRows = 64;
+constexpr int kTcMaxSplits = 16;
+constexpr int kTcMinTiles = 4;   // token tiles a part holds, at least (on average)
+
 struct AttendPlan {
-  bool narrow, wide;
-  int narrow_grid, wide_grid;
+  bool narrow, wide, tc;
+  int narrow_grid, wide_grid;      // wide_grid: the wide or the tensor-memory kernel's
+  int splits;                      // tensor-memory kernel: parts per unit
+  long long wide_tickets;
   long long part_floats;
 };
-constexpr int kNarrowRows = 16;
 
-AttendPlan plan_attend(const AttnParams &p, int kv_dtype, int sms) {
+AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_attention &a, int sms) {
   AttendPlan pl;
+  std::memset(&pl, 0, sizeof(pl));
   const long long rows = p.tab.max_new * p.group;
-  pl.wide = rows > kNarrowRows;
-  pl.narrow = !pl.wide || (p.tab.total_new != p.tab.num_requests * p.tab.max_new &&
-                           p.group <= kNarrowRows);
+  const long long R = p.tab.num_requests;
+  const bool alike = p.tab.total_new == R * p.tab.max_new;
+  const bool more = rows > kNarrowRows;
+  pl.tc = rows > kWideRows && tc_takes(c, p.map.block_size, a);
+  pl.wide = more && !pl.tc;
+  pl.narrow = !more || (!alike && p.group <= kNarrowRows);
   long long nf = 0, wf = 0;
-  auto shape = kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::shape
-               : kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::shape
-                                             : &AttendLaunch<kKvFp8>::shape;
+  auto shape = a.kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::shape
+               : a.kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::shape
+                                               : &AttendLaunch<kKvFp8>::shape;
   shape(p.head_dim, false, sms, &pl.narrow_grid, &nf);
   shape(p.head_dim, true, sms, &pl.wide_grid, &wf);
-  pl.part_floats = std::max(pl.narrow ? nf : 0, pl.wide ? wf : 0);
+  pl.wide_tickets = pl.wide_grid;
+  if (pl.tc) {
+    const long long tiles = alike ? R * ((rows + kTcRows - 1) / kTcRows)
+                                  : p.tab.total_new * p.group / kTcRows + std::min(R, p.tab.total_new);
+    const long long units = tiles * p.kv_heads;
+    // few units: the token ranges are split, as far as their parts stay long
+    const long long key_tiles = p.tab.total_positions * p.map.block_size / std::max(1ll, R) / kTcKeys;
+    pl.splits = static_cast<int>(std::max(
+        1ll, std::min({sms / std::max(1ll, units), key_tiles / kTcMinTiles,
+                       static_cast<long long>(kTcMaxSplits)})));
+    pl.wide_grid = static_cast<int>(std::min<long long>(sms, units * pl.splits));
+    pl.wide_tickets = pl.splits > 1 ? units * 8 : 0;   // one per warp's rows
+    wf = pl.splits > 1 ? units * pl.splits * kTcRows * (p.head_dim + 2) : 0;
+  }
+  pl.part_floats = std::max(pl.narrow ? nf : 0, pl.wide || pl.tc ? wf : 0);
   return pl;
 }
 
-// Counters first (two launches' worth), then the partial results.
+// Counters first (both launches'), then the partial results.
+long long attend_tickets(const AttendPlan &pl) { return pl.narrow_grid + pl.wide_tickets; }
 int64_t attend_workspace(const AttendPlan &pl) {
-  const int64_t tickets = (static_cast<int64_t>(pl.narrow_grid) + pl.wide_grid) * 4;
-  return (tickets + 255) / 256 * 256 + pl.part_floats * 4;
+  return (attend_tickets(pl) * 4 + 255) / 256 * 256 + pl.part_floats * 4;
 }
 
 __global__ void __launch_bounds__(1024) kvcs_tickets_kernel(u32 *tickets, int n) {
@@ -183,8 +272,8 @@ using namespace kvcs;
 extern "C" {
 
 int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_t num_requests,
-                             const kvcs_attention *att, int32_t num_sms, int64_t *bytes) {
-  if (!bytes || num_requests < 0) return KVCS_EINVAL;
+                             int64_t total_positions, const kvcs_attention *att, int32_t num_sms, int64_t *bytes) {
+  if (!bytes || num_requests < 0 || total_positions < 0) return KVCS_EINVAL;
   const int rc = check_attention(cache, block_size, att);
   if (rc != KVCS_OK) return rc;
   int sms = num_sms;
@@ -192,8 +281,8 @@ int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_
   kvcs_requests reqs;
   std::memset(&reqs, 0, sizeof(reqs));
   reqs.num_requests = num_requests;
-  const AttnParams p = attn_params(cache, block_size, &reqs, 0, att, nullptr);
-  *bytes = attend_workspace(plan_attend(p, att->kv_dtype, sms));
+  const AttnParams p = attn_params(cache, block_size, &reqs, total_positions, att, nullptr);
+  *bytes = attend_workspace(plan_attend(p, *cache, *att, sms));
   return KVCS_OK;
 }
 
@@ -212,11 +301,11 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
   AttnParams p = attn_params(cache, block_size, reqs, total_positions, att, status);
-  const AttendPlan pl = plan_attend(p, att->kv_dtype, sms);
+  const AttendPlan pl = plan_attend(p, *cache, *att, sms);
   if (att->workspace_bytes < attend_workspace(pl)) return KVCS_EINVAL;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   u32 *tickets = static_cast<u32 *>(att->workspace);
-  const int n_tickets = pl.narrow_grid + pl.wide_grid;
+  const int n_tickets = static_cast<int>(attend_tickets(pl));
   p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(att->workspace) +
                                      (n_tickets * 4ll + 255) / 256 * 256);
   {
@@ -249,8 +338,26 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
     p.tickets = tickets + pl.narrow_grid;
     if (attend(p, true, pl.wide_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;
   }
+  if (pl.tc) {
+    TcParams t;
+    std::memset(&t, 0, sizeof(t));
+    t.a = p;
+    t.a.row_lo = pl.narrow ? kNarrowRows + 1 : 1;
+    t.a.row_hi = 0x7fffffff;
+    t.a.tickets = tickets + pl.narrow_grid;
+    t.box = tc_box(*cache, block_size);
+    t.splits = pl.splits;
+    t.timeout_ns = kAttendTimeoutNs;
+    const bool bf16 = att->kv_dtype == KVCS_DTYPE_BF16;
+    CUtensorMap mk, mv;
+    if (!half_map(&mk, p.map, 0, p.kv_heads, p.head_dim, bf16, t.box) ||
+        !half_map(&mv, p.map, 1, p.kv_heads, p.head_dim, bf16, t.box))
+      return KVCS_ECUDA;
+    auto run = bf16 ? &AttendLaunch<kKvBf16>::attend_tc : &AttendLaunch<kKvFp16>::attend_tc;
+    if (run(t, mk, mv, pl.wide_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;
+  }
   if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-  count_launches(1 + (pl.narrow ? 1 : 0) + (pl.wide ? 1 : 0));
+  count_launches(1 + (pl.narrow ? 1 : 0) + (pl.wide ? 1 : 0) + (pl.tc ? 1 : 0));
   return KVCS_OK;
 }
 

@@ -6,7 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "kvcs.h"
-#include "kvcs_attn_common.cuh"
+#include "kvcs_attend_tc.cuh"
 
 namespace kvcs {
 
@@ -22,6 +22,9 @@ struct AttendLaunch {
   static void shape(int dim, bool wide, int sms, int *grid, long long *part_floats);
   static cudaError_t attend(const AttnParams &p, bool wide, int grid, bool after_zero,
                             cudaStream_t st);
+  // the tensor-memory kernel (16-bit caches, heads of 64 or 128)
+  static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
+                               int grid, bool after_zero, cudaStream_t st);
   static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st);
 };
 

@@ -1,0 +1,680 @@
+// kvcs_attend_tc.cuh -- attention of a chunk of new tokens over a paged cache
+// on the tensor-memory tensor cores (16-bit caches, heads of 64 or 128).
+//
+// Mathematics as in kvcs_attend.cuh.  Bound: 4 * head_dim operations per
+// visible (row, token) pair, far above the bytes, so the tensor cores are the
+// floor, and next to them the exponentials (one per pair).
+//
+// A unit is 256 query rows (new tokens x the KV head's query group, so that
+// the group shares every K and V tile) in two tiles of 128, against tiles of
+// 128 tokens.  Roles of the CTA's warps:
+//   warp 9     loads K and V tiles page by page with TMA (boxes of as many
+//              slots as a page holds in a row, 128-byte swizzle) into a ring;
+//   warp 8     issues the products: S_i = Q_i K^T into tensor memory, then
+//              O_i += P_i V with P_i read from tensor memory;
+//   warps 0-3, warps 4-7   the softmax of one query tile each, a thread per
+//              row: S from tensor memory, weights back over S as 16-bit P.
+// The two tiles take turns: while one tile's weights are made, the other
+// tile's products run.  The tensor cores work in issue order, so P_i is read
+// before S_i of the next token tile overwrites it, and the signal that S_i is
+// ready also says that O_i's last addition is done.
+//
+// The running maximum is only raised when a row's scores pass it by more than
+// 2^8: weights then stay below 2^8 and nothing has to be rescaled for most
+// tiles; when a row does pass, its thread rescales its row of O in tensor
+// memory itself (the additions to it are done by then).
+//
+// A weight of 0 times a NaN or infinite V value would be NaN.  V rows of slots
+// that hold no token are therefore zeroed in shared memory, and in tiles that
+// some row sees only in part, rows with a non-finite value are zeroed and
+// noted; the rows that do see them add them at the end.
+#pragma once
+
+#include "kvcs_attend.cuh"
+#include "kvcs_tcgen.cuh"
+
+namespace kvcs {
+
+// Three warpgroups (the third: loads, products, two idle warps).  Launched
+// with 168 registers a thread, 64512 in all; the softmax warpgroups take 208
+// (a row of S is 128 of them), the third keeps 88: 2 * 208 + 88 = 3 * 168.
+constexpr int kTcThreads = 384;
+constexpr int kTcRegsSoftmax = 208;
+constexpr int kTcRegsOther = 88;
+constexpr int kTcRows = 256;      // query rows of a unit
+constexpr int kTcKeys = 128;      // tokens of a tile
+constexpr float kTcSlack = 8.0f;  // log2 of the largest weight left unscaled
+constexpr int kTcDirty = 8;       // partly seen tiles of a unit, at most
+
+template <int kDim>
+struct TcShape {
+  static constexpr int kHalves = kDim / 64;               // 128-byte column halves
+  static constexpr int kHalfBytes = 128 * 128;            // 128 rows of 128 bytes
+  static constexpr int kTileBytes = kHalves * kHalfBytes;  // Q, K or V tile
+  static constexpr int kStages = kDim == 128 ? 5 : 10;
+  static constexpr int kSmemBytes = (2 + kStages) * kTileBytes + 1024;
+  static constexpr int kPartFloats = kDim + 2;
+};
+
+struct TcParams {
+  AttnParams a;
+  int box;        // slots a TMA box takes
+  int splits;     // parts of the token range per unit
+  u64 timeout_ns;
+};
+
+// A unit as every role sees it.
+struct TcUnit {
+  Request q;
+  int head, row0, rows_all;
+  int tiles;          // query tiles with rows: 1 or 2
+  int k0, k1;         // token tiles of this part
+  int lo, hi;         // tokens some row sees: [lo, hi)
+  int split;
+  long long index;    // unit number (of the join)
+};
+
+// Finds units in growing order; every lane of a warp calls it together.
+struct TcFinder {
+  long long chunk = 0, before = 0;   // requests [chunk, chunk + 32) start at tile `before`
+
+  __device__ __forceinline__ TcUnit find(const TcParams &p, long long u) {
+    const AttnParams &a = p.a;
+    const int lane = threadIdx.x & 31;
+    TcUnit x;
+    x.split = static_cast<int>(u % p.splits);
+    x.index = u / p.splits;
+    x.head = static_cast<int>(x.index % a.kv_heads);
+    const long long tile = x.index / a.kv_heads;
+    for (;;) {
+      const long long r = chunk + lane;
+      Request q;
+      q.n = 0;
+      if (r < a.tab.num_requests) q = read_request(a.tab, r, a.map.block_size, false);
+      const long long rows = static_cast<long long>(q.n) * a.group;
+      const int tiles = rows < a.row_lo || rows > a.row_hi
+                            ? 0 : static_cast<int>((rows + kTcRows - 1) / kTcRows);
+      int inc = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const int all = __shfl_sync(0xffffffffu, inc, 31);
+      if (tile < before + all) {
+        const int at = static_cast<int>(tile - before);
+        const int src = __ffs(__ballot_sync(0xffffffffu, inc > at)) - 1;
+        const int first = __shfl_sync(0xffffffffu, inc - tiles, src);
+        const int n_tiles = __shfl_sync(0xffffffffu, tiles, src);
+        x.q.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+        x.q.q0 = __shfl_sync(0xffffffffu, q.q0, src);
+        x.q.n = __shfl_sync(0xffffffffu, q.n, src);
+        x.q.keys = __shfl_sync(0xffffffffu, q.keys, src);
+        x.q.at = __shfl_sync(0xffffffffu, q.at, src);
+        x.q.base = 0;
+        // the rows that see most tokens first
+        x.row0 = (n_tiles - 1 - (at - first)) * kTcRows;
+        break;
+      }
+      before += all;
+      chunk += 32;
+    }
+    x.rows_all = x.q.n * a.group;
+    x.tiles = x.rows_all - x.row0 > 128 ? 2 : 1;
+    const int last_row = min(x.row0 + kTcRows, x.rows_all) - 1;
+    const int at0 = x.q.at + x.row0 / a.group, at1 = x.q.at + last_row / a.group;
+    x.lo = a.window > 0 ? max(0, at0 - a.window + 1) : 0;
+    x.hi = max(0, min(x.q.keys, at1 + 1));
+    const int t0 = x.lo / kTcKeys;
+    const int t1 = x.hi > x.lo ? (x.hi + kTcKeys - 1) / kTcKeys : t0;
+    const int per = (t1 - t0 + p.splits - 1) / p.splits;
+    x.k0 = min(t1, t0 + x.split * per);
+    x.k1 = min(t1, x.k0 + per);
+    return x;
+  }
+};
+
+struct TcShared {
+  u64 full[10], empty[10];
+  u64 q_full[2], s_full[2], p_ready[2], o_full[2];
+  u64 fix, loaded, released, drain;
+  u32 tmem;
+  int any_bad[2];                  // some block id of the unit's request is bad
+  int n_dirty[2];                  // noted tiles, by parity of the unit
+  int dirty_tile[2][kTcDirty];
+  u32 dirty[2][kTcDirty][4];
+};
+
+// Whether token `key` (below the request's count) lies in a block of the pool.
+__device__ __forceinline__ bool good_block(const AttnParams &a, const Request &q, int key) {
+  const int b = a.tab.block_ids[q.pos0 + key / a.map.block_size];
+  return b >= 0 && b < a.map.num_blocks;
+}
+
+__device__ __forceinline__ float lo_of(u32 w, bool bf16) { return half_bits_to_float(w & 0xffffu, bf16); }
+__device__ __forceinline__ float hi_of(u32 w, bool bf16) { return half_bits_to_float(w >> 16, bf16); }
+
+template <bool kBf16, int kDim>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    kvcs_attend_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v) {
+  using S = TcShape<kDim>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ TcShared sh;
+  __shared__ long long s_sum[kTcThreads / 32];
+  const AttnParams &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const u32 smem = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;   // swizzled tiles: 1 KiB
+  const u32 q_smem = smem, ring = smem + 2 * S::kTileBytes;
+  const u32 full = ptx::smem_addr(sh.full), empty = ptx::smem_addr(sh.empty);
+  const u32 q_full = ptx::smem_addr(sh.q_full), s_full = ptx::smem_addr(sh.s_full);
+  const u32 p_ready = ptx::smem_addr(sh.p_ready), o_full = ptx::smem_addr(sh.o_full);
+  const u32 fix = ptx::smem_addr(&sh.fix), loaded = ptx::smem_addr(&sh.loaded);
+  const u32 released = ptx::smem_addr(&sh.released), drain = ptx::smem_addr(&sh.drain);
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(q_full + 8 * i, 4);
+      ptx::mbar_init(s_full + 8 * i, 1);
+      ptx::mbar_init(p_ready + 8 * i, 4);
+      ptx::mbar_init(o_full + 8 * i, 1);
+    }
+    ptx::mbar_init(fix, 1);
+    ptx::mbar_init(loaded, 1);
+    ptx::mbar_init(drain, 1);
+    ptx::mbar_init(released, 8);
+    ptx::fence_barrier_init();
+  }
+  if (warp == 8) tc::tmem_alloc(ptx::smem_addr(&sh.tmem), 512);
+  // units of the launch
+  long long mine = 0;
+  for (long long r = tid; r < a.tab.num_requests; r += kTcThreads) {
+    const Request q = read_request(a.tab, r, a.map.block_size, blockIdx.x == 0);
+    const long long rows = static_cast<long long>(q.n) * a.group;
+    if (rows >= a.row_lo && rows <= a.row_hi) mine += (rows + kTcRows - 1) / kTcRows;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_sum[warp] = mine;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  long long units = 0;
+  for (int w = 0; w < kTcThreads / 32; ++w) units += s_sum[w];
+  units *= static_cast<long long>(a.kv_heads) * p.splits;
+  const u32 tmem = sh.tmem;
+  // columns: S0, S1 (weights over their first half), O0, O1
+  const u64 limit = p.timeout_ns;
+  bool ok = true;
+  TcFinder finder;
+
+  if (warp >= 8) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsOther));
+   if (warp == 9) {
+    // ----------------------------------------------------------------- loads
+    const int boxes = kTcKeys / p.box;
+    long long n_unit = 0;
+    u32 it = 0;          // tiles put into the ring
+    u32 n_fix = 0;
+    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x, ++n_unit) {
+      const TcUnit x = finder.find(p, u);
+      const int par = n_unit & 1;
+      // block ids of the tokens this part needs
+      bool bad = false;
+      const int bs = a.map.block_size;
+      const int key_lo = max(x.k0 * kTcKeys, x.lo), key_hi = min(x.k1 * kTcKeys, x.hi);
+      for (int b = key_lo / bs + lane; b * static_cast<long long>(bs) < key_hi; b += 32) {
+        const int id = a.tab.block_ids[x.q.pos0 + b];
+        bad |= id < 0 || id >= a.map.num_blocks;
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad && lane == 0) raise(a.tab, kStatusBadBlockId);
+      if (lane == 0) {
+        sh.any_bad[par] = bad;
+        sh.n_dirty[par] = 0;
+      }
+      const int at0 = x.q.at + x.row0 / a.group;
+      const int at1 = x.q.at + (min(x.row0 + kTcRows, x.rows_all) - 1) / a.group;
+      int n_dirty = 0;
+      for (int k = x.k0; k < x.k1 && ok; ++k) {
+        const int key0 = k * kTcKeys;
+        // tiles some row sees only in part, or with slots that hold no token
+        const bool partly = key0 + kTcKeys - 1 > at0 || (a.window > 0 && key0 <= at1 - a.window);
+        const bool holes = key0 + kTcKeys > x.q.keys || bad;
+        // this lane's boxes of the tile (boxes of 8 slots: up to 16)
+        for (int half = 0; half < 2 && ok; ++half, ++it) {   // K, then V
+          const u32 stage = it % S::kStages;
+          if (it >= S::kStages)
+            ok = ptx::mbar_wait_bounded(empty + 8 * stage, (it / S::kStages - 1) & 1, limit);
+          if (!ok) break;
+          const u32 dst = ring + stage * S::kTileBytes;
+          const bool mend = half == 1 && (partly || holes);
+          const u32 bar = mend ? fix : full + 8 * stage;
+          int block = -1, slot = 0;
+          const int key = key0 + lane * p.box;
+          if (lane < boxes && key < x.q.keys) {
+            const int pos = key / bs;
+            slot = key - pos * bs;
+            block = a.tab.block_ids[x.q.pos0 + pos];
+            if (block >= a.map.num_blocks) block = -1;
+          }
+          const int n = __popc(__ballot_sync(0xffffffffu, block >= 0));
+          if (lane == 0)
+            ptx::mbar_arrive_expect_tx(bar, static_cast<u32>(n) * p.box * 128 * S::kHalves);
+          __syncwarp();
+          if (block >= 0) {
+            const int sub = slot / a.map.kbs;
+#pragma unroll
+            for (int h = 0; h < S::kHalves; ++h)
+              tc::tma_load(dst + h * S::kHalfBytes + lane * p.box * 128, half ? &map_v : &map_k,
+                           h * 64, slot - sub * a.map.kbs, x.head, sub, block, bar);
+          }
+          if (mend) {
+            ok = ptx::mbar_wait_bounded(fix, n_fix & 1, limit);
+            ++n_fix;
+            u32 words = 0;   // lane i < 4: the noted rows of its quarter
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const int row = i * 32 + lane, kk = key0 + row;
+              const bool has = kk >= x.lo && kk < x.hi && (!bad || good_block(a, x.q, kk));
+              bool odd = false;
+              if (has && partly) {
+                constexpr u32 kExp = kBf16 ? 0x7f80u : 0x7c00u;
+#pragma unroll 1
+                for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll 4
+                  for (int c = 0; c < 8; ++c) {
+                    // in an order that spreads the lanes over the banks
+                    const uint4 v = lds128(dst + h * S::kHalfBytes + row * 128 + ((c ^ (lane & 7)) << 4));
+                    const u32 w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      odd |= (w[e] & kExp) == kExp || (w[e] >> 16 & kExp) == kExp;
+                  }
+              }
+              if (!has || odd) {
+#pragma unroll 1
+                for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll 4
+                  for (int c = 0; c < 8; ++c)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                     dst + h * S::kHalfBytes + row * 128 + ((c ^ (lane & 7)) << 4)),
+                                 "r"(0)
+                                 : "memory");
+              }
+              const u32 noted = __ballot_sync(0xffffffffu, odd);
+              if (lane == i) words = noted;
+            }
+            if (__any_sync(0xffffffffu, words != 0)) {
+              if (n_dirty < kTcDirty) {
+                if (lane < 4) sh.dirty[par][n_dirty][lane] = words;
+                if (lane == 0) {
+                  sh.dirty_tile[par][n_dirty] = k;
+                  sh.n_dirty[par] = n_dirty + 1;
+                }
+              }
+              ++n_dirty;
+            }
+            tc::fence_async();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(full + 8 * stage);
+          }
+        }
+      }
+      // one unit ahead of the softmax at most: its notes are kept twice
+      if (ok && n_unit > 0) ok = ptx::mbar_wait_bounded(released, (n_unit - 1) & 1, limit);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(loaded);
+    }
+    // after a wait that ran out: nothing may still be on its way to this CTA
+    if (!ok)
+      for (u32 i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+        ptx::mbar_wait_bounded(full + 8 * (i % S::kStages), (i / S::kStages) & 1, limit);
+   } else if (warp == 8) {
+    // -------------------------------------------------------------- products
+    constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
+    constexpr u32 kDescO = tc::instr_desc(kBf16, 128, kDim, true);
+    u32 it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    auto scores = [&](int i, u32 stage) {
+      const u32 q = q_smem + i * S::kTileBytes, k = ring + stage * S::kTileBytes;
+#pragma unroll
+      for (int s = 0; s < kDim / 16; ++s) {
+        const u32 off = (s >> 2) * S::kHalfBytes + (s & 3) * 32;
+        tc::mma_ss(tmem + i * 128, tc::smem_desc(q + off, 16, 1024), tc::smem_desc(k + off, 16, 1024),
+                   kDescS, s > 0);
+      }
+    };
+    auto values = [&](int i, u32 stage, bool add) {
+      const u32 v = ring + stage * S::kTileBytes;
+#pragma unroll
+      for (int s = 0; s < kTcKeys / 16; ++s)
+        tc::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8,
+                   tc::smem_desc(v + s * 2048, S::kHalfBytes, 1024), kDescO, add || s > 0);
+    };
+    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const TcUnit x = finder.find(p, u);
+      if (lane == 0) {
+        u32 k_stage = it % S::kStages;
+        for (int k = x.k0; k <= x.k1 && ok; ++k) {
+          // at k: S of tile k and O of tile k - 1
+          if (x.k0 == x.k1) break;
+          const bool do_s = k < x.k1, do_o = k > x.k0;
+          // ring order: K0 V0 K1 V1 ...; V of tile k - 1 precedes K of tile k
+          u32 v_stage = 0;
+          if (do_o) {
+            v_stage = it % S::kStages;
+            ok = ptx::mbar_wait_bounded(full + 8 * v_stage, (it / S::kStages) & 1, limit);
+            if (!ok) break;
+            ++it;
+          }
+          bool have_k = false;
+          for (int i = 0; i < x.tiles && ok; ++i) {
+            if (do_o) {
+              ok = ptx::mbar_wait_bounded(p_ready + 8 * i, n_p[i] & 1, limit);
+              if (!ok) break;
+              ++n_p[i];
+              tc::fence_after();
+              values(i, v_stage, k - 1 > x.k0);
+              if (i == x.tiles - 1) tc::commit(empty + 8 * v_stage);
+              if (!do_s) tc::commit(o_full + 8 * i);
+            }
+            if (do_s) {
+              if (!have_k) {
+                k_stage = it % S::kStages;
+                ok = ptx::mbar_wait_bounded(full + 8 * k_stage, (it / S::kStages) & 1, limit);
+                if (!ok) break;
+                ++it;
+                have_k = true;
+              }
+              if (k == x.k0) {
+                ok = ptx::mbar_wait_bounded(q_full + 8 * i, n_q[i] & 1, limit);
+                if (!ok) break;
+                ++n_q[i];
+              }
+              tc::fence_after();
+              scores(i, k_stage);
+              tc::commit(s_full + 8 * i);
+              if (i == x.tiles - 1) tc::commit(empty + 8 * k_stage);
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      it = __shfl_sync(0xffffffffu, it, 0);
+    }
+    if (!ok && lane == 0) {   // let the products issued so far end
+      tc::commit(drain);
+      ptx::mbar_wait_bounded(drain, 0, limit);
+    }
+   }
+  } else {
+    // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsSoftmax));
+    const int i = warp >> 2;                 // query tile
+    const int lr = (warp & 3) * 32 + lane;   // row of the tile
+    const u32 lanes = static_cast<u32>((warp & 3) * 32) << 16;
+    const u32 ts = tmem + i * 128 + lanes, to = tmem + 256 + i * 128 + lanes;
+    u32 n_s = 0, n_o = 0;
+    long long n_unit = 0;
+    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x, ++n_unit) {
+      const TcUnit x = finder.find(p, u);
+      const int par = n_unit & 1;
+      const bool work = i < x.tiles;
+      const int row = x.row0 + i * 128 + lr;
+      const bool has = row < x.rows_all;
+      const int row_c = has ? row : x.rows_all - 1;
+      const int tok_i = row_c / a.group, hq = x.head * a.group + row_c - tok_i * a.group;
+      const int at = x.q.at + tok_i;
+      float m = kNegInf, l = 0.0f;
+      const int nk = x.k1 - x.k0;
+      const unsigned char *q_row =
+          static_cast<const unsigned char *>(a.q) +
+          ((x.q.q0 + tok_i) * a.q_stride + static_cast<long long>(hq) * kDim) * 2;
+      if (work && nk > 0) {
+        // the warp's query rows into shared memory, 16 bytes a lane
+        const u32 qs = q_smem + i * S::kTileBytes;
+        constexpr int kPieces = kDim / 8;   // 16-byte pieces of a row
+#pragma unroll 8
+        for (int n = 0; n < kPieces; ++n) {
+          const int e = n * 32 + lane, r = e / kPieces, c = e % kPieces;
+          const u64 src = __shfl_sync(0xffffffffu, reinterpret_cast<u64>(q_row), r);
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+          const int tr = (warp & 3) * 32 + r;
+          const u32 d = qs + (c >> 3) * S::kHalfBytes + tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(v.x), "r"(v.y),
+                       "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        tc::fence_async();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(q_full + 8 * i);
+        // what the warp's rows all see, and what none of them sees
+        const int row_first = min(x.row0 + i * 128 + (warp & 3) * 32, x.rows_all - 1);
+        const int row_last = min(row_first + 31, x.rows_all - 1);
+        const int at_min = x.q.at + row_first / a.group, at_max = x.q.at + row_last / a.group;
+        const int upto = min(at, x.q.keys - 1);
+        for (int k = x.k0; k < x.k1; ++k) {
+          ok = ptx::mbar_wait_bounded(s_full + 8 * i, n_s & 1, limit);
+          if (__any_sync(0xffffffffu, !ok)) {
+            ok = false;
+            break;
+          }
+          ++n_s;
+          tc::fence_after();
+          const int key0 = k * kTcKeys;
+          u32 s[128];
+          tc::ld32(ts, s);
+          tc::ld32(ts + 32, s + 32);
+          tc::ld32(ts + 64, s + 64);
+          tc::ld32(ts + 96, s + 96);
+          tc::wait_ld();
+          // scores = sc * s; capped ones, and those of a scale that would turn
+          // the maximum round or make 0 of a masked score, are made first
+          float sc = a.scale;
+          if (a.cap != 0.0f || a.scale <= 0.0f) {
+            sc = 1.0f;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              s[c] = __float_as_uint(score_of(a, __uint_as_float(s[c]), 1.0f));
+          }
+          if (key0 + kTcKeys - 1 > min(at_min, x.q.keys - 1) ||
+              (a.window > 0 && key0 <= at_max - a.window)) {
+            const int hi = upto - key0, lo = a.window > 0 ? at - a.window + 1 - key0 : 0;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > hi || c < lo) s[c] = 0xff800000u;
+          }
+          if (sh.any_bad[par]) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (key0 + c < x.q.keys && !good_block(a, x.q, key0 + c)) s[c] = 0xff800000u;
+          }
+          float m0 = kNegInf, m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            m0 = fmaxf(m0, __uint_as_float(s[c]));
+            m1 = fmaxf(m1, __uint_as_float(s[c + 1]));
+            m2 = fmaxf(m2, __uint_as_float(s[c + 2]));
+            m3 = fmaxf(m3, __uint_as_float(s[c + 3]));
+          }
+          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
+          const bool raise_m = mx > m + kTcSlack || (m == kNegInf && mx != kNegInf);
+          if (__any_sync(0xffffffffu, raise_m)) {
+            const float f = raise_m ? (m == kNegInf ? 0.0f : ex2(m - mx)) : 1.0f;
+            if (raise_m) m = mx;
+            l *= f;
+            if (k > x.k0) {
+              const u64 ff = tc::pair(f, f);
+#pragma unroll 1
+              for (int c = 0; c < kDim; c += 16) {
+                u32 o[16];
+                tc::ld16(to + c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  float y0, y1;
+                  tc::unpair(tc::mul2(tc::pair(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), ff),
+                             y0, y1);
+                  o[e] = __float_as_uint(y0);
+                  o[e + 1] = __float_as_uint(y1);
+                }
+                tc::st16(to + c, o);
+              }
+            }
+          }
+          const float base = m == kNegInf ? 0.0f : -m;
+          const u64 sc2 = tc::pair(sc, sc), base2 = tc::pair(base, base);
+          u64 sum0 = 0, sum1 = 0;   // pairs of +0
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            u32 w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float y[4];
+              tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])),
+                                  sc2, base2), y[0], y[1]);
+              tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c + e + 2]),
+                                           __uint_as_float(s[c + e + 3])), sc2, base2), y[2], y[3]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
+              sum0 = tc::add2(sum0, tc::pair(y[0], y[1]));
+              sum1 = tc::add2(sum1, tc::pair(y[2], y[3]));
+              w[e / 2] = pack2<kBf16>(y[0], y[1]);
+              w[e / 2 + 1] = pack2<kBf16>(y[2], y[3]);
+            }
+            tc::st16(ts + c / 2, w);
+          }
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(p_ready + 8 * i);
+          float x0, x1;
+          tc::unpair(tc::add2(sum0, sum1), x0, x1);
+          l += x0 + x1;
+        }
+        if (ok) {
+          const bool done = ptx::mbar_wait_bounded(o_full + 8 * i, n_o & 1, limit);
+          ok = !__any_sync(0xffffffffu, !done);
+          ++n_o;
+          tc::fence_after();
+        }
+      }
+      if (!ok) break;
+      // all loads of the unit are noted before this
+      const bool noted = ptx::mbar_wait_bounded(loaded, n_unit & 1, limit);
+      ok = !__any_sync(0xffffffffu, !noted);
+      if (!ok) break;
+      const int n_dirty = sh.n_dirty[par];
+      const bool whole = p.splits == 1;
+      if (work) {
+        const float inv = l > 0.0f || l != l ? a.v_scale / l : 0.0f;
+        float *part = a.part + ((x.index * p.splits + x.split) * kTcRows + i * 128 + lr) *
+                                   static_cast<long long>(S::kPartFloats);
+        const long long out_row = (x.q.q0 + tok_i) * (a.group * a.kv_heads) + hq;
+#pragma unroll
+        for (int c = 0; c < kDim; c += 32) {
+          u32 o[32];
+          if (nk > 0) {
+            tc::ld32(to + c, o);
+            tc::wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
+          }
+          // tokens whose V was taken out of the tiles: for the rows that see them
+          for (int d = 0; d < n_dirty; ++d) {
+            const int key0 = sh.dirty_tile[par][d] * kTcKeys;
+            for (int kk = 0; kk < kTcKeys; ++kk) {
+              if (!(sh.dirty[par][d][kk >> 5] >> (kk & 31) & 1u)) continue;
+              const int key = key0 + kk;
+              if (key > at || (a.window > 0 && key <= at - a.window)) continue;
+              const int pos = key / a.map.block_size;
+              const unsigned char *kp =
+                  a.map.base + token_offset(a.map, a.tab.block_ids[x.q.pos0 + pos],
+                                            key - pos * a.map.block_size, x.head);
+              float dot = 0.0f;
+              for (int e = 0; e < kDim / 2; ++e) {
+                const u32 kw = reinterpret_cast<const u32 *>(kp)[e];
+                const u32 qw = reinterpret_cast<const u32 *>(q_row)[e];
+                dot += lo_of(kw, kBf16) * lo_of(qw, kBf16) + hi_of(kw, kBf16) * hi_of(qw, kBf16);
+              }
+              const float w = ex2(score_of(a, dot, 1.0f) - m);
+              const u32 *vp = reinterpret_cast<const u32 *>(kp + a.map.half_stride) + c / 2;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const u32 vw = vp[e];
+                o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + w * lo_of(vw, kBf16));
+                o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + w * hi_of(vw, kBf16));
+              }
+            }
+          }
+          if (has && whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.out) +
+                                                   (out_row * kDim + c) * 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              u32 w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = pack2<kBf16>(__uint_as_float(o[8 * e + 2 * j]) * inv,
+                                    __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (has) {
+            float2 *dst = reinterpret_cast<float2 *>(part + c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              dst[e] = make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          }
+        }
+        if (has && whole && a.lse) a.lse[out_row] = l == 0.0f ? kNegInf : kLn2 * (m + log2f(l));
+        if (has && !whole) *reinterpret_cast<float2 *>(part + kDim) = make_float2(m, l);
+      }
+      if (!whole && work) {
+        // a counter per warp's rows: the last part's warp to arrive joins them, in order
+        ptx::grid_dep_wait();   // the counters are zero from here on
+        __threadfence();
+        __syncwarp();
+        u32 before_me = 0;
+        if (lane == 0) before_me = atomicAdd(a.tickets + x.index * 8 + warp, 1u);
+        if (__shfl_sync(0xffffffffu, before_me, 0) == static_cast<u32>(p.splits - 1)) {
+          __threadfence();
+          const int first = i * 128 + (warp & 3) * 32;
+          const int rows = min(32, x.rows_all - x.row0 - first);
+          for (int e = lane; e < rows * (kDim / 2); e += 32) {
+            const int r = first + e / (kDim / 2), col = e % (kDim / 2) * 2;
+            float jm = kNegInf, jl = 0.0f, o0 = 0.0f, o1 = 0.0f;
+            for (int s = 0; s < p.splits; ++s) {
+              const float *src = a.part + ((x.index * p.splits + s) * kTcRows + r) *
+                                              static_cast<long long>(S::kPartFloats);
+              const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + kDim));
+              const float2 o = __ldcg(reinterpret_cast<const float2 *>(src + col));
+              const float mn = fmaxf(jm, ml.x), mb = mn == kNegInf ? 0.0f : mn;
+              const float f0 = ex2(jm - mb), f1 = ex2(ml.x - mb);
+              jl = jl * f0 + ml.y * f1;
+              o0 = o0 * f0 + o.x * f1;
+              o1 = o1 * f0 + o.y * f1;
+              jm = mn;
+            }
+            const float inv = jl > 0.0f || jl != jl ? a.v_scale / jl : 0.0f;
+            store_out(a, x.q, x.head, x.row0 + r, col, o0 * inv, o1 * inv, kBf16);
+            if (col == 0) store_lse(a, x.q, x.head, x.row0 + r, jm, jl);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(released);
+    }
+  }
+  if (!ok && lane == 0) raise(a.tab, kStatusTimeout);
+  ptx::grid_dep_wait();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 8) tc::tmem_free(tmem, 512);
+}
+
+}  // namespace kvcs

@@ -1,7 +1,6 @@
 // kvcs_attend_type.cu -- the attention and attention-mass kernels of one
 // cache type (KVCS_KV_TYPE), compiled once per type.
 
-#include "kvcs_attend.cuh"
 #include "kvcs_attend_host.h"
 #include "kvcs_mass.cuh"
 
@@ -43,6 +42,31 @@ struct TypeLaunch {
   }
 
   template <int kDim>
+  static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
+                               int grid, bool after_zero, cudaStream_t st) {
+    if constexpr (kType == kKvFp8) {
+      return cudaErrorNotSupported;
+    } else {
+      auto kernel = kvcs_attend_tc_kernel<kType == kKvBf16, kDim>;
+      constexpr int smem = TcShape<kDim>::kSmemBytes;
+      const cudaError_t e = cudaFuncSetAttribute(
+          reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(grid));
+      cfg.blockDim = dim3(kTcThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = st;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = after_zero ? 1 : 0;
+      return cudaLaunchKernelEx(&cfg, kernel, p, k, v);
+    }
+  }
+
+  template <int kDim>
   static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st) {
     kvcs_mass_kernel<kType, kDim><<<static_cast<unsigned>(grid), kMassThreads, 0, st>>>(p);
     return cudaGetLastError();
@@ -73,6 +97,14 @@ cudaError_t AttendLaunch<kThisType>::attend(const AttnParams &p, bool wide, int 
       return wide ? This::attend<256, true>(p, grid, after_zero, st)
                   : This::attend<256, false>(p, grid, after_zero, st);
   }
+}
+
+template <>
+cudaError_t AttendLaunch<kThisType>::attend_tc(const TcParams &p, const CUtensorMap &k,
+                                               const CUtensorMap &v, int grid, bool after_zero,
+                                               cudaStream_t st) {
+  return p.a.head_dim == 64 ? This::attend_tc<64>(p, k, v, grid, after_zero, st)
+                            : This::attend_tc<128>(p, k, v, grid, after_zero, st);
 }
 
 template <>

@@ -100,19 +100,23 @@ def test_attention_alone():
 def test_workspace_sizes():
     fn = K.load_library().kvcs_attention_workspace
 
-    def size(cache=None, requests=2, sms=152, **kw):
+    def size(cache=None, requests=2, sms=152, positions=100, **kw):
         n = ctypes.c_int64(-1)
         a = attention(q=None, out=None, workspace=None, **kw)
-        rc = fn(K.cache_array([cache or FakeCache()]), 16, requests, ctypes.byref(a), sms,
+        rc = fn(K.cache_array([cache or FakeCache()]), 16, requests, positions, ctypes.byref(a), sms,
                 ctypes.byref(n))
         return n.value if rc == K.KVCS_OK else rc
     one = size(total_new=2, max_new=1)
-    many = size(total_new=400, max_new=200)
+    many = size(FakeCache(layout=3), total_new=400, max_new=200)
     assert 0 < one < many
+    # few long rows: their token range is split, which takes room
+    split = size(requests=1, positions=4000, total_new=64, max_new=64)
+    assert size(requests=64, positions=4000, total_new=64 * 64, max_new=64) < split
     assert size(total_new=2, max_new=1, sms=76) < one
     assert size(q_heads=3) == K.KVCS_EINVAL
     assert size(requests=-1) == K.KVCS_EINVAL
-    assert fn(K.cache_array([FakeCache()]), 16, 2, ctypes.byref(attention()), 152, None) == \
+    assert size(positions=-1) == K.KVCS_EINVAL
+    assert fn(K.cache_array([FakeCache()]), 16, 2, 10, ctypes.byref(attention()), 152, None) == \
         K.KVCS_EINVAL
 
 

@@ -160,7 +160,7 @@ def test_strided_queries_and_given_outputs():
     assert q.stride(0) != hq * d
     out = torch.empty_like(case.q)
     lse = torch.empty((n, hq), device="cuda")
-    ws = torch.full((K.attention_workspace_bytes(case.cache, case.bs, 2, q, max_new=100),), 255,
+    ws = torch.full((K.attention_workspace_bytes(case.cache, case.bs, 2, case.total, q, max_new=100),), 255,
                     dtype=torch.uint8, device="cuda")
     got = K.paged_attention(case.cache, case.bs, *case.table, q, case.new_offsets, out=out, lse=lse,
                             workspace=ws, max_new=100)
