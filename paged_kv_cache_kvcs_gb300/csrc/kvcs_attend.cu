@@ -176,20 +176,24 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// One half (K or V) of a pool as a tensor [block][sub-block][head][slot][element],
-// read in boxes of `box` slots by 64 elements.
-bool half_map(CUtensorMap *map, const PageMap &m, int half, int heads, int dim, bool bf16, int box) {
+// One half (K or V) of a pool as a tensor [block][group of 8 slots][128-byte
+// column][slot of the group][64 elements], read in boxes of `box` slots of one
+// head.  NHD: a token's columns run through its heads; HND: a block's groups
+// run through its sub-blocks and heads.
+bool half_map(CUtensorMap *map, const PageMap &m, int half, int heads, int dim, bool bf16, int box,
+              bool heads_in_groups) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
-  const long long subs = m.block_size / m.kbs;
-  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(m.kbs),
-                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(subs),
+  const int halves = dim / 64;
+  const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(heads_in_groups ? halves : heads * halves),
+                              static_cast<cuuint64_t>(m.block_size / 8) *
+                                  (heads_in_groups ? heads : 1),
                               static_cast<cuuint64_t>(m.num_blocks)};
-  const cuuint64_t strides[4] = {
-      static_cast<cuuint64_t>(m.slot_stride), static_cast<cuuint64_t>(m.head_stride),
-      static_cast<cuuint64_t>(subs > 1 ? m.sub_stride : m.block_stride),
-      static_cast<cuuint64_t>(m.block_stride)};
-  const cuuint32_t boxes[5] = {64, static_cast<cuuint32_t>(box), 1, 1, 1};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(m.slot_stride), 128,
+                                 8 * static_cast<cuuint64_t>(m.slot_stride),
+                                 static_cast<cuuint64_t>(m.block_stride)};
+  const cuuint32_t boxes[5] = {64, 8, static_cast<cuuint32_t>(halves),
+                               static_cast<cuuint32_t>(box / 8), 1};
   const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
   return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                 const_cast<unsigned char *>(m.base) + half * m.half_stride, dims, strides, boxes,
@@ -346,12 +350,14 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
     t.a.row_hi = 0x7fffffff;
     t.a.tickets = tickets + pl.narrow_grid;
     t.box = tc_box(*cache, block_size);
+    t.heads_in_groups = cache->layout == KVCS_LAYOUT_HND;
     t.splits = pl.splits;
     t.timeout_ns = kAttendTimeoutNs;
     const bool bf16 = att->kv_dtype == KVCS_DTYPE_BF16;
     CUtensorMap mk, mv;
-    if (!half_map(&mk, p.map, 0, p.kv_heads, p.head_dim, bf16, t.box) ||
-        !half_map(&mv, p.map, 1, p.kv_heads, p.head_dim, bf16, t.box))
+    const bool hig = t.heads_in_groups != 0;
+    if (!half_map(&mk, p.map, 0, p.kv_heads, p.head_dim, bf16, t.box, hig) ||
+        !half_map(&mv, p.map, 1, p.kv_heads, p.head_dim, bf16, t.box, hig))
       return KVCS_ECUDA;
     auto run = bf16 ? &AttendLaunch<kKvBf16>::attend_tc : &AttendLaunch<kKvFp16>::attend_tc;
     if (run(t, mk, mv, pl.wide_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;

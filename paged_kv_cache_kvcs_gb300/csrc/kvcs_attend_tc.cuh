@@ -8,14 +8,14 @@
 // A unit is 256 query rows (new tokens x the KV head's query group, so that
 // the group shares every K and V tile) in two tiles of 128, against tiles of
 // 128 tokens.  Roles of the CTA's warps:
-//   warp 9     loads K and V tiles page by page with TMA (boxes of as many
+//   warps 9, 11  load K and V tiles page by page with TMA (boxes of as many
 //              slots as a page holds in a row, 128-byte swizzle) into a ring;
-//   warp 8     issues the products: S_i = Q_i K^T into tensor memory, then
-//              O_i += P_i V with P_i read from tensor memory;
+//   warps 8, 10  issue the products of one query tile each: S_i = Q_i K^T into
+//              tensor memory, then O_i += P_i V with P_i from tensor memory;
 //   warps 0-3, warps 4-7   the softmax of one query tile each, a thread per
 //              row: S from tensor memory, weights back over S as 16-bit P.
 // The two tiles take turns: while one tile's weights are made, the other
-// tile's products run.  The tensor cores work in issue order, so P_i is read
+// tile's products run.  One thread's products run in issue order, so P_i is read
 // before S_i of the next token tile overwrites it, and the signal that S_i is
 // ready also says that O_i's last addition is done.
 //
@@ -49,7 +49,9 @@ constexpr int kTcDirty = 8;       // partly seen tiles of a unit, at most
 template <int kDim>
 struct TcShape {
   static constexpr int kHalves = kDim / 64;               // 128-byte column halves
-  static constexpr int kHalfBytes = 128 * 128;            // 128 rows of 128 bytes
+  // Q tile: [half][128 rows][128 bytes]; K and V tiles, as their boxes arrive:
+  // [8 rows][half][128 bytes each], the groups of 8 rows one after another
+  static constexpr int kHalfBytes = 128 * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // Q, K or V tile
   static constexpr int kStages = kDim == 128 ? 5 : 10;
   static constexpr int kSmemBytes = (2 + kStages) * kTileBytes + 1024;
@@ -59,6 +61,7 @@ struct TcShape {
 struct TcParams {
   AttnParams a;
   int box;        // slots a TMA box takes
+  int heads_in_groups;   // HND: the maps' groups of 8 slots run through the heads
   int splits;     // parts of the token range per unit
   u64 timeout_ns;
 };
@@ -136,10 +139,9 @@ struct TcFinder {
 
 struct TcShared {
   u64 full[10], empty[10];
-  u64 q_full[2], s_full[2], p_ready[2], o_full[2];
+  u64 q_full[2], s_full[2], p_half[2], p_ready[2], o_full[2];
   u64 fix, loaded, released, drain;
   u32 tmem;
-  int any_bad[2];                  // some block id of the unit's request is bad
   int n_dirty[2];                  // noted tiles, by parity of the unit
   int dirty_tile[2][kTcDirty];
   u32 dirty[2][kTcDirty][4];
@@ -151,10 +153,22 @@ __device__ __forceinline__ bool good_block(const AttnParams &a, const Request &q
   return b >= 0 && b < a.map.num_blocks;
 }
 
+// Whether some block of the tokens that a unit's part needs is bad (a warp).
+__device__ __forceinline__ bool bad_blocks(const AttnParams &a, const TcUnit &x) {
+  const int bs = a.map.block_size;
+  const int lo = max(x.k0 * kTcKeys, x.lo), hi = min(x.k1 * kTcKeys, x.hi);
+  bool bad = false;
+  for (int b = lo / bs + (threadIdx.x & 31); b * static_cast<long long>(bs) < hi; b += 32) {
+    const int id = a.tab.block_ids[x.q.pos0 + b];
+    bad |= id < 0 || id >= a.map.num_blocks;
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
 __device__ __forceinline__ float lo_of(u32 w, bool bf16) { return half_bits_to_float(w & 0xffffu, bf16); }
 __device__ __forceinline__ float hi_of(u32 w, bool bf16) { return half_bits_to_float(w >> 16, bf16); }
 
-template <bool kBf16, int kDim>
+template <bool kBf16, int kDim, bool kPlain>
 __global__ void __launch_bounds__(kTcThreads, 1)
     kvcs_attend_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v) {
@@ -168,23 +182,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const u32 q_smem = smem, ring = smem + 2 * S::kTileBytes;
   const u32 full = ptx::smem_addr(sh.full), empty = ptx::smem_addr(sh.empty);
   const u32 q_full = ptx::smem_addr(sh.q_full), s_full = ptx::smem_addr(sh.s_full);
-  const u32 p_ready = ptx::smem_addr(sh.p_ready), o_full = ptx::smem_addr(sh.o_full);
+  const u32 p_half = ptx::smem_addr(sh.p_half), p_ready = ptx::smem_addr(sh.p_ready);
+  const u32 o_full = ptx::smem_addr(sh.o_full);
   const u32 fix = ptx::smem_addr(&sh.fix), loaded = ptx::smem_addr(&sh.loaded);
   const u32 released = ptx::smem_addr(&sh.released), drain = ptx::smem_addr(&sh.drain);
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
-      ptx::mbar_init(empty + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(q_full + 8 * i, 4);
       ptx::mbar_init(s_full + 8 * i, 1);
+      ptx::mbar_init(p_half + 8 * i, 4);
       ptx::mbar_init(p_ready + 8 * i, 4);
       ptx::mbar_init(o_full + 8 * i, 1);
     }
     ptx::mbar_init(fix, 1);
     ptx::mbar_init(loaded, 1);
-    ptx::mbar_init(drain, 1);
+    ptx::mbar_init(drain, 2);
     ptx::mbar_init(released, 8);
     ptx::fence_barrier_init();
   }
@@ -213,201 +229,206 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp >= 8) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsOther));
-   if (warp == 9) {
+   if (warp == 9 || warp == 11) {
     // ----------------------------------------------------------------- loads
+    // of K (warp 9) and V (warp 11), which take turns in the ring; a lane per
+    // box.  (One lane issuing all boxes, or one warp both halves, was slower
+    // than the products: a TMA instruction takes an issuing warp 100 to 150
+    // cycles.)
+    const int half = warp == 9 ? 0 : 1;
     const int boxes = kTcKeys / p.box;
+    const int bs = a.map.block_size;
+    const CUtensorMap *map = half ? &map_v : &map_k;
     long long n_unit = 0;
-    u32 it = 0;          // tiles put into the ring
+    u32 it = half;       // position in the ring's sequence
     u32 n_fix = 0;
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x, ++n_unit) {
       const TcUnit x = finder.find(p, u);
       const int par = n_unit & 1;
-      // block ids of the tokens this part needs
       bool bad = false;
-      const int bs = a.map.block_size;
-      const int key_lo = max(x.k0 * kTcKeys, x.lo), key_hi = min(x.k1 * kTcKeys, x.hi);
-      for (int b = key_lo / bs + lane; b * static_cast<long long>(bs) < key_hi; b += 32) {
-        const int id = a.tab.block_ids[x.q.pos0 + b];
-        bad |= id < 0 || id >= a.map.num_blocks;
-      }
-      bad = __any_sync(0xffffffffu, bad);
-      if (bad && lane == 0) raise(a.tab, kStatusBadBlockId);
-      if (lane == 0) {
-        sh.any_bad[par] = bad;
-        sh.n_dirty[par] = 0;
+      if (half) {
+        bad = bad_blocks(a, x);
+        if (bad && lane == 0) raise(a.tab, kStatusBadBlockId);
+        if (lane == 0) sh.n_dirty[par] = 0;
       }
       const int at0 = x.q.at + x.row0 / a.group;
       const int at1 = x.q.at + (min(x.row0 + kTcRows, x.rows_all) - 1) / a.group;
       int n_dirty = 0;
-      for (int k = x.k0; k < x.k1 && ok; ++k) {
+      // lane b holds the block of the tile's box b, read one tile ahead
+      auto block_of = [&](int k) {
+        const int key = k * kTcKeys + lane * p.box;
+        int block = -1;
+        if (k < x.k1 && lane < boxes && key < x.q.keys) {
+          block = a.tab.block_ids[x.q.pos0 + key / bs];
+          if (block >= a.map.num_blocks) block = -1;
+        }
+        return block;
+      };
+      int ahead = block_of(x.k0);
+      for (int k = x.k0; k < x.k1 && ok; ++k, it += 2) {
         const int key0 = k * kTcKeys;
+        const int block = ahead;
+        ahead = block_of(k + 1);
+        const u32 stage = it % S::kStages;
+        const u32 dst = ring + stage * S::kTileBytes;
+        // where the box starts, in the map's groups of 8 slots
+        const int slot = (key0 + lane * p.box) % bs, sub = slot / a.map.kbs;
+        const int group = p.heads_in_groups
+                              ? (sub * a.kv_heads + x.head) * (a.map.kbs / 8) + (slot - sub * a.map.kbs) / 8
+                              : slot / 8;
+        const int column = p.heads_in_groups ? 0 : x.head * S::kHalves;
         // tiles some row sees only in part, or with slots that hold no token
         const bool partly = key0 + kTcKeys - 1 > at0 || (a.window > 0 && key0 <= at1 - a.window);
         const bool holes = key0 + kTcKeys > x.q.keys || bad;
-        // this lane's boxes of the tile (boxes of 8 slots: up to 16)
-        for (int half = 0; half < 2 && ok; ++half, ++it) {   // K, then V
-          const u32 stage = it % S::kStages;
-          if (it >= S::kStages)
-            ok = ptx::mbar_wait_bounded(empty + 8 * stage, (it / S::kStages - 1) & 1, limit);
-          if (!ok) break;
-          const u32 dst = ring + stage * S::kTileBytes;
-          const bool mend = half == 1 && (partly || holes);
-          const u32 bar = mend ? fix : full + 8 * stage;
-          int block = -1, slot = 0;
-          const int key = key0 + lane * p.box;
-          if (lane < boxes && key < x.q.keys) {
-            const int pos = key / bs;
-            slot = key - pos * bs;
-            block = a.tab.block_ids[x.q.pos0 + pos];
-            if (block >= a.map.num_blocks) block = -1;
-          }
-          const int n = __popc(__ballot_sync(0xffffffffu, block >= 0));
-          if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar, static_cast<u32>(n) * p.box * 128 * S::kHalves);
-          __syncwarp();
-          if (block >= 0) {
-            const int sub = slot / a.map.kbs;
-#pragma unroll
-            for (int h = 0; h < S::kHalves; ++h)
-              tc::tma_load(dst + h * S::kHalfBytes + lane * p.box * 128, half ? &map_v : &map_k,
-                           h * 64, slot - sub * a.map.kbs, x.head, sub, block, bar);
-          }
-          if (mend) {
-            ok = ptx::mbar_wait_bounded(fix, n_fix & 1, limit);
-            ++n_fix;
-            u32 words = 0;   // lane i < 4: the noted rows of its quarter
+        const bool mend = half == 1 && (partly || holes);
+        const u32 bar = mend ? fix : full + 8 * stage;
+        const int n = __popc(__ballot_sync(0xffffffffu, block >= 0));
+        if (it >= S::kStages) ok = tc::wait(empty + 8 * stage, (it / S::kStages - 1) & 1, limit);
+        if (!ok) break;
+        if (lane == 0)
+          ptx::mbar_arrive_expect_tx(bar, static_cast<u32>(n) * p.box * 128 * S::kHalves);
+        __syncwarp();
+        if (block >= 0)
+          tc::tma_load(dst + lane * p.box * 128 * S::kHalves, map, 0, 0, column, group, block, bar);
+        if (mend) {
+          ok = tc::wait(fix, n_fix & 1, limit);
+          ++n_fix;
+          u32 words = 0;   // lane i < 4: the noted rows of its quarter
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              const int row = i * 32 + lane, kk = key0 + row;
-              const bool has = kk >= x.lo && kk < x.hi && (!bad || good_block(a, x.q, kk));
-              bool odd = false;
-              if (has && partly) {
-                constexpr u32 kExp = kBf16 ? 0x7f80u : 0x7c00u;
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 32 + lane, kk = key0 + row;
+            const u32 at = dst + (row >> 3) * (S::kHalves * 1024) + (row & 7) * 128;
+            const bool has = kk >= x.lo && kk < x.hi && (!bad || good_block(a, x.q, kk));
+            bool odd = false;
+            if (has && partly) {
+              constexpr u32 kExp = kBf16 ? 0x7f80u : 0x7c00u;
 #pragma unroll 1
-                for (int h = 0; h < S::kHalves; ++h)
+              for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll 4
-                  for (int c = 0; c < 8; ++c) {
-                    // in an order that spreads the lanes over the banks
-                    const uint4 v = lds128(dst + h * S::kHalfBytes + row * 128 + ((c ^ (lane & 7)) << 4));
-                    const u32 w[4] = {v.x, v.y, v.z, v.w};
+                for (int c = 0; c < 8; ++c) {
+                  // in an order that spreads the lanes over the banks
+                  const uint4 v = lds128(at + h * 1024 + ((c ^ (lane & 7)) << 4));
+                  const u32 w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      odd |= (w[e] & kExp) == kExp || (w[e] >> 16 & kExp) == kExp;
-                  }
-              }
-              if (!has || odd) {
-#pragma unroll 1
-                for (int h = 0; h < S::kHalves; ++h)
-#pragma unroll 4
-                  for (int c = 0; c < 8; ++c)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                     dst + h * S::kHalfBytes + row * 128 + ((c ^ (lane & 7)) << 4)),
-                                 "r"(0)
-                                 : "memory");
-              }
-              const u32 noted = __ballot_sync(0xffffffffu, odd);
-              if (lane == i) words = noted;
-            }
-            if (__any_sync(0xffffffffu, words != 0)) {
-              if (n_dirty < kTcDirty) {
-                if (lane < 4) sh.dirty[par][n_dirty][lane] = words;
-                if (lane == 0) {
-                  sh.dirty_tile[par][n_dirty] = k;
-                  sh.n_dirty[par] = n_dirty + 1;
+                  for (int e = 0; e < 4; ++e)
+                    odd |= (w[e] & kExp) == kExp || (w[e] >> 16 & kExp) == kExp;
                 }
-              }
-              ++n_dirty;
             }
-            tc::fence_async();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(full + 8 * stage);
+            if (!has || odd) {
+#pragma unroll 1
+              for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll 4
+                for (int c = 0; c < 8; ++c)
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                   at + h * 1024 + ((c ^ (lane & 7)) << 4)),
+                               "r"(0)
+                               : "memory");
+            }
+            const u32 noted = __ballot_sync(0xffffffffu, odd);
+            if (lane == i) words = noted;
           }
+          if (__any_sync(0xffffffffu, words != 0)) {
+            if (n_dirty < kTcDirty) {
+              if (lane < 4) sh.dirty[par][n_dirty][lane] = words;
+              if (lane == 0) {
+                sh.dirty_tile[par][n_dirty] = k;
+                sh.n_dirty[par] = n_dirty + 1;
+              }
+            }
+            ++n_dirty;
+          }
+          tc::fence_async();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(full + 8 * stage);
         }
       }
-      // one unit ahead of the softmax at most: its notes are kept twice
-      if (ok && n_unit > 0) ok = ptx::mbar_wait_bounded(released, (n_unit - 1) & 1, limit);
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(loaded);
+      if (half) {
+        // one unit ahead of the softmax at most: its notes are kept twice
+        if (ok && n_unit > 0) ok = tc::wait(released, (n_unit - 1) & 1, limit);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(loaded);
+      }
     }
     // after a wait that ran out: nothing may still be on its way to this CTA
     if (!ok)
       for (u32 i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-        ptx::mbar_wait_bounded(full + 8 * (i % S::kStages), (i / S::kStages) & 1, limit);
-   } else if (warp == 8) {
+        tc::wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, limit);
+   } else if (warp == 8 || warp == 10) {
     // -------------------------------------------------------------- products
+    // one issuing thread per query tile: while one waits for its weights, the
+    // other's products run
     constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
     constexpr u32 kDescO = tc::instr_desc(kBf16, 128, kDim, true);
-    u32 it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-    auto scores = [&](int i, u32 stage) {
-      const u32 q = q_smem + i * S::kTileBytes, k = ring + stage * S::kTileBytes;
-#pragma unroll
-      for (int s = 0; s < kDim / 16; ++s) {
-        const u32 off = (s >> 2) * S::kHalfBytes + (s & 3) * 32;
-        tc::mma_ss(tmem + i * 128, tc::smem_desc(q + off, 16, 1024), tc::smem_desc(k + off, 16, 1024),
-                   kDescS, s > 0);
+    const int i = warp == 8 ? 0 : 1;
+    const u32 ts = tmem + i * 128, to = tmem + 256 + i * 128;
+    const u32 q_low = tc::desc_low(q_smem + i * S::kTileBytes, 16);
+    const u32 k_low = tc::desc_low(ring, 16), v_low = tc::desc_low(ring, 1024);
+    u32 stage = 0, turn = 0, n_q = 0, n_p = 0;   // ring position and its phase
+    auto next_stage = [&]() {
+      if (++stage == S::kStages) {
+        stage = 0;
+        turn ^= 1;
       }
-    };
-    auto values = [&](int i, u32 stage, bool add) {
-      const u32 v = ring + stage * S::kTileBytes;
-#pragma unroll
-      for (int s = 0; s < kTcKeys / 16; ++s)
-        tc::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8,
-                   tc::smem_desc(v + s * 2048, S::kHalfBytes, 1024), kDescO, add || s > 0);
     };
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TcUnit x = finder.find(p, u);
-      if (lane == 0) {
-        u32 k_stage = it % S::kStages;
-        for (int k = x.k0; k <= x.k1 && ok; ++k) {
-          // at k: S of tile k and O of tile k - 1
-          if (x.k0 == x.k1) break;
-          const bool do_s = k < x.k1, do_o = k > x.k0;
-          // ring order: K0 V0 K1 V1 ...; V of tile k - 1 precedes K of tile k
-          u32 v_stage = 0;
-          if (do_o) {
-            v_stage = it % S::kStages;
-            ok = ptx::mbar_wait_bounded(full + 8 * v_stage, (it / S::kStages) & 1, limit);
+      if (lane == 0 && i >= x.tiles) {
+        // nothing to do for this tile but to let the ring go on
+        for (int n = 0; n < 2 * (x.k1 - x.k0) && ok; ++n, next_stage()) {
+          ok = tc::wait(full + 8 * stage, turn, limit);
+          if (ok) ptx::mbar_arrive(empty + 8 * stage);
+        }
+      } else if (lane == 0) {
+        // at k: O of token tile k - 1 (ring: K0 V0 K1 V1 ...), then S of tile k;
+        // half of the weights at a time: the second half is made while the
+        // first half's products run
+        for (int k = x.k0; k < x.k1 + (x.k1 > x.k0 ? 1 : 0); ++k) {
+          if (k > x.k0) {
+            ok = tc::wait(full + 8 * stage, turn, limit) && tc::wait(p_half + 8 * i, n_p & 1, limit);
             if (!ok) break;
-            ++it;
+            tc::fence_after();
+            const u32 v = v_low + stage * (S::kTileBytes >> 4);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)), kDescO,
+                         k - 1 > x.k0 || s > 0);
+            ok = tc::wait(p_ready + 8 * i, n_p & 1, limit);
+            if (!ok) break;
+            ++n_p;
+            tc::fence_after();
+#pragma unroll
+            for (int s = 4; s < 8; ++s)
+              tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)), kDescO, true);
+            tc::commit(empty + 8 * stage);
+            next_stage();
+            if (k == x.k1) tc::commit(o_full + 8 * i);
           }
-          bool have_k = false;
-          for (int i = 0; i < x.tiles && ok; ++i) {
-            if (do_o) {
-              ok = ptx::mbar_wait_bounded(p_ready + 8 * i, n_p[i] & 1, limit);
-              if (!ok) break;
-              ++n_p[i];
-              tc::fence_after();
-              values(i, v_stage, k - 1 > x.k0);
-              if (i == x.tiles - 1) tc::commit(empty + 8 * v_stage);
-              if (!do_s) tc::commit(o_full + 8 * i);
+          if (k < x.k1) {
+            ok = tc::wait(full + 8 * stage, turn, limit);
+            if (ok && k == x.k0) {
+              ok = tc::wait(q_full + 8 * i, n_q & 1, limit);
+              ++n_q;
             }
-            if (do_s) {
-              if (!have_k) {
-                k_stage = it % S::kStages;
-                ok = ptx::mbar_wait_bounded(full + 8 * k_stage, (it / S::kStages) & 1, limit);
-                if (!ok) break;
-                ++it;
-                have_k = true;
-              }
-              if (k == x.k0) {
-                ok = ptx::mbar_wait_bounded(q_full + 8 * i, n_q[i] & 1, limit);
-                if (!ok) break;
-                ++n_q[i];
-              }
-              tc::fence_after();
-              scores(i, k_stage);
-              tc::commit(s_full + 8 * i);
-              if (i == x.tiles - 1) tc::commit(empty + 8 * k_stage);
+            if (!ok) break;
+            tc::fence_after();
+            const u32 kk = k_low + stage * (S::kTileBytes >> 4);
+#pragma unroll
+            for (int s = 0; s < kDim / 16; ++s) {
+              tc::mma_ss(ts, tc::desc<1024>(q_low + (((s >> 2) * S::kHalfBytes + (s & 3) * 32) >> 4)),
+                         tc::desc<S::kHalves * 1024>(kk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4)),
+                         kDescS, s > 0);
             }
+            tc::commit(s_full + 8 * i);
+            tc::commit(empty + 8 * stage);
+            next_stage();
           }
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      it = __shfl_sync(0xffffffffu, it, 0);
     }
     if (!ok && lane == 0) {   // let the products issued so far end
       tc::commit(drain);
-      ptx::mbar_wait_bounded(drain, 0, limit);
+      tc::wait(drain, 0, limit);
     }
    }
   } else {
@@ -451,13 +472,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::fence_async();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(q_full + 8 * i);
+        const bool bad = bad_blocks(a, x);
         // what the warp's rows all see, and what none of them sees
         const int row_first = min(x.row0 + i * 128 + (warp & 3) * 32, x.rows_all - 1);
         const int row_last = min(row_first + 31, x.rows_all - 1);
         const int at_min = x.q.at + row_first / a.group, at_max = x.q.at + row_last / a.group;
         const int upto = min(at, x.q.keys - 1);
         for (int k = x.k0; k < x.k1; ++k) {
-          ok = ptx::mbar_wait_bounded(s_full + 8 * i, n_s & 1, limit);
+          ok = tc::wait(s_full + 8 * i, n_s & 1, limit);
           if (__any_sync(0xffffffffu, !ok)) {
             ok = false;
             break;
@@ -474,31 +496,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // scores = sc * s; capped ones, and those of a scale that would turn
           // the maximum round or make 0 of a masked score, are made first
           float sc = a.scale;
-          if (a.cap != 0.0f || a.scale <= 0.0f) {
+          if constexpr (!kPlain) {
             sc = 1.0f;
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               s[c] = __float_as_uint(score_of(a, __uint_as_float(s[c]), 1.0f));
           }
-          if (key0 + kTcKeys - 1 > min(at_min, x.q.keys - 1) ||
-              (a.window > 0 && key0 <= at_max - a.window)) {
+          if (__builtin_expect(key0 + kTcKeys - 1 > min(at_min, x.q.keys - 1) ||
+                                   (a.window > 0 && key0 <= at_max - a.window) || bad,
+                               0)) {
             const int hi = upto - key0, lo = a.window > 0 ? at - a.window + 1 - key0 : 0;
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > hi || c < lo) s[c] = 0xff800000u;
-          }
-          if (sh.any_bad[par]) {
+            for (int w = 0; w < 4; ++w) {
+              // bit c: the row sees token 32 w + c
+              const int n1 = min(max(hi + 1 - 32 * w, 0), 32), n0 = min(max(lo - 32 * w, 0), 32);
+              u32 see = (n1 == 32 ? 0xffffffffu : (1u << n1) - 1u) &
+                        ~(n0 == 32 ? 0xffffffffu : (1u << n0) - 1u);
+              if (bad) {
+#pragma unroll 1
+                for (int c = 0; c < 32; ++c)
+                  if (see >> c & 1u && !good_block(a, x.q, key0 + 32 * w + c)) see &= ~(1u << c);
+              }
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (key0 + c < x.q.keys && !good_block(a, x.q, key0 + c)) s[c] = 0xff800000u;
+              for (int c = 0; c < 32; ++c)
+                if (!(see >> c & 1u)) s[32 * w + c] = 0xff800000u;
+            }
           }
           float m0 = kNegInf, m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            m0 = fmaxf(m0, __uint_as_float(s[c]));
-            m1 = fmaxf(m1, __uint_as_float(s[c + 1]));
-            m2 = fmaxf(m2, __uint_as_float(s[c + 2]));
-            m3 = fmaxf(m3, __uint_as_float(s[c + 3]));
+          for (int c = 0; c < 128; c += 8) {
+            m0 = tc::max3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            m1 = tc::max3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+            m2 = tc::max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+            m3 = tc::max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
           }
           const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
           const bool raise_m = mx > m + kTcSlack || (m == kNegInf && mx != kNegInf);
@@ -527,36 +557,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const float base = m == kNegInf ? 0.0f : -m;
           const u64 sc2 = tc::pair(sc, sc), base2 = tc::pair(base, base);
-          u64 sum0 = 0, sum1 = 0;   // pairs of +0
 #pragma unroll
           for (int c = 0; c < 128; c += 32) {
             u32 w[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float y[4];
+            for (int e = 0; e < 32; e += 2) {
+              float y0, y1;
               tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])),
-                                  sc2, base2), y[0], y[1]);
-              tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c + e + 2]),
-                                           __uint_as_float(s[c + e + 3])), sc2, base2), y[2], y[3]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
-              sum0 = tc::add2(sum0, tc::pair(y[0], y[1]));
-              sum1 = tc::add2(sum1, tc::pair(y[2], y[3]));
-              w[e / 2] = pack2<kBf16>(y[0], y[1]);
-              w[e / 2 + 1] = pack2<kBf16>(y[2], y[3]);
+                                  sc2, base2), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              s[c + e] = __float_as_uint(y0);
+              s[c + e + 1] = __float_as_uint(y1);
+              w[e / 2] = pack2<kBf16>(y0, y1);
             }
             tc::st16(ts + c / 2, w);
+            if (c == 32 || c == 96) {
+              tc::wait_st();
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive((c == 32 ? p_half : p_ready) + 8 * i);
+            }
           }
-          tc::wait_st();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(p_ready + 8 * i);
+          // the row sum is off the products' path
+          u64 sum[4] = {0, 0, 0, 0};   // pairs of +0
+#pragma unroll
+          for (int c = 0; c < 128; c += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sum[j] = tc::add2(sum[j], tc::pair(__uint_as_float(s[c + 2 * j]),
+                                                 __uint_as_float(s[c + 2 * j + 1])));
           float x0, x1;
-          tc::unpair(tc::add2(sum0, sum1), x0, x1);
+          tc::unpair(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), x0, x1);
           l += x0 + x1;
         }
         if (ok) {
-          const bool done = ptx::mbar_wait_bounded(o_full + 8 * i, n_o & 1, limit);
+          const bool done = tc::wait(o_full + 8 * i, n_o & 1, limit);
           ok = !__any_sync(0xffffffffu, !done);
           ++n_o;
           tc::fence_after();
@@ -564,7 +600,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!ok) break;
       // all loads of the unit are noted before this
-      const bool noted = ptx::mbar_wait_bounded(loaded, n_unit & 1, limit);
+      const bool noted = tc::wait(loaded, n_unit & 1, limit);
       ok = !__any_sync(0xffffffffu, !noted);
       if (!ok) break;
       const int n_dirty = sh.n_dirty[par];

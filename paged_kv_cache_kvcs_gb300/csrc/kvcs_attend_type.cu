@@ -41,13 +41,13 @@ struct TypeLaunch {
     return cudaLaunchKernelEx(&cfg, kvcs_attend_kernel<kType, kDim, kWide>, p);
   }
 
-  template <int kDim>
+  template <int kDim, bool kPlain>
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
                                int grid, bool after_zero, cudaStream_t st) {
     if constexpr (kType == kKvFp8) {
       return cudaErrorNotSupported;
     } else {
-      auto kernel = kvcs_attend_tc_kernel<kType == kKvBf16, kDim>;
+      auto kernel = kvcs_attend_tc_kernel<kType == kKvBf16, kDim, kPlain>;
       constexpr int smem = TcShape<kDim>::kSmemBytes;
       const cudaError_t e = cudaFuncSetAttribute(
           reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -103,8 +103,10 @@ template <>
 cudaError_t AttendLaunch<kThisType>::attend_tc(const TcParams &p, const CUtensorMap &k,
                                                const CUtensorMap &v, int grid, bool after_zero,
                                                cudaStream_t st) {
-  return p.a.head_dim == 64 ? This::attend_tc<64>(p, k, v, grid, after_zero, st)
-                            : This::attend_tc<128>(p, k, v, grid, after_zero, st);
+  const bool plain = p.a.cap == 0.0f && p.a.scale > 0.0f;
+  auto run = p.a.head_dim == 64 ? (plain ? &This::attend_tc<64, true> : &This::attend_tc<64, false>)
+                                : (plain ? &This::attend_tc<128, true> : &This::attend_tc<128, false>);
+  return run(p, k, v, grid, after_zero, st);
 }
 
 template <>

@@ -41,13 +41,21 @@ __device__ __forceinline__ void commit(u32 bar) {
       : "memory");
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle.  K-major operands: rows
-// of 128 bytes, 8-row groups `sbo` bytes apart.  MN-major operands: 64
-// contiguous elements along M or N, blocks of 64 `lbo` apart, 8-deep groups
-// along K `sbo` apart.
-__device__ __forceinline__ u64 smem_desc(u32 addr, u32 lbo, u32 sbo) {
-  return static_cast<u64>((addr & 0x3ffffu) >> 4) | static_cast<u64>(lbo >> 4) << 16 |
-         static_cast<u64>(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// Shared-memory matrix descriptors, 128-byte swizzle.  K-major operands: rows
+// of 128 bytes, 8-row groups `group` bytes apart (`lbo` unused).  MN-major
+// operands: 64 contiguous elements along M or N, blocks of 64 `lbo` bytes
+// apart, 8-deep groups along K `group` apart.  Moving the operand by n bytes
+// adds n / 16 to the low word (the products' issue rate hangs on how little
+// is computed between two of them).
+__host__ __device__ constexpr u32 desc_high(u32 group) { return group >> 4 | 1u << 14 | 2u << 29; }
+__device__ __forceinline__ u32 desc_low(u32 addr, u32 lbo) {
+  return (addr & 0x3ffffu) >> 4 | (lbo >> 4) << 16;
+}
+template <u32 kGroup>
+__device__ __forceinline__ u64 desc(u32 low) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(low), "r"(desc_high(kGroup)));
+  return r;
 }
 
 // Instruction descriptor of kind::f16 with 32-bit accumulators.
@@ -77,6 +85,25 @@ __device__ __forceinline__ void mma_ts(u32 d, u32 a, u64 b, u32 idesc, bool add)
                       "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
 #define KVCS_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), \
                       "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// As ptx::mbar_wait_bounded, without a look at the global timer (a read of
+// about a microsecond) before 1024 probes have failed: the waits of a
+// product pipeline are shorter than that, and on its critical path.
+// The first probe stands apart: one that succeeds costs about 15 cycles, the
+// loop's bookkeeping about 100 more.
+__device__ __forceinline__ bool wait(u32 bar, u32 parity, u64 limit_ns) {
+  if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
+  u64 t0 = 0;
+  for (u32 i = 0; i < (1u << 28); ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 1023u) {
+      const u64 now = ptx::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) return false;
+    }
+  }
+  return false;
+}
 
 // 32 columns of this warp's 32 lanes.
 __device__ __forceinline__ void ld32(u32 addr, u32 *v) {
@@ -136,6 +163,11 @@ __device__ __forceinline__ void unpair(u64 v, float &a, float &b) {
 __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   u64 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ u64 add2(u64 a, u64 b) {
