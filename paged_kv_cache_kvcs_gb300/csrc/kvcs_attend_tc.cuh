@@ -10,12 +10,12 @@
 // 128 tokens.  Roles of the CTA's warps:
 //   warps 9, 11  load K and V tiles page by page with TMA (boxes of as many
 //              slots as a page holds in a row, 128-byte swizzle) into a ring;
-//   warps 8, 10  issue the products of one query tile each: S_i = Q_i K^T into
-//              tensor memory, then O_i += P_i V with P_i from tensor memory;
+//   warp 8     issues the products: S_i = Q_i K^T into tensor memory, then
+//              O_i += P_i V with P_i from tensor memory;
 //   warps 0-3, warps 4-7   the softmax of one query tile each, a thread per
 //              row: S from tensor memory, weights back over S as 16-bit P.
 // The two tiles take turns: while one tile's weights are made, the other
-// tile's products run.  One thread's products run in issue order, so P_i is read
+// tile's products run.  One warp's products run in issue order, so P_i is read
 // before S_i of the next token tile overwrites it, and the signal that S_i is
 // ready also says that O_i's last addition is done.
 //
@@ -140,6 +140,7 @@ struct TcFinder {
 struct TcShared {
   u64 full[10], empty[10];
   u64 q_full[2], s_full[2], p_half[2], p_ready[2], o_full[2];
+  u64 turns[2];                    // the products' warps hand each other the turn
   u64 fix, loaded, released, drain;
   u32 tmem;
   int n_dirty[2];                  // noted tiles, by parity of the unit
@@ -183,13 +184,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const u32 full = ptx::smem_addr(sh.full), empty = ptx::smem_addr(sh.empty);
   const u32 q_full = ptx::smem_addr(sh.q_full), s_full = ptx::smem_addr(sh.s_full);
   const u32 p_half = ptx::smem_addr(sh.p_half), p_ready = ptx::smem_addr(sh.p_ready);
+  const u32 turns = ptx::smem_addr(sh.turns);
   const u32 o_full = ptx::smem_addr(sh.o_full);
   const u32 fix = ptx::smem_addr(&sh.fix), loaded = ptx::smem_addr(&sh.loaded);
   const u32 released = ptx::smem_addr(&sh.released), drain = ptx::smem_addr(&sh.drain);
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
-      ptx::mbar_init(empty + 8 * i, 2);
+      ptx::mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(q_full + 8 * i, 4);
@@ -197,6 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ptx::mbar_init(p_half + 8 * i, 4);
       ptx::mbar_init(p_ready + 8 * i, 4);
       ptx::mbar_init(o_full + 8 * i, 1);
+      ptx::mbar_init(turns + 8 * i, 1);
     }
     ptx::mbar_init(fix, 1);
     ptx::mbar_init(loaded, 1);
@@ -353,17 +356,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (!ok)
       for (u32 i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
         tc::wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, limit);
-   } else if (warp == 8 || warp == 10) {
+   } else {
     // -------------------------------------------------------------- products
-    // one issuing thread per query tile: while one waits for its weights, the
-    // other's products run
+    // A warp per query tile.  They take turns, each with O of token tile
+    // k - 1 and then S of tile k in one go, so that the tiles settle half a
+    // turn apart: one's products run while the other's weights are made, and
+    // one warp's waits pass while the other's products run.  (Without turns
+    // the two share the tensor cores product by product, which keeps both in
+    // step and both waiting: 863 us.  One warp for both tiles shows its waits,
+    // 721 us.)  A warp stays together and one lane issues: with the waits
+    // inside a one-lane branch the whole took 822 us.
     constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
     constexpr u32 kDescO = tc::instr_desc(kBf16, 128, kDim, true);
     const int i = warp == 8 ? 0 : 1;
     const u32 ts = tmem + i * 128, to = tmem + 256 + i * 128;
     const u32 q_low = tc::desc_low(q_smem + i * S::kTileBytes, 16);
     const u32 k_low = tc::desc_low(ring, 16), v_low = tc::desc_low(ring, 1024);
-    u32 stage = 0, turn = 0, n_q = 0, n_p = 0;   // ring position and its phase
+    u32 stage = 0, turn = 0, n_q = 0, n_p = 0, n_t = 0;   // stage: ring position, turn: its phase
     auto next_stage = [&]() {
       if (++stage == S::kStages) {
         stage = 0;
@@ -372,62 +381,71 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TcUnit x = finder.find(p, u);
-      if (lane == 0 && i >= x.tiles) {
-        // nothing to do for this tile but to let the ring go on
-        for (int n = 0; n < 2 * (x.k1 - x.k0) && ok; ++n, next_stage()) {
+      if (i >= x.tiles) {   // the ring goes on without this warp
+        for (int n = 0; n < 2 * (x.k1 - x.k0); ++n) next_stage();
+        continue;
+      }
+      const bool last = i == x.tiles - 1, pair = x.tiles == 2;
+      // ring: K0 V0 K1 V1 ...; V of tile k - 1 comes before K of tile k.
+      for (int k = x.k0; k < x.k1 + (x.k1 > x.k0 ? 1 : 0) && ok; ++k) {
+        const bool do_o = k > x.k0, do_s = k < x.k1;
+        const u32 v_stage = stage;
+        if (do_o) {
           ok = tc::wait(full + 8 * stage, turn, limit);
-          if (ok) ptx::mbar_arrive(empty + 8 * stage);
+          next_stage();
         }
-      } else if (lane == 0) {
-        // at k: O of token tile k - 1 (ring: K0 V0 K1 V1 ...), then S of tile k;
-        // half of the weights at a time: the second half is made while the
-        // first half's products run
-        for (int k = x.k0; k < x.k1 + (x.k1 > x.k0 ? 1 : 0); ++k) {
-          if (k > x.k0) {
-            ok = tc::wait(full + 8 * stage, turn, limit) && tc::wait(p_half + 8 * i, n_p & 1, limit);
-            if (!ok) break;
-            tc::fence_after();
-            const u32 v = v_low + stage * (S::kTileBytes >> 4);
+        const u32 k_stage = stage;
+        if (do_s) {
+          ok = ok && tc::wait(full + 8 * stage, turn, limit);
+          next_stage();
+          if (k == x.k0) ok = ok && tc::wait(q_full + 8 * i, n_q++ & 1, limit);
+        }
+        if (do_o) ok = ok && tc::wait(p_half + 8 * i, n_p & 1, limit);
+        if (pair && (i == 1 || k > x.k0)) ok = ok && tc::wait(turns + 8 * i, n_t++ & 1, limit);
+        if (!ok) break;
+        tc::fence_after();
+        if (do_o) {
+          // half of the weights at a time: the second half is made while the
+          // first half's products run
+          const u32 v = v_low + v_stage * (S::kTileBytes >> 4);
+          if (tc::elect()) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)), kDescO,
-                         k - 1 > x.k0 || s > 0);
-            ok = tc::wait(p_ready + 8 * i, n_p & 1, limit);
-            if (!ok) break;
-            ++n_p;
-            tc::fence_after();
+              tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)),
+                         kDescO, k - 1 > x.k0 || s > 0);
+          }
+          __syncwarp();
+          ok = tc::wait(p_ready + 8 * i, n_p++ & 1, limit);
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect()) {
 #pragma unroll
             for (int s = 4; s < 8; ++s)
-              tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)), kDescO, true);
-            tc::commit(empty + 8 * stage);
-            next_stage();
-            if (k == x.k1) tc::commit(o_full + 8 * i);
+              tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)),
+                         kDescO, true);
+            if (!do_s) tc::commit(o_full + 8 * i);
+            if (last) tc::commit(empty + 8 * v_stage);
           }
-          if (k < x.k1) {
-            ok = tc::wait(full + 8 * stage, turn, limit);
-            if (ok && k == x.k0) {
-              ok = tc::wait(q_full + 8 * i, n_q & 1, limit);
-              ++n_q;
-            }
-            if (!ok) break;
-            tc::fence_after();
-            const u32 kk = k_low + stage * (S::kTileBytes >> 4);
+          __syncwarp();
+        }
+        if (tc::elect()) {
+          if (do_s) {
+            const u32 kk = k_low + k_stage * (S::kTileBytes >> 4);
 #pragma unroll
-            for (int s = 0; s < kDim / 16; ++s) {
+            for (int s = 0; s < kDim / 16; ++s)
               tc::mma_ss(ts, tc::desc<1024>(q_low + (((s >> 2) * S::kHalfBytes + (s & 3) * 32) >> 4)),
                          tc::desc<S::kHalves * 1024>(kk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4)),
                          kDescS, s > 0);
-            }
             tc::commit(s_full + 8 * i);
-            tc::commit(empty + 8 * stage);
-            next_stage();
+            if (last) tc::commit(empty + 8 * k_stage);
           }
+          if (pair && (i == 0 || do_s)) ptx::mbar_arrive(turns + 8 * (1 - i));
         }
+        __syncwarp();
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     }
-    if (!ok && lane == 0) {   // let the products issued so far end
-      tc::commit(drain);
+    if (!ok) {   // let the products issued so far end
+      if (lane == 0) tc::commit(drain);
       tc::wait(drain, 0, limit);
     }
    }
@@ -480,10 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int upto = min(at, x.q.keys - 1);
         for (int k = x.k0; k < x.k1; ++k) {
           ok = tc::wait(s_full + 8 * i, n_s & 1, limit);
-          if (__any_sync(0xffffffffu, !ok)) {
-            ok = false;
-            break;
-          }
+          if (!ok) break;
           ++n_s;
           tc::fence_after();
           const int key0 = k * kTcKeys;
@@ -592,16 +607,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l += x0 + x1;
         }
         if (ok) {
-          const bool done = tc::wait(o_full + 8 * i, n_o & 1, limit);
-          ok = !__any_sync(0xffffffffu, !done);
+          ok = tc::wait(o_full + 8 * i, n_o & 1, limit);
           ++n_o;
           tc::fence_after();
         }
       }
       if (!ok) break;
       // all loads of the unit are noted before this
-      const bool noted = tc::wait(loaded, n_unit & 1, limit);
-      ok = !__any_sync(0xffffffffu, !noted);
+      ok = tc::wait(loaded, n_unit & 1, limit);
       if (!ok) break;
       const int n_dirty = sh.n_dirty[par];
       const bool whole = p.splits == 1;

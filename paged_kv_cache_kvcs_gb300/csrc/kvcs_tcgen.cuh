@@ -34,6 +34,15 @@ __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  u32 r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Arrives on `bar` once every product this thread issued before is done.
 __device__ __forceinline__ void commit(u32 bar) {
   asm volatile(
@@ -90,7 +99,9 @@ __device__ __forceinline__ void mma_ts(u32 d, u32 a, u64 b, u32 idesc, bool add)
 // about a microsecond) before 1024 probes have failed: the waits of a
 // product pipeline are shorter than that, and on its critical path.
 // The first probe stands apart: one that succeeds costs about 15 cycles, the
-// loop's bookkeeping about 100 more.
+// loop's bookkeeping about 100 more.  A warp calls it converged: its lanes
+// probe with one instruction and read one clock, and so get one answer (a
+// vote on it cost 3 to 9% of a product pipeline's time).
 __device__ __forceinline__ bool wait(u32 bar, u32 parity, u64 limit_ns) {
   if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
   u64 t0 = 0;
@@ -104,7 +115,6 @@ __device__ __forceinline__ bool wait(u32 bar, u32 parity, u64 limit_ns) {
   }
   return false;
 }
-
 // 32 columns of this warp's 32 lanes.
 __device__ __forceinline__ void ld32(u32 addr, u32 *v) {
   asm volatile(
