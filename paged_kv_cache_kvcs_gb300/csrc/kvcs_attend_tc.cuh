@@ -537,17 +537,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!(see >> c & 1u)) s[32 * w + c] = 0xff800000u;
             }
           }
-          float m0 = kNegInf, m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
+          // The first half's weights are made with the maximum of the tiles
+          // before while this tile's is found (it would stand in the way of
+          // both halves otherwise); only where a row passes it are they made
+          // again.
+          const u64 sc2 = tc::pair(sc, sc);
+          u32 w[32];
+          u64 sum0, sum1, base2;
+#pragma unroll 1
+          for (bool first = true;; first = false) {
+            const float base = m == kNegInf ? 0.0f : -m;
+            base2 = tc::pair(base, base);
+            sum0 = sum1 = 0;   // pairs of +0
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            m0 = tc::max3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            m1 = tc::max3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-            m2 = tc::max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-            m3 = tc::max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-          }
-          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
-          const bool raise_m = mx > m + kTcSlack || (m == kNegInf && mx != kNegInf);
-          if (__any_sync(0xffffffffu, raise_m)) {
+            for (int c = 0; c < 64; c += 4) {
+              float y[4];
+              tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2,
+                                  base2), y[0], y[1]);
+              tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc2,
+                                  base2), y[2], y[3]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = ex2(y[j]);
+              sum0 = tc::add2(sum0, tc::pair(y[0], y[1]));
+              sum1 = tc::add2(sum1, tc::pair(y[2], y[3]));
+              w[c / 2] = pack2<kBf16>(y[0], y[1]);
+              w[c / 2 + 1] = pack2<kBf16>(y[2], y[3]);
+            }
+            if (!first) break;
+            float m0 = kNegInf, m1 = kNegInf, m2 = kNegInf, m3 = kNegInf;
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+              m0 = tc::max3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              m1 = tc::max3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+              m2 = tc::max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+              m3 = tc::max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+            }
+            const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
+            const bool raise_m = mx > m + kTcSlack || (m == kNegInf && mx != kNegInf);
+            if (!__any_sync(0xffffffffu, raise_m)) break;
             const float f = raise_m ? (m == kNegInf ? 0.0f : ex2(m - mx)) : 1.0f;
             if (raise_m) m = mx;
             l *= f;
@@ -570,40 +597,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          const float base = m == kNegInf ? 0.0f : -m;
-          const u64 sc2 = tc::pair(sc, sc), base2 = tc::pair(base, base);
+          tc::st32(ts, w);
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(p_half + 8 * i);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            u32 w[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float y0, y1;
-              tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])),
-                                  sc2, base2), y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              s[c + e] = __float_as_uint(y0);
-              s[c + e + 1] = __float_as_uint(y1);
-              w[e / 2] = pack2<kBf16>(y0, y1);
-            }
-            tc::st16(ts + c / 2, w);
-            if (c == 32 || c == 96) {
-              tc::wait_st();
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive((c == 32 ? p_half : p_ready) + 8 * i);
-            }
+          for (int c = 64; c < 128; c += 2) {
+            float y0, y1;
+            tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, base2),
+                       y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            s[c] = __float_as_uint(y0);
+            s[c + 1] = __float_as_uint(y1);
+            w[c / 2 - 32] = pack2<kBf16>(y0, y1);
           }
-          // the row sum is off the products' path
-          u64 sum[4] = {0, 0, 0, 0};   // pairs of +0
+          tc::st32(ts + 32, w);
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(p_ready + 8 * i);
+          // this half's sum is off the products' path
 #pragma unroll
-          for (int c = 0; c < 128; c += 8)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              sum[j] = tc::add2(sum[j], tc::pair(__uint_as_float(s[c + 2 * j]),
-                                                 __uint_as_float(s[c + 2 * j + 1])));
+          for (int c = 64; c < 128; c += 4) {
+            sum0 = tc::add2(sum0, tc::pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+            sum1 = tc::add2(sum1, tc::pair(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
+          }
           float x0, x1;
-          tc::unpair(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), x0, x1);
+          tc::unpair(tc::add2(sum0, sum1), x0, x1);
           l += x0 + x1;
         }
         if (ok) {
