@@ -202,6 +202,27 @@ bool half_map(CUtensorMap *map, const PageMap &m, int half, int heads, int dim, 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries of one call as a tensor [half][token][head][64 elements], read in
+// boxes of one KV head's query group by `tokens` new tokens.
+bool query_map(CUtensorMap *map, const AttnParams &p, bool bf16, int tokens) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const int halves = p.head_dim / 64;
+  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(p.kv_heads) * p.group,
+                              static_cast<cuuint64_t>(p.tab.total_new),
+                              static_cast<cuuint64_t>(halves), 1};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(p.head_dim) * 2,
+                                 static_cast<cuuint64_t>(p.q_stride) * 2, 128,
+                                 static_cast<cuuint64_t>(p.q_stride) * 2};
+  const cuuint32_t boxes[5] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(tokens),
+                               1, 1};
+  const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                const_cast<void *>(p.q), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The launches of one attention call.  A request's rows are its new tokens
 // times the query heads per KV head: up to 16 rows go to the narrow kernel,
 // more to the tensor-memory kernel, or to the wide one where that does not
@@ -212,6 +233,7 @@ bool half_map(CUtensorMap *map, const PageMap &m, int half, int heads, int dim, 
 constexpr int kNarrowRows = 16;
 constexpr int kWideRows = 64;
 constexpr int kTcMaxSplits = 16;
+constexpr int kMassRows = 32;    // observed rows the small mass kernel takes, at most
 constexpr int kTcMinTiles = 4;   // token tiles a part holds, at least (on average)
 
 struct AttendPlan {
@@ -382,11 +404,42 @@ int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_
   if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
   AttnParams p = attn_params(cache, block_size, reqs, total_positions, att, status);
   p.mass = mass;
-  auto run = att->kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::mass
-             : att->kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::mass
-                                                : &AttendLaunch<kKvFp8>::mass;
-  if (run(p, 4 * sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVCS_ECUDA;
-  count_launches(1);
+  // rows a request has observed: few go to the small kernel, more to the
+  // tensor-memory one, as in the attention
+  long long observed = p.tab.max_new;
+  if (p.observe > 0) observed = std::min<long long>(observed, p.observe);
+  const long long rows = observed * p.group;
+  const bool tc = rows > kMassRows && p.group <= 128 && tc_takes(*cache, block_size, *att) &&
+                  p.q_stride * 2 < (1ll << 40);
+  const bool alike = p.tab.total_new == p.tab.num_requests * p.tab.max_new;
+  const bool small = !tc || (!alike && p.group <= kMassRows);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (small) {
+    p.row_hi = tc ? kMassRows : 0x7fffffff;
+    auto run = att->kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::mass
+               : att->kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::mass
+                                                  : &AttendLaunch<kKvFp8>::mass;
+    if (run(p, 4 * sms, st) != cudaSuccess) return KVCS_ECUDA;
+  }
+  if (tc) {
+    MtParams t;
+    std::memset(&t, 0, sizeof(t));
+    t.a = p;
+    t.a.row_lo = small ? kMassRows + 1 : 1;
+    t.a.row_hi = 0x7fffffff;
+    t.box = tc_box(*cache, block_size);
+    t.heads_in_groups = cache->layout == KVCS_LAYOUT_HND;
+    t.tile_tokens = 128 / p.group;
+    t.timeout_ns = kAttendTimeoutNs;
+    const bool bf16 = att->kv_dtype == KVCS_DTYPE_BF16;
+    CUtensorMap mk, mq;
+    if (!half_map(&mk, p.map, 0, p.kv_heads, p.head_dim, bf16, t.box, t.heads_in_groups != 0) ||
+        !query_map(&mq, p, bf16, t.tile_tokens))
+      return KVCS_ECUDA;
+    auto run = bf16 ? &AttendLaunch<kKvBf16>::mass_tc : &AttendLaunch<kKvFp16>::mass_tc;
+    if (run(t, mk, mq, sms, st) != cudaSuccess) return KVCS_ECUDA;
+  }
+  count_launches((small ? 1 : 0) + (tc ? 1 : 0));
   return KVCS_OK;
 }
 

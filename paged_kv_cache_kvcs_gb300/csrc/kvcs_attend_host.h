@@ -6,7 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "kvcs.h"
-#include "kvcs_attend_tc.cuh"
+#include "kvcs_mass_tc.cuh"
 
 namespace kvcs {
 
@@ -26,6 +26,8 @@ struct AttendLaunch {
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
                                int grid, bool after_zero, cudaStream_t st);
   static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st);
+  static cudaError_t mass_tc(const MtParams &p, const CUtensorMap &k, const CUtensorMap &q, int grid,
+                             cudaStream_t st);
 };
 
 }  // namespace kvcs

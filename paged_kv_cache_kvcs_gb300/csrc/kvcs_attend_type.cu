@@ -2,7 +2,6 @@
 // cache type (KVCS_KV_TYPE), compiled once per type.
 
 #include "kvcs_attend_host.h"
-#include "kvcs_mass.cuh"
 
 namespace kvcs {
 
@@ -71,6 +70,22 @@ struct TypeLaunch {
     kvcs_mass_kernel<kType, kDim><<<static_cast<unsigned>(grid), kMassThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
+
+  template <int kDim, bool kPlain>
+  static cudaError_t mass_tc(const MtParams &p, const CUtensorMap &k, const CUtensorMap &q, int grid,
+                             cudaStream_t st) {
+    if constexpr (kType == kKvFp8) {
+      return cudaErrorNotSupported;
+    } else {
+      auto kernel = kvcs_mass_tc_kernel<kType == kKvBf16, kDim, kPlain>;
+      constexpr int smem = MtShape<kDim>::kSmemBytes;
+      const cudaError_t e = cudaFuncSetAttribute(
+          reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      kernel<<<static_cast<unsigned>(grid), kTcThreads, smem, st>>>(p, k, q);
+      return cudaGetLastError();
+    }
+  }
 };
 
 using This = TypeLaunch<kThisType>;
@@ -107,6 +122,15 @@ cudaError_t AttendLaunch<kThisType>::attend_tc(const TcParams &p, const CUtensor
   auto run = p.a.head_dim == 64 ? (plain ? &This::attend_tc<64, true> : &This::attend_tc<64, false>)
                                 : (plain ? &This::attend_tc<128, true> : &This::attend_tc<128, false>);
   return run(p, k, v, grid, after_zero, st);
+}
+
+template <>
+cudaError_t AttendLaunch<kThisType>::mass_tc(const MtParams &p, const CUtensorMap &k,
+                                             const CUtensorMap &q, int grid, cudaStream_t st) {
+  const bool plain = p.a.cap == 0.0f && p.a.scale > 0.0f;
+  auto run = p.a.head_dim == 64 ? (plain ? &This::mass_tc<64, true> : &This::mass_tc<64, false>)
+                                : (plain ? &This::mass_tc<128, true> : &This::mass_tc<128, false>);
+  return run(p, k, q, grid, st);
 }
 
 template <>

@@ -94,7 +94,9 @@ __global__ void __launch_bounds__(kMassThreads)
     u32 valid = 0;
     {
       const int key = key0 + (lane & 15);
-      bool ok = key < q.keys;
+      // (blocks of tokens that no observed row sees are not looked at)
+      bool ok = key < q.keys && key < q.at + q.n &&
+                (p.window == 0 || key > q.at + sp.first - p.window);
       long long off = 0;
       if (ok) {
         const int pos = key / p.map.block_size;
