@@ -540,7 +540,19 @@ typedef struct kvcs_eviction {
                            kept tokens (kvcs_write_kv's running words) over
                            the caches of this call; in place, the words of
                            the request's emptied blocks become 0 */
+  void *workspace;      /* DEVICE, kvcs_eviction_workspace bytes, 16-byte
+                           aligned; scratch of this call alone while it runs,
+                           needs no clearing */
+  int64_t workspace_bytes;
 } kvcs_eviction;
+
+/*
+ * kvcs_eviction_workspace -- bytes of workspace a kvcs_evict call with these
+ * caches and sizes needs (about 1/1000 of the K and V it looks over).
+ * Returns the error codes of kvcs_evict for bad caches and sizes.
+ */
+int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
+                            int64_t num_requests, int64_t total_positions, int64_t *bytes);
 
 /*
  * kvcs_evict -- thins out the caches of a batch: the kept tokens' K, V (or
@@ -554,6 +566,10 @@ typedef struct kvcs_eviction {
  * all its blocks), listed once.  A request with a bad block id
  * (KVCS_STATUS_BAD_BLOCK_ID), inconsistent tables or a negative keep
  * (KVCS_STATUS_BAD_REQUESTS) is left untouched.
+ * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a
+ * STATE cache, a negative count, missing or misaligned pointers or a short
+ * workspace; KVCS_EUNSUPPORTED for a page of 2 GiB or more, or 2^31 or more
+ * tokens in the listed blocks.
  */
 int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                const kvcs_requests *reqs, int64_t total_positions, const kvcs_eviction *ev,
@@ -644,8 +660,8 @@ uint64_t kvcs_launch_count(void);
  * KVCS_OUT_WORKSPACE (callers built against minor 2 never set it).
  * Minor 4 added kvcs_plan_requests and kvcs_plan_info.slot_launches (the
  * struct grew: callers pass the minor-4 layout).  Minor 5 added
- * kvcs_paged_attention, kvcs_attention_workspace, kvcs_attention_mass and
- * kvcs_evict. */
+ * kvcs_paged_attention, kvcs_attention_workspace, kvcs_attention_mass,
+ * kvcs_evict and kvcs_eviction_workspace. */
 int32_t kvcs_version(void);
 
 #ifdef __cplusplus

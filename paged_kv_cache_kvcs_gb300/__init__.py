@@ -25,4 +25,5 @@ from ._binding import (  # noqa: F401
     kvcs_block_checksums_noalloc, KVCS_DTYPE_BF16, KVCS_DTYPE_FP16, KVCS_DTYPE_FP8_E4M3,
     kvcs_attention, kvcs_eviction)
 from ._attention import (  # noqa: F401
-    attention_mass, attention_workspace_bytes, evict, paged_attention)
+    attention_mass, attention_workspace_bytes, evict, eviction_workspace_bytes,
+    paged_attention)

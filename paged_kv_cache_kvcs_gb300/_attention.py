@@ -43,6 +43,18 @@ def _raise(rc: int, where: str) -> None:
         raise B.KvcsError(rc, where)
 
 
+def _workspace(given, n: int, stream, handle: int, dev):
+    """The caller's workspace, checked, or one of ``n`` bytes."""
+    if given is not None:
+        B._check_tensor("workspace", given, (torch.uint8,), n, dev)
+        return given
+    if stream is None or handle == torch.cuda.current_stream(dev).cuda_stream:
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    # freed on return: it has to belong to the stream that uses it
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
 def _queries(cache, q, new_offsets, num_requests, kv_dtype, dev):
     """Checks q and new_offsets; returns a kvcs_attention with their fields."""
     if not (getattr(q, "is_cuda", False) and q.dim() == 3):
@@ -149,14 +161,7 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     _raise(lib.kvcs_attention_workspace(arr, block_size, R, total_positions, a_ref, 0, ctypes.byref(n)),
            "kvcs_attention_workspace")
     handle = _stream_handle(stream, dev)
-    if workspace is None:
-        if stream is None or handle == torch.cuda.current_stream(dev).cuda_stream:
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        else:   # freed on return: it has to belong to the stream that uses it
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    else:
-        B._check_tensor("workspace", workspace, (torch.uint8,), n.value, dev)
+    workspace = _workspace(workspace, n.value, stream, handle, dev)
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel()
     reqs = _requests(pos_offsets, first_position, num_tokens, block_ids)
@@ -194,15 +199,27 @@ def attention_mass(cache, block_size: int, pos_offsets, first_position, num_toke
     return mass
 
 
+def eviction_workspace_bytes(caches: Sequence, block_size: int, num_requests: int,
+                             total_positions: int) -> int:
+    """Bytes of workspace ``evict`` needs (``kvcs_eviction_workspace``)."""
+    n = ctypes.c_int64()
+    _raise(B.load_library().kvcs_eviction_workspace(
+        B.cache_array(caches), len(caches), block_size, num_requests, total_positions,
+        ctypes.byref(n)), "kvcs_eviction_workspace")
+    return n.value
+
+
 def evict(caches: Sequence, block_size: int, pos_offsets, first_position, num_tokens, block_ids,
           scores: Sequence, keep, *, sinks: int = 0, recent: int = 0, new_block_ids=None,
-          block_sums=None, status=None, stream=None, total_positions: int | None = None) -> None:
+          block_sums=None, workspace=None, status=None, stream=None,
+          total_positions: int | None = None) -> None:
     """Torch front end of ``kvcs_evict``: keeps ``keep[r]`` (int64 CUDA) tokens
     of each request in every cache of ``caches``, chosen per KV head by
     ``scores`` (one float32 tensor ``[num_blocks, num_heads, block_size]`` per
     cache), and moves them to the front of the request's blocks, or of
     ``new_block_ids`` (int32, one per position).  ``block_sums`` (one word per
-    block) get the filled blocks' checksums."""
+    block) get the filled blocks' checksums.  ``workspace`` is a CUDA uint8
+    tensor of ``eviction_workspace_bytes`` (by default allocated)."""
     if not isinstance(caches, (list, tuple)):
         caches, scores = [caches], [scores]
     if len(scores) != len(caches):
@@ -221,9 +238,14 @@ def evict(caches: Sequence, block_size: int, pos_offsets, first_position, num_to
                         min(c.num_blocks for c in caches), dev)
     B._check_status(status, dev)
     ptrs = (ctypes.c_void_p * max(1, len(caches)))(*[t.data_ptr() for t in scores])
+    lib, arr, R = B.load_library(), B.cache_array(caches), pos_offsets.numel() - 1
+    n = ctypes.c_int64()
+    _raise(lib.kvcs_eviction_workspace(arr, len(caches), block_size, R, total_positions,
+                                       ctypes.byref(n)), "kvcs_eviction_workspace")
+    handle = _stream_handle(stream, dev)
+    workspace = _workspace(workspace, n.value, stream, handle, dev)
     ev = B.kvcs_eviction(ptrs, keep.data_ptr(), sinks, recent, B._ptr(new_block_ids),
-                         B._ptr(block_sums))
+                         B._ptr(block_sums), workspace.data_ptr(), workspace.numel())
     reqs = _requests(pos_offsets, first_position, num_tokens, block_ids)
-    _raise(B.load_library().kvcs_evict(
-        B.cache_array(caches), len(caches), block_size, ctypes.byref(reqs), total_positions,
-        ctypes.byref(ev), B._ptr(status), _stream_handle(stream, dev)), "kvcs_evict")
+    _raise(lib.kvcs_evict(arr, len(caches), block_size, ctypes.byref(reqs), total_positions,
+                          ctypes.byref(ev), B._ptr(status), handle), "kvcs_evict")

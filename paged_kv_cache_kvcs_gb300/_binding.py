@@ -80,7 +80,8 @@ class kvcs_attention(ctypes.Structure):
 class kvcs_eviction(ctypes.Structure):
     _fields_ = [("scores", ctypes.POINTER(ctypes.c_void_p)), ("keep", ctypes.c_void_p),
                 ("sinks", ctypes.c_int64), ("recent", ctypes.c_int64),
-                ("new_block_ids", ctypes.c_void_p), ("block_sums", ctypes.c_void_p)]
+                ("new_block_ids", ctypes.c_void_p), ("block_sums", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 class kvcs_plan_info(ctypes.Structure):
@@ -127,6 +128,9 @@ SIGNATURES = {
         ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.POINTER(kvcs_requests),
         ctypes.c_int64, ctypes.POINTER(kvcs_attention), ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_void_p]),
+    "kvcs_eviction_workspace": (ctypes.c_int, [
+        ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+        ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
     "kvcs_evict": (ctypes.c_int, [
         ctypes.POINTER(kvcs_cache), ctypes.c_int32, ctypes.c_int32,
         ctypes.POINTER(kvcs_requests), ctypes.c_int64, ctypes.POINTER(kvcs_eviction),

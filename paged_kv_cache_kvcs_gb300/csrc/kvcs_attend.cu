@@ -54,6 +54,8 @@ PageMap page_map(const kvcs_cache &c, int block_size) {
       m.head_stride = hb;
       break;
   }
+  m.by_block = FastDiv::of(static_cast<u32>(m.block_size));
+  m.by_sub = FastDiv::of(static_cast<u32>(m.kbs));
   return m;
 }
 
@@ -121,6 +123,7 @@ AttnParams attn_params(const kvcs_cache *cache, int32_t block_size, const kvcs_r
   p.lse = a->lse;
   p.kv_heads = cache->num_heads;
   p.group = a->q_heads / cache->num_heads;
+  p.by_group = FastDiv::of(static_cast<u32>(p.group));
   p.q_bf16 = a->q_dtype == KVCS_DTYPE_BF16;
   p.window = static_cast<int>(a->window < kMaxRequestTokens ? a->window : 0);
   p.observe = static_cast<int>(std::min<int64_t>(a->observe, kMaxRequestTokens));
@@ -284,6 +287,65 @@ int64_t attend_workspace(const AttendPlan &pl) {
   return (attend_tickets(pl) * 4 + 255) / 256 * 256 + pl.part_floats * 4;
 }
 
+constexpr int kEvictSmemTokens = 24576;   // 96 KiB of scores: two CTAs an SM
+
+// Bits and window counts of one row, over all requests.
+struct EvictSizes {
+  long long words, windows;
+};
+EvictSizes evict_sizes(int64_t num_requests, int64_t total_positions, int32_t block_size) {
+  const long long tokens = total_positions * block_size;
+  return {tokens / 32 + num_requests + 1, tokens / kEvictWindow + num_requests + 1};
+}
+
+// As many caches from `lo` on as one launch holds and its grid can number
+// (up to 64 column groups and spans a row).
+struct EvictLaunch {
+  int caches;
+  long long rows;
+};
+EvictLaunch evict_launch(const kvcs_cache *caches, int32_t lo, int32_t num_caches,
+                         int64_t num_requests) {
+  EvictLaunch l = {0, 0};
+  while (lo + l.caches < num_caches && l.caches < kMaxCachesPerLaunch) {
+    const long long rows = l.rows + caches[lo + l.caches].num_heads;
+    if (static_cast<double>(rows) * num_requests * 16.0 >= 2147483648.0) break;
+    l.rows = rows;
+    ++l.caches;
+  }
+  return l;
+}
+
+// Checks of the caches of an eviction.
+int check_evict_caches(const kvcs_cache *caches, int32_t num_caches, int32_t block_size) {
+  if (!caches || num_caches < 1) return KVCS_EINVAL;
+  std::vector<kvcs_cache> plain(caches, caches + num_caches);
+  for (kvcs_cache &c : plain) c.column = 0;
+  const int rc = check_caches(plain.data(), num_caches, block_size);
+  if (rc != KVCS_OK) return rc;
+  for (int32_t i = 0; i < num_caches; ++i) {
+    if (caches[i].layout == KVCS_LAYOUT_STATE) return KVCS_EINVAL;
+    if (static_cast<double>(block_size) * caches[i].num_heads * caches[i].head_bytes >=
+        2147483648.0)
+      return KVCS_EUNSUPPORTED;
+  }
+  return KVCS_OK;
+}
+
+// Launches follow one another on the stream and share the space.
+int64_t evict_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
+                        int64_t num_requests, int64_t total_positions) {
+  const EvictSizes s = evict_sizes(num_requests, total_positions, block_size);
+  long long rows = 0;
+  for (int32_t lo = 0; lo < num_caches;) {
+    const EvictLaunch l = evict_launch(caches, lo, num_caches, num_requests);
+    if (l.caches == 0) break;
+    rows = std::max(rows, l.rows);
+    lo += l.caches;
+  }
+  return rows * (s.words + s.windows) * 4;
+}
+
 __global__ void __launch_bounds__(1024) kvcs_tickets_kernel(u32 *tickets, int n) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
@@ -443,27 +505,34 @@ int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_
   return KVCS_OK;
 }
 
+int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
+                            int64_t num_requests, int64_t total_positions, int64_t *bytes) {
+  if (!bytes || num_requests < 0 || total_positions < 0) return KVCS_EINVAL;
+  const int rc = check_evict_caches(caches, num_caches, block_size);
+  if (rc != KVCS_OK) return rc;
+  *bytes = evict_workspace(caches, num_caches, block_size, num_requests, total_positions);
+  return KVCS_OK;
+}
+
 int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                const kvcs_requests *reqs, int64_t total_positions, const kvcs_eviction *ev,
                uint32_t *status, void *stream) {
-  if (!caches || num_caches < 1 || !ev) return KVCS_EINVAL;
-  std::vector<kvcs_cache> plain(caches, caches + num_caches);
-  for (kvcs_cache &c : plain) c.column = 0;
-  int rc = check_caches(plain.data(), num_caches, block_size);
+  if (!ev) return KVCS_EINVAL;
+  int rc = check_evict_caches(caches, num_caches, block_size);
   if (rc != KVCS_OK) return rc;
   rc = check_tables(reqs, total_positions);
   if (rc != KVCS_OK) return rc;
   if (ev->sinks < 0 || ev->recent < 0 || !ev->scores) return KVCS_EINVAL;
-  for (int32_t i = 0; i < num_caches; ++i) {
-    if (caches[i].layout == KVCS_LAYOUT_STATE) return KVCS_EINVAL;
+  for (int32_t i = 0; i < num_caches; ++i)
     if (!ev->scores[i] || !aligned(ev->scores[i], 4)) return KVCS_EINVAL;
-    if (static_cast<double>(block_size) * caches[i].num_heads * caches[i].head_bytes >=
-        2147483648.0)
-      return KVCS_EUNSUPPORTED;
-  }
   if (!aligned(ev->new_block_ids, 4) || !aligned(ev->block_sums, 8)) return KVCS_EINVAL;
   if (reqs->num_requests == 0 || total_positions == 0) return KVCS_OK;
   if (!ev->keep || !aligned(ev->keep, 8)) return KVCS_EINVAL;
+  if (static_cast<double>(total_positions) * block_size >= 2147483648.0) return KVCS_EUNSUPPORTED;
+  if (!ev->workspace || !aligned(ev->workspace, 16) ||
+      ev->workspace_bytes <
+          evict_workspace(caches, num_caches, block_size, reqs->num_requests, total_positions))
+    return KVCS_EINVAL;
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -486,6 +555,16 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   for (int32_t i = 1; i < num_caches; ++i)
     p.num_blocks = std::min<long long>(p.num_blocks, caches[i].num_blocks);
   int launches = 0;
+  p.by_block = FastDiv::of(static_cast<u32>(block_size));
+  const EvictSizes sizes = evict_sizes(reqs->num_requests, total_positions, block_size);
+  p.bit_words = sizes.words;
+  p.windows = sizes.windows;
+  // scores in shared memory up to twice the average length (short of what
+  // two CTAs an SM can have); longer rows read them again in every pass
+  const int64_t tokens = total_positions * block_size;
+  const int64_t average = tokens / reqs->num_requests;
+  p.smem_tokens = static_cast<int>(
+      std::min<int64_t>({tokens, std::max<int64_t>(2 * average, 4096), kEvictSmemTokens}));
   if (p.block_sums) {
     const unsigned grid =
         static_cast<unsigned>(std::min<int64_t>(reqs->num_requests, 4ll * sms));
@@ -493,31 +572,53 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
     ++launches;
   }
+  if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kvcs_evict_select_kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kEvictSmemTokens * 4) != cudaSuccess)
+    return KVCS_ECUDA;
   for (int32_t lo = 0; lo < num_caches;) {
-    // as many caches as a launch holds and its grid can number
-    int n = 0;
-    long long rows = 0;
-    while (lo + n < num_caches && n < kMaxCachesPerLaunch) {
+    const EvictLaunch l = evict_launch(caches, lo, num_caches, reqs->num_requests);
+    if (l.caches == 0) return KVCS_EUNSUPPORTED;
+    // few rows: each is split by halves and columns of at least 128 bytes, and
+    // into fresh blocks by windows too
+    const long long rows = l.rows * reqs->num_requests;
+    int parts = 1;
+    while (parts < 8 && rows * 2 * parts < 2ll * sms) parts *= 2;
+    p.num_caches = l.caches;
+    p.rows = static_cast<int>(l.rows);
+    p.halves_parts = 1;
+    long long first = 0;
+    for (int n = 0; n < l.caches; ++n) {
       const kvcs_cache &c = caches[lo + n];
-      if ((rows + c.num_heads) * static_cast<double>(reqs->num_requests) >= 2147483648.0) break;
       EvictCache &e = p.c[n];
       e.map = page_map(c, block_size);
       e.scores = ev->scores[lo + n];
       e.m0 = 2ull * (static_cast<u64>(c.layer) * KVCS_MAX_KV_HEADS_PER_LAYER + c.head_offset) + 1;
       e.heads = c.num_heads;
       e.head_bytes = c.head_bytes;
-      e.first_row = static_cast<int>(rows);
-      e.unit8 = needs_8(c) ? 1 : 0;
-      rows += c.num_heads;
-      ++n;
+      e.first_row = static_cast<int>(first);
+      e.unit = needs_8(c) ? 8 : 16;
+      const int pieces = c.head_bytes / e.unit;
+      const int least = std::max(1, 128 / e.unit);
+      e.part_pieces = std::max(std::min(least, pieces), (pieces + parts - 1) / parts);
+      e.parts = (pieces + e.part_pieces - 1) / e.part_pieces;
+      e.by_part = FastDiv::of(static_cast<u32>(e.part_pieces));
+      p.halves_parts = std::max(p.halves_parts, e.map.halves * e.parts);
+      first += c.num_heads;
     }
-    if (n == 0) return KVCS_EUNSUPPORTED;
-    p.num_caches = n;
-    p.rows = static_cast<int>(rows);
-    kvcs_evict_kernel<<<static_cast<unsigned>(rows * reqs->num_requests), kEvictThreads, 0, st>>>(p);
+    const long long units = rows * p.halves_parts;
+    p.spans = 1;
+    if (ev->new_block_ids)
+      p.spans = static_cast<int>(std::max<int64_t>(
+          1, std::min<int64_t>({average / kEvictWindow, 8ll * sms / units, 64})));
+    p.bits = static_cast<u32 *>(ev->workspace);
+    p.ahead = p.bits + l.rows * sizes.words;
+    kvcs_evict_select_kernel<<<static_cast<unsigned>(rows), kEvictThreads, p.smem_tokens * 4, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-    ++launches;
-    lo += n;
+    kvcs_evict_move_kernel<<<static_cast<unsigned>(units * p.spans), kEvictThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+    launches += 2;
+    lo += l.caches;
   }
   count_launches(launches);
   return KVCS_OK;

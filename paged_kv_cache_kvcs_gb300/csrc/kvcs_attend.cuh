@@ -315,8 +315,8 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Request 
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     rs[r] = 1.0f;
-    const long long tok = q.q0 + row[r] / p.group;
-    const int hq = head * p.group + row[r] % p.group;
+    const long long tok = q.q0 + p.by_group(row[r]);
+    const int hq = head * p.group + (row[r] - p.by_group(row[r]) * p.group);
     const unsigned char *src =
         base + (tok * p.q_stride + static_cast<long long>(hq) * p.head_dim) * 2;
     constexpr int kPiece = kType == kKvFp8 ? 16 : 8;   // elements a lane takes at once
@@ -367,7 +367,7 @@ __device__ __forceinline__ u32 load_chunk(const AttnParams &p, const Request &q,
   bool ok = key >= lo && key < hi;
   long long off = 0;
   if (ok) {
-    const int pos = key / p.map.block_size;
+    const int pos = p.map.by_block(key);
     const int block = p.tab.block_ids[q.pos0 + pos];
     if (block < 0 || block >= p.map.num_blocks) {
       ok = false;
@@ -411,8 +411,8 @@ __device__ __forceinline__ u32 load_chunk(const AttnParams &p, const Request &q,
 // Final values of one row: o / l, the log-sum-exp, in the output's type.
 __device__ __forceinline__ void store_out(const AttnParams &p, const Request &q, int head, int row,
                                           int col, float a, float b, bool bf16) {
-  const long long tok = q.q0 + row / p.group;
-  const int hq = head * p.group + row % p.group;
+  const long long tok = q.q0 + p.by_group(row);
+  const int hq = head * p.group + (row - p.by_group(row) * p.group);
   unsigned char *dst = static_cast<unsigned char *>(p.out) +
                        ((tok * (p.group * p.kv_heads) + hq) * p.head_dim + col) * 2;
   *reinterpret_cast<u32 *>(dst) = bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
@@ -421,8 +421,8 @@ __device__ __forceinline__ void store_out(const AttnParams &p, const Request &q,
 __device__ __forceinline__ void store_lse(const AttnParams &p, const Request &q, int head, int row,
                                           float m, float l) {
   if (!p.lse) return;
-  const long long tok = q.q0 + row / p.group;
-  const int hq = head * p.group + row % p.group;
+  const long long tok = q.q0 + p.by_group(row);
+  const int hq = head * p.group + (row - p.by_group(row) * p.group);
   p.lse[tok * (p.group * p.kv_heads) + hq] = l == 0.0f ? kNegInf : kLn2 * (m + log2f(l));
 }
 
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kAttendThreads)
       const int rr = row0 + g + 8 * i;
       has[i] = rr < rows_all;
       row[i] = has[i] ? rr : rows_all - 1;   // spare rows repeat the last one
-      at[i] = q.at + row[i] / p.group;
+      at[i] = q.at + p.by_group(row[i]);
     }
     const int warp_last = min(row0 + 15, rows_all - 1);
     const int at_min = q.at + min(row0, rows_all - 1) / p.group;

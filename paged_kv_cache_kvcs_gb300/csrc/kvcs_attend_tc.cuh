@@ -150,7 +150,7 @@ struct TcShared {
 
 // Whether token `key` (below the request's count) lies in a block of the pool.
 __device__ __forceinline__ bool good_block(const AttnParams &a, const Request &q, int key) {
-  const int b = a.tab.block_ids[q.pos0 + key / a.map.block_size];
+  const int b = a.tab.block_ids[q.pos0 + a.map.by_block(key)];
   return b >= 0 && b < a.map.num_blocks;
 }
 
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int key = k * kTcKeys + lane * p.box;
         int block = -1;
         if (k < x.k1 && lane < boxes && key < x.q.keys) {
-          block = a.tab.block_ids[x.q.pos0 + key / bs];
+          block = a.tab.block_ids[x.q.pos0 + a.map.by_block(key)];
           if (block >= a.map.num_blocks) block = -1;
         }
         return block;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const u32 stage = it % S::kStages;
         const u32 dst = ring + stage * S::kTileBytes;
         // where the box starts, in the map's groups of 8 slots
-        const int slot = (key0 + lane * p.box) % bs, sub = slot / a.map.kbs;
+        const int slot = (key0 + lane * p.box) % bs, sub = a.map.by_sub(slot);
         const int group = p.heads_in_groups
                               ? (sub * a.kv_heads + x.head) * (a.map.kbs / 8) + (slot - sub * a.map.kbs) / 8
                               : slot / 8;
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row = x.row0 + i * 128 + lr;
       const bool has = row < x.rows_all;
       const int row_c = has ? row : x.rows_all - 1;
-      const int tok_i = row_c / a.group, hq = x.head * a.group + row_c - tok_i * a.group;
+      const int tok_i = a.by_group(row_c), hq = x.head * a.group + row_c - tok_i * a.group;
       const int at = x.q.at + tok_i;
       float m = kNegInf, l = 0.0f;
       const int nk = x.k1 - x.k0;
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (!(sh.dirty[par][d][kk >> 5] >> (kk & 31) & 1u)) continue;
               const int key = key0 + kk;
               if (key > at || (a.window > 0 && key <= at - a.window)) continue;
-              const int pos = key / a.map.block_size;
+              const int pos = a.map.by_block(key);
               const unsigned char *kp =
                   a.map.base + token_offset(a.map, a.tab.block_ids[x.q.pos0 + pos],
                                             key - pos * a.map.block_size, x.head);

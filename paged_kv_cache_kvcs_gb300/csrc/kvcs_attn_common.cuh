@@ -21,6 +21,23 @@ constexpr long long kMaxRequestTokens = 1ll << 30;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Division of 31-bit numbers by a fixed divisor: n * m >> s with
+// s = 31 + ceil(log2 d) and m = ceil(2^s / d), exact for every n < 2^31.
+struct FastDiv {
+  u32 m, s;
+  __host__ __device__ static FastDiv of(u32 d) {
+    FastDiv f;
+    u32 l = 0;
+    while ((1ull << l) < d) ++l;
+    f.s = 31 + l;
+    f.m = static_cast<u32>(((1ull << f.s) + d - 1) / d);
+    return f;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(static_cast<u64>(static_cast<u32>(n)) * m >> s);
+  }
+};
+
 // Where a token's bytes are: half (K, V), block, slot, head and 16-byte
 // chunk each add their stride; kernel sub-blocks add sub_stride.
 struct PageMap {
@@ -35,12 +52,14 @@ struct PageMap {
   int chunk_stride;        // 16 but for x-split pools
   int block_size;
   int halves;
+  FastDiv by_block;        // division by block_size and by kbs
+  FastDiv by_sub;
 };
 
 // Byte offset of (block, slot, head) from the pool's base.
 __device__ __forceinline__ long long token_offset(const PageMap &m, long long block, int slot,
                                                   int head) {
-  const int sub = slot / m.kbs;
+  const int sub = m.by_sub(slot);
   return block * m.block_stride + sub * m.sub_stride +
          static_cast<long long>(slot - sub * m.kbs) * m.slot_stride + head * m.head_stride;
 }
@@ -130,6 +149,7 @@ struct AttnParams {
   float *part;            // partial results of groups split between CTAs
   u32 *tickets;           // one per CTA, zeroed before the launch
   int kv_heads, group, head_dim;
+  FastDiv by_group;
   int q_bf16;             // fp8 caches: queries (and out) are bf16, else fp16
   int window;             // 0: none
   int observe;            // mass: last new tokens observed (0: all)

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kMassThreads)
                 (p.window == 0 || key > q.at + sp.first - p.window);
       long long off = 0;
       if (ok) {
-        const int pos = key / p.map.block_size;
+        const int pos = p.map.by_block(key);
         const int block = p.tab.block_ids[q.pos0 + pos];
         if (block < 0 || block >= p.map.num_blocks) {
           ok = false;
@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(kMassThreads)
         const int rr = row0 + g + 8 * i;
         has[i] = rr < rows_end;
         row[i] = has[i] ? rr : row0;
-        at[i] = has[i] ? q.at + row[i] / p.group : -1;   // spare rows see nothing
-        const long long tok = q.q0 + row[i] / p.group;
+        at[i] = has[i] ? q.at + p.by_group(row[i]) : -1;   // spare rows see nothing
+        const long long tok = q.q0 + p.by_group(row[i]);
         lse[i] = kLog2e * __ldg(p.lse + tok * (p.group * p.kv_heads) + head * p.group +
-                                row[i] % p.group);
+                                (row[i] - p.by_group(row[i]) * p.group));
       }
       u32 qf[kDim / 8][2];
       float rs[2];
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kMassThreads)
         v += __shfl_xor_sync(0xffffffffu, v, 16);
         const int kk = j * 8 + t + 4 * i;
         if (g == 0 && (valid >> kk & 1u)) {
-          const int key = key0 + kk, pos = key / p.map.block_size;
+          const int key = key0 + kk, pos = p.map.by_block(key);
           const long long block = p.tab.block_ids[q.pos0 + pos];
           atomicAdd(p.mass + (block * p.kv_heads + head) * p.map.block_size +
                         (key - pos * p.map.block_size), v);

@@ -204,10 +204,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int key = x.key0 + i * 128 + lane * p.box;
         int block = -1;
         if (lane < boxes && key < x.q.keys) {
-          block = a.tab.block_ids[x.q.pos0 + key / bs];
+          block = a.tab.block_ids[x.q.pos0 + a.map.by_block(key)];
           if (block >= a.map.num_blocks) block = -1;
         }
-        const int in = key % bs, sub = in / a.map.kbs;
+        const int in = key % bs, sub = a.map.by_sub(in);
         const int group = p.heads_in_groups
                               ? (sub * a.kv_heads + x.head) * (a.map.kbs / 8) + (in - sub * a.map.kbs) / 8
                               : in / 8;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     : rows_end;
       float *dst = nullptr;
       if (work && r_hi > r_lo && key < x.q.keys) {
-        const int pos = key / a.map.block_size;
+        const int pos = a.map.by_block(key);
         const long long block = a.tab.block_ids[x.q.pos0 + pos];
         if (block < 0 || block >= a.map.num_blocks)
           raise(a.tab, kStatusBadBlockId);

@@ -123,7 +123,7 @@ def test_workspace_sizes():
 def evict(caches=None, positions=10, reqs=None, scores=None, n=None, **kw):
     caches = caches or [FakeCache()]
     ptrs = (ctypes.c_void_p * len(caches))(*(scores or [1 << 20] * len(caches)))
-    ev = B.kvcs_eviction(ptrs, 1 << 16, 0, 0, None, None)
+    ev = B.kvcs_eviction(ptrs, 1 << 16, 0, 0, None, None, 1 << 17, 1 << 30)
     for k, v in kw.items():
         setattr(ev, k, v)
     r = B.kvcs_requests(**{**REQS, **(reqs or {})})
@@ -141,12 +141,19 @@ def test_evict_refusals():
     assert evict(scores=[None]) == K.KVCS_EINVAL
     assert evict(scores=[(1 << 20) + 2]) == K.KVCS_EINVAL
     for bad in (dict(sinks=-1), dict(recent=-1), dict(keep=None), dict(keep=(1 << 16) + 4),
-                dict(new_block_ids=(1 << 16) + 2), dict(block_sums=(1 << 16) + 4)):
+                dict(new_block_ids=(1 << 16) + 2), dict(block_sums=(1 << 16) + 4),
+                dict(workspace=None), dict(workspace=(1 << 17) + 8), dict(workspace_bytes=8)):
         assert evict(**bad) == K.KVCS_EINVAL, bad
     assert evict(positions=-1) == K.KVCS_EINVAL
     assert evict(reqs=dict(block_ids=None)) == K.KVCS_EINVAL
     assert evict(reqs=dict(num_requests=0)) == K.KVCS_OK
     assert evict(positions=0, reqs=dict(block_ids=None)) == K.KVCS_OK
+    assert evict(positions=1 << 27) == K.KVCS_EUNSUPPORTED        # 2^31 tokens
+    n = K.eviction_workspace_bytes([FakeCache()], 16, 2, 10)
+    assert n > 0 and evict(workspace_bytes=n) == K.KVCS_ECUDA
+    assert evict(workspace_bytes=n - 1) == K.KVCS_EINVAL
+    with pytest.raises(K.KvcsError):
+        K.eviction_workspace_bytes([FakeCache(head_bytes=12)], 16, 2, 10)
 
 
 class FakeQ(FakeTensor):
