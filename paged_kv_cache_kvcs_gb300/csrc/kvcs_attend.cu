@@ -287,7 +287,7 @@ int64_t attend_workspace(const AttendPlan &pl) {
   return (attend_tickets(pl) * 4 + 255) / 256 * 256 + pl.part_floats * 4;
 }
 
-constexpr int kEvictSmemTokens = 24576;   // 96 KiB of scores: two CTAs an SM
+constexpr int kEvictSmemTokens = 49152;   // 192 KiB of scores
 
 // Bits and window counts of one row, over all requests.
 struct EvictSizes {
@@ -559,8 +559,8 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   const EvictSizes sizes = evict_sizes(reqs->num_requests, total_positions, block_size);
   p.bit_words = sizes.words;
   p.windows = sizes.windows;
-  // scores in shared memory up to twice the average length (short of what
-  // two CTAs an SM can have); longer rows read them again in every pass
+  // scores in shared memory up to twice the average length; longer rows read
+  // them again in every pass
   const int64_t tokens = total_positions * block_size;
   const int64_t average = tokens / reqs->num_requests;
   p.smem_tokens = static_cast<int>(
@@ -600,9 +600,10 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
       e.unit = needs_8(c) ? 8 : 16;
       const int pieces = c.head_bytes / e.unit;
       const int least = std::max(1, 128 / e.unit);
-      e.part_pieces = std::max(std::min(least, pieces), (pieces + parts - 1) / parts);
+      // (at most a thread per piece)
+      e.part_pieces = std::min(kEvictThreads, std::max(std::min(least, pieces),
+                                                       (pieces + parts - 1) / parts));
       e.parts = (pieces + e.part_pieces - 1) / e.part_pieces;
-      e.by_part = FastDiv::of(static_cast<u32>(e.part_pieces));
       p.halves_parts = std::max(p.halves_parts, e.map.halves * e.parts);
       first += c.num_heads;
     }
@@ -611,13 +612,27 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     if (ev->new_block_ids)
       p.spans = static_cast<int>(std::max<int64_t>(
           1, std::min<int64_t>({average / kEvictWindow, 8ll * sms / units, 64})));
+    if (static_cast<double>(units) * p.spans >= 2147483648.0) return KVCS_EUNSUPPORTED;
     p.bits = static_cast<u32 *>(ev->workspace);
     p.ahead = p.bits + l.rows * sizes.words;
-    kvcs_evict_select_kernel<<<static_cast<unsigned>(rows), kEvictThreads, p.smem_tokens * 4, st>>>(p);
+    // large CTAs where the rows are few
+    const int threads = rows < 4ll * sms ? kEvictSelectThreads : kEvictSelectThreads / 4;
+    kvcs_evict_select_kernel<<<static_cast<unsigned>(rows), threads, p.smem_tokens * 4, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-    kvcs_evict_move_kernel<<<static_cast<unsigned>(units * p.spans), kEvictThreads, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-    launches += 2;
+    ++launches;
+    // a launch for the caches of either piece size
+    bool has[2] = {false, false};
+    for (int n = 0; n < l.caches; ++n) has[p.c[n].unit == 16] = true;
+    const dim3 grid(static_cast<unsigned>(units * p.spans));
+    for (int u = 0; u < 2; ++u) {
+      if (!has[u]) continue;
+      auto move = p.block_sums
+                      ? (u ? kvcs_evict_move_kernel<true, true> : kvcs_evict_move_kernel<true, false>)
+                      : (u ? kvcs_evict_move_kernel<false, true> : kvcs_evict_move_kernel<false, false>);
+      move<<<grid, kEvictThreads, 0, st>>>(p);
+      if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+      ++launches;
+    }
     lo += l.caches;
   }
   count_launches(launches);

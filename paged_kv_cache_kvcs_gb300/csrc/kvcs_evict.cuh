@@ -34,6 +34,7 @@
 namespace kvcs {
 
 constexpr int kEvictThreads = 256;
+constexpr int kEvictSelectThreads = 1024;   // at most
 constexpr int kEvictWindow = 1024;   // tokens a step of either kernel looks over
 constexpr int kEvictPieces = 8;      // pieces a thread moves at once
 
@@ -47,7 +48,6 @@ struct EvictCache {
   int unit;           // bytes of a piece: 16, or 8 on 8-byte boundaries
   int parts;          // column groups per half
   int part_pieces;    // pieces of a column group (the last may hold fewer)
-  FastDiv by_part;    // division by part_pieces
 };
 
 struct EvictParams {
@@ -141,13 +141,40 @@ __device__ __forceinline__ long long first_window(const EvictParams &p, long lon
   return q.pos0 * p.block_size / kEvictWindow + r;
 }
 
-__global__ void __launch_bounds__(kEvictThreads)
+// Sum of a value over the CTA's threads before this one; *total: over all.
+__device__ __forceinline__ int cta_scan(int v, int *warp_sums, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  const int w = lane < warps ? warp_sums[lane] : 0;
+  int sum = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  *total = __shfl_sync(0xffffffffu, sum, 31);
+  return __shfl_sync(0xffffffffu, sum - w, warp) + inc - v;
+}
+
+// Digits of the counting passes: 11, 11 and 10 bits from the top.
+constexpr int kEvictBins = 2048;
+
+__global__ void __launch_bounds__(kEvictSelectThreads)
     kvcs_evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ u32 s_score[];   // the row's scores, if they fit
-  __shared__ u32 s_hist[256];
+  __shared__ u32 s_hist[kEvictBins];
+  __shared__ int s_sums[32];
   __shared__ u32 s_pick[2];
-  __shared__ int s_count[kEvictWindow / 32], s_tie[kEvictWindow / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, warps = threads >> 5;
   const long long r = blockIdx.x / p.rows;
   const int row = static_cast<int>(blockIdx.x % p.rows);
   const EvictCache &c = cache_of_row(p, row);
@@ -164,12 +191,15 @@ __global__ void __launch_bounds__(kEvictThreads)
   const int lo = sinks, hi = N - recent, want = B - sinks - recent;   // candidates [lo, hi)
   const bool held = N <= p.smem_tokens;
   u32 *const scores = reinterpret_cast<u32 *>(c.scores);
+  const long long per_block = static_cast<long long>(c.heads) * bs, at_head = static_cast<long long>(head) * bs;
   auto place = [&](const int *blocks, int j) -> u32 * {
     const int pos = p.by_block(j);
-    return scores + (static_cast<long long>(blocks[pos]) * c.heads + head) * bs + (j - pos * bs);
+    return scores + blocks[pos] * per_block + at_head + (j - pos * bs);
   };
-  if (held)
-    for (int j = tid; j < N; j += kEvictThreads) s_score[j] = *place(ids, j);
+  if (held) {
+#pragma unroll 4
+    for (int j = tid; j < N; j += threads) s_score[j] = *place(ids, j);
+  }
   auto score = [&](int j) { return held ? s_score[j] : *place(ids, j); };
 
   // the least key kept, and how many tokens of that key are
@@ -177,128 +207,109 @@ __global__ void __launch_bounds__(kEvictThreads)
   const bool all = want == hi - lo;
   if (!all && want > 0) {
     u32 prefix = 0, left = static_cast<u32>(want);
-    for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
+      const u32 bins = shift == 0 ? 1024u : 2048u, above = shift == 0 ? 10u : 11u;
       __syncthreads();
-      s_hist[tid] = 0;
+      for (u32 i = tid; i < bins; i += threads) s_hist[i] = 0;
       __syncthreads();
-      for (int j0 = lo; j0 < hi; j0 += kEvictThreads) {
-        const int j = j0 + tid;
-        bool in = j < hi;
-        u32 k = 0;
-        if (in) {
-          k = score_key(score(j));
-          in = shift == 24 || (k >> (shift + 8)) == prefix;
-        }
-        // scores crowd into few digits: lanes of one digit add once
-        const u32 digit = in ? k >> shift & 255u : 256u;
-        const u32 peers = __match_any_sync(0xffffffffu, digit);
-        if (in && lane == __ffs(peers) - 1) atomicAdd(&s_hist[digit], __popc(peers));
+#pragma unroll 4
+      for (int j = lo + tid; j < hi; j += threads) {
+        const u32 k = score_key(score(j));
+        if (shift == 21 || (k >> (shift + above)) == prefix)
+          atomicAdd(&s_hist[k >> shift & (bins - 1)], 1u);
       }
       __syncthreads();
-      if (warp == 0) {
-        // digits from the greatest down: the one where the count reaches `left`
-        u32 mine[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mine[i] = s_hist[255 - (lane * 8 + i)];
-          sum += mine[i];
+      // digits from the greatest down: the one where the count reaches `left`
+      const u32 each = bins / threads > 0 ? bins / threads : 1;   // per thread
+      u32 sum = 0;
+      for (u32 i = 0; i < each; ++i) {
+        const u32 bin = tid * each + i;
+        if (bin < bins) sum += s_hist[bins - 1 - bin];
+      }
+      int total;
+      u32 at = static_cast<u32>(cta_scan(static_cast<int>(sum), s_sums, &total));
+      for (u32 i = 0; i < each; ++i) {
+        const u32 bin = tid * each + i;
+        const u32 n = bin < bins ? s_hist[bins - 1 - bin] : 0;
+        if (at < left && left <= at + n) {
+          s_pick[0] = bins - 1 - bin;
+          s_pick[1] = left - at;
         }
-        u32 inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u32 u = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += u;
-        }
-        u32 at = inc - sum;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (at < left && left <= at + mine[i]) {
-            s_pick[0] = 255 - (lane * 8 + i);
-            s_pick[1] = left - at;
-          }
-          at += mine[i];
-        }
+        at += n;
       }
       __syncthreads();
-      prefix = prefix << 8 | s_pick[0];
+      prefix = prefix << above | s_pick[0];
       left = s_pick[1];
     }
     least = prefix;
     ties = left;
   }
 
+  // Kept tokens in order.  A warp takes a run of words of 32 tokens, first
+  // counting, then, from the counts before it, marking and moving scores.
+  // (Scores that are not held in shared memory are moved by one warp alone,
+  // word after word: it reads a word's scores before it writes behind them.)
   u32 *const bits = p.bits + row * p.bit_words + first_word(p, r, q);
   u32 *const ahead = p.ahead + row * p.windows + first_window(p, r, q);
-  int done = 0;         // tokens kept before the window
-  u32 ties_seen = 0;    // tokens of key `least` before the window
-  for (int w0 = 0, win = 0; w0 < N; w0 += kEvictWindow, ++win) {
-    // a warp takes every eighth group of 32 tokens
-    constexpr int kEach = kEvictWindow / kEvictThreads;
-    u32 keep[kEach], tie[kEach], value[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int j = w0 + (i * 8 + warp) * 32 + lane;
-      bool stay = j < N && (all || j < lo || j >= hi), equal = false;
-      value[i] = j < N ? score(j) : 0u;
-      if (j < N && !stay && want > 0) {
-        const u32 k = score_key(value[i]);
-        stay = k > least;
-        equal = k == least;
-      }
-      keep[i] = __ballot_sync(0xffffffffu, stay);
-      tie[i] = __ballot_sync(0xffffffffu, equal);
-      if (lane == 0) s_tie[i * 8 + warp] = __popc(tie[i]);
+  const int words = (N + 31) / 32;
+  const int run = held ? (words + warps - 1) / warps : words;
+  const int w0 = min(words, held ? warp * run : warp == 0 ? 0 : words), w1 = min(words, w0 + run);
+  auto look = [&](int w, u32 *value, u32 *tie) {
+    const int j = w * 32 + lane;
+    bool stay = j < N && (all || j < lo || j >= hi), equal = false;
+    *value = j < N ? score(j) : 0u;
+    if (j < N && !stay && want > 0) {
+      const u32 k = score_key(*value);
+      stay = k > least;
+      equal = k == least;
     }
-    __syncthreads();
-    const u32 t = lane < kEvictWindow / 32 ? s_tie[lane] : 0;
-    u32 inc = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u32 u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
+    *tie = __ballot_sync(0xffffffffu, equal);
+    return __ballot_sync(0xffffffffu, stay);
+  };
+  int sure = 0, equal = 0;
+  if (held)
+    for (int w = w0; w < w1; ++w) {
+      u32 value, tie;
+      sure += __popc(look(w, &value, &tie));
+      equal += __popc(tie);
     }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      // the first of the equal ones, as far as they are wanted
-      const u32 before = ties_seen + __shfl_sync(0xffffffffu, inc - t, i * 8 + warp);
-      const int room = static_cast<int>(min(max(static_cast<long long>(ties) - before, 0ll), 32ll));
-      u32 take = tie[i];
-      for (int extra = __popc(take) - room; extra > 0; --extra) take &= ~(1u << (31 - __clz(take)));
-      keep[i] |= take;
-      if (lane == 0) s_count[i * 8 + warp] = __popc(keep[i]);
+  int total;
+  const int tie0 = cta_scan(lane == 0 ? equal : 0, s_sums, &total);
+  // of the equal ones the first are kept, as far as they are wanted
+  auto taken = [&](int before, int n) {
+    return static_cast<int>(min(max(static_cast<long long>(ties) - before, 0ll),
+                                static_cast<long long>(n)));
+  };
+  const int mine_tie0 = __shfl_sync(0xffffffffu, tie0, 0);
+  int seen = mine_tie0;
+  const int kept = sure + taken(seen, equal);
+  int done = cta_scan(lane == 0 ? kept : 0, s_sums, &total);
+  done = __shfl_sync(0xffffffffu, done, 0);
+  for (int w = w0; w < w1; ++w) {
+    u32 value, tie;
+    u32 keep = look(w, &value, &tie);
+    const int n = __popc(tie);
+    u32 take = tie;
+    for (int extra = n - taken(seen, n); extra > 0; --extra) take &= ~(1u << (31 - __clz(take)));
+    keep |= take;
+    seen += n;
+    if (lane == 0) {
+      bits[w] = keep;
+      if (w % (kEvictWindow / 32) == 0) ahead[w / (kEvictWindow / 32)] = done;
     }
-    ties_seen += __shfl_sync(0xffffffffu, inc, 31);
-    __syncthreads();
-    const int n = s_count[lane];
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += u;
-    }
-    if (tid == 0) ahead[win] = done;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int g = i * 8 + warp;
-      const int first = done + __shfl_sync(0xffffffffu, sum - n, g);
-      if (w0 + g * 32 < N) {
-        if (lane == 0) bits[(w0 >> 5) + g] = keep[i];
-        const int j = first + __popc(keep[i] & ((1u << lane) - 1u));
-        // (the window's scores were read before the barriers above)
-        if (keep[i] >> lane & 1u) *place(to_ids, j) = value[i];
-      }
-    }
-    done += __shfl_sync(0xffffffffu, sum, 31);
+    if (keep >> lane & 1u) *place(to_ids, done + __popc(keep & ((1u << lane) - 1u))) = value;
+    done += __popc(keep);
+    if (!held) __syncwarp();
   }
 }
 
+template <bool kWords, bool kUnit16>
 __global__ void __launch_bounds__(kEvictThreads)
     kvcs_evict_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ long long s_from[kEvictWindow], s_to[kEvictWindow];   // kept tokens' byte offsets
-  __shared__ int s_block[kEvictWindow];                            // and target blocks
+  __shared__ int s_block[kWords ? kEvictWindow : 1];               // and target blocks
   __shared__ int s_before[kEvictWindow / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  ptx::grid_dep_wait();   // the selection's bits
   long long idx = blockIdx.x;
   const int span = static_cast<int>(idx % p.spans);
   idx /= p.spans;
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(kEvictThreads)
   const EvictCache &c = cache_of_row(p, row);
   const int head = row - c.first_row;
   const int half = hp / c.parts, part = hp - half * c.parts;
-  if (half >= c.map.halves) return;
+  if (half >= c.map.halves || (c.unit == 16) != kUnit16) return;
   Request q;
   int B;
   if (!evict_request(p, r, &q, &B, false)) return;
@@ -317,15 +328,23 @@ __global__ void __launch_bounds__(kEvictThreads)
   const int *ids = p.tab.block_ids + q.pos0;
   const int *to_ids = p.new_block_ids ? p.new_block_ids + q.pos0 : ids;
   const bool in_place = to_ids == ids;
-  if (B == 0 || (B == N && in_place && !p.block_sums)) return;
+  if (B == 0 || (B == N && in_place && !kWords)) return;
   const u32 *const bits = p.bits + row * p.bit_words + first_word(p, r, q);
   const u32 *const ahead = p.ahead + row * p.windows + first_window(p, r, q);
+  constexpr int kUnit = kUnit16 ? 16 : 8;
   const int piece0 = part * c.part_pieces;
-  const int pieces = min(c.part_pieces, c.head_bytes / c.unit - piece0);   // of a token, here
-  const bool even = pieces == c.part_pieces;
+  const int pieces = min(c.part_pieces, c.head_bytes / kUnit - piece0);   // of a token, here
+  // a thread has one column, and eight consecutive tokens of every step
+  const int slot = tid / pieces;
+  const int tokens = kEvictThreads / pieces;   // threads side by side on tokens
+  const bool active = slot < tokens;
+  const int x = (piece0 + tid - slot * pieces) * kUnit;
+  unsigned char *const base = const_cast<unsigned char *>(c.map.base) + half * c.map.half_stride +
+                              static_cast<long long>(x >> 4) * c.map.chunk_stride + (x & 15);
   const u64 P = static_cast<u64>(c.map.halves) * (c.head_bytes / 8);
   const u64 m = c.m0 + 2ull * head;
-  unsigned char *const base = const_cast<unsigned char *>(c.map.base) + half * c.map.half_stride;
+  const u64 piece = static_cast<u64>(half) * (c.head_bytes / 8) + x / 8;
+  const PageMap &map = c.map;
 
   for (int w0 = span * kEvictWindow; w0 < N; w0 += p.spans * kEvictWindow) {
     // the window's kept tokens: where they are and where they go
@@ -343,39 +362,32 @@ __global__ void __launch_bounds__(kEvictThreads)
     }
     __syncthreads();
     const int done = static_cast<int>(ahead[w0 / kEvictWindow]);
-    for (int g = warp; g < words; g += kEvictThreads / 32) {
-      const u32 k = bits[(w0 >> 5) + g];
+#pragma unroll
+    for (int i = 0; i < kEvictWindow / kEvictThreads; ++i) {
+      const int g = i * (kEvictThreads / 32) + warp;
+      const u32 k = g < words ? bits[(w0 >> 5) + g] : 0u;
       if (k >> lane & 1u) {
         const int at = s_before[g] + __popc(k & ((1u << lane) - 1u));
         const int src = w0 + g * 32 + lane, sp = p.by_block(src);
         const int j = done + at, dp = p.by_block(j);
-        s_from[at] = token_offset(c.map, ids[sp], src - sp * bs, head);
-        s_block[at] = to_ids[dp];
-        s_to[at] = token_offset(c.map, to_ids[dp], j - dp * bs, head);
+        const int to = to_ids[dp];
+        s_from[at] = token_offset(map, ids[sp], src - sp * bs, head);
+        s_to[at] = token_offset(map, to, j - dp * bs, head);
+        if (kWords) s_block[at] = to;
       }
     }
     const int kept = s_before[words - 1] + __popc(bits[(w0 >> 5) + words - 1]);
     __syncthreads();
-    const int total = kept * pieces;
     uint4 v[2][kEvictPieces];
-    auto split = [&](int u, int *tok, long long *col) {
-      *tok = even ? c.by_part(u) : u / pieces;
-      const int x = (piece0 + u - *tok * pieces) * c.unit;
-      *col = static_cast<long long>(x >> 4) * c.map.chunk_stride + (x & 15);
-      return x;
-    };
-    auto fetch = [&](uint4 (&d)[kEvictPieces], int u0) {
+    auto fetch = [&](uint4 (&d)[kEvictPieces], int t0) {
+      const int t = t0 + slot * kEvictPieces;
 #pragma unroll
       for (int i = 0; i < kEvictPieces; ++i) {
-        const int u = u0 + i * kEvictThreads + tid;
-        if (u >= total) continue;
-        int tok;
-        long long col;
-        split(u, &tok, &col);
+        if (!active || t + i >= kept) continue;
         // tokens that stay where they are pass through only for their words
-        if (!p.block_sums && s_from[tok] == s_to[tok]) continue;
-        const unsigned char *from = base + s_from[tok] + col;
-        if (c.unit == 16) {
+        if (!kWords && s_from[t + i] == s_to[t + i]) continue;
+        const unsigned char *from = base + s_from[t + i];
+        if (kUnit16) {
           d[i] = *reinterpret_cast<const uint4 *>(from);
         } else {
           const uint2 w = *reinterpret_cast<const uint2 *>(from);
@@ -383,53 +395,60 @@ __global__ void __launch_bounds__(kEvictThreads)
         }
       }
     };
-    auto put = [&](const uint4 (&d)[kEvictPieces], int u0) {
+    auto put = [&](const uint4 (&d)[kEvictPieces], int t0) {
+      const int t = t0 + slot * kEvictPieces;
 #pragma unroll
       for (int i = 0; i < kEvictPieces; ++i) {
-        const int u = u0 + i * kEvictThreads + tid;
-        u64 word = 0;
+        if (!active || t + i >= kept || s_from[t + i] == s_to[t + i]) continue;
+        unsigned char *to = base + s_to[t + i];
+        if (kUnit16)
+          *reinterpret_cast<uint4 *>(to) = d[i];
+        else
+          *reinterpret_cast<uint2 *>(to) = make_uint2(d[i].x, d[i].y);
+      }
+      if constexpr (kWords) {
+        // sums of runs of tokens of one block, then of the warp's lanes
+        u64 sum = 0;
         int block = -1;
-        if (u < total) {
-          int tok;
-          long long col;
-          const int x = split(u, &tok, &col);
-          if (s_from[tok] != s_to[tok]) {
-            unsigned char *to = base + s_to[tok] + col;
-            if (c.unit == 16)
-              *reinterpret_cast<uint4 *>(to) = d[i];
-            else
-              *reinterpret_cast<uint2 *>(to) = make_uint2(d[i].x, d[i].y);
+        auto flush = [&]() {
+          u32 open = __ballot_sync(0xffffffffu, block >= 0);
+          while (open) {
+            const int b = __shfl_sync(0xffffffffu, block, __ffs(open) - 1);
+            const bool same = block == b;
+            const u64 all = warp_sum(same ? sum : 0ull);
+            if (lane == __ffs(open) - 1) atomicAdd(p.block_sums + b, m * all);
+            open &= ~__ballot_sync(0xffffffffu, same);
           }
-          if (p.block_sums) {
-            block = s_block[tok];
+        };
+#pragma unroll
+        for (int i = 0; i < kEvictPieces; ++i) {
+          const bool in = active && t + i < kept;
+          const int b = in ? s_block[t + i] : block;
+          if (__any_sync(0xffffffffu, b != block && block >= 0)) {
+            flush();
+            sum = 0;
+            block = -1;
+          }
+          if (in) {
             const u64 x0 = static_cast<u64>(d[i].y) << 32 | d[i].x;
             const u64 x1 = static_cast<u64>(d[i].w) << 32 | d[i].z;
-            const u64 piece = static_cast<u64>(half) * (c.head_bytes / 8) + x / 8;
-            const u64 f = 2ull * ((static_cast<u64>(q.base) + done + tok) * P + piece) + 1;
-            word = m * (x0 * f + x1 * (f + 2));
+            const u64 f = 2ull * ((static_cast<u64>(q.base) + done + t + i) * P + piece) + 1;
+            sum += (x0 + x1) * f + 2ull * x1;
+            block = b;
           }
         }
-        if (p.block_sums) {
-          // one add per warp where its pieces share a block
-          const int b0 = __shfl_sync(0xffffffffu, block, 0);
-          if (__all_sync(0xffffffffu, block == b0 || block < 0)) {
-            word = warp_sum(word);
-            if (lane == 0 && b0 >= 0) atomicAdd(p.block_sums + b0, word);
-          } else if (block >= 0) {
-            atomicAdd(p.block_sums + block, word);
-          }
-        }
+        flush();
       }
     };
-    constexpr int kStep = kEvictThreads * kEvictPieces;
+    const int step = tokens * kEvictPieces;
     fetch(v[0], 0);
-    for (int u0 = 0; u0 < total; u0 += 2 * kStep) {
-      fetch(v[1], u0 + kStep);
+    for (int t0 = 0; t0 < kept; t0 += 2 * step) {
+      fetch(v[1], t0 + step);
       __syncthreads();
-      put(v[0], u0);
-      fetch(v[0], u0 + 2 * kStep);
+      put(v[0], t0);
+      fetch(v[0], t0 + 2 * step);
       __syncthreads();
-      put(v[1], u0 + kStep);
+      put(v[1], t0 + step);
     }
   }
 }
