@@ -289,15 +289,6 @@ int64_t attend_workspace(const AttendPlan &pl) {
 
 constexpr int kEvictSmemTokens = 49152;   // 192 KiB of scores
 
-// Bits and window counts of one row, over all requests.
-struct EvictSizes {
-  long long words, windows;
-};
-EvictSizes evict_sizes(int64_t num_requests, int64_t total_positions, int32_t block_size) {
-  const long long tokens = total_positions * block_size;
-  return {tokens / 32 + num_requests + 1, tokens / kEvictWindow + num_requests + 1};
-}
-
 // As many caches from `lo` on as one launch holds and its grid can number
 // (up to 64 column groups and spans a row).
 struct EvictLaunch {
@@ -335,7 +326,6 @@ int check_evict_caches(const kvcs_cache *caches, int32_t num_caches, int32_t blo
 // Launches follow one another on the stream and share the space.
 int64_t evict_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                         int64_t num_requests, int64_t total_positions) {
-  const EvictSizes s = evict_sizes(num_requests, total_positions, block_size);
   long long rows = 0;
   for (int32_t lo = 0; lo < num_caches;) {
     const EvictLaunch l = evict_launch(caches, lo, num_caches, num_requests);
@@ -343,7 +333,7 @@ int64_t evict_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t bl
     rows = std::max(rows, l.rows);
     lo += l.caches;
   }
-  return rows * (s.words + s.windows) * 4;
+  return rows * total_positions * block_size * 4;
 }
 
 __global__ void __launch_bounds__(1024) kvcs_tickets_kernel(u32 *tickets, int n) {
@@ -556,9 +546,6 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     p.num_blocks = std::min<long long>(p.num_blocks, caches[i].num_blocks);
   int launches = 0;
   p.by_block = FastDiv::of(static_cast<u32>(block_size));
-  const EvictSizes sizes = evict_sizes(reqs->num_requests, total_positions, block_size);
-  p.bit_words = sizes.words;
-  p.windows = sizes.windows;
   // scores in shared memory up to twice the average length; longer rows read
   // them again in every pass
   const int64_t tokens = total_positions * block_size;
@@ -580,7 +567,7 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     const EvictLaunch l = evict_launch(caches, lo, num_caches, reqs->num_requests);
     if (l.caches == 0) return KVCS_EUNSUPPORTED;
     // few rows: each is split by halves and columns of at least 128 bytes, and
-    // into fresh blocks by windows too
+    // into fresh blocks by runs of kept tokens too
     const long long rows = l.rows * reqs->num_requests;
     int parts = 1;
     while (parts < 8 && rows * 2 * parts < 2ll * sms) parts *= 2;
@@ -611,10 +598,9 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     p.spans = 1;
     if (ev->new_block_ids)
       p.spans = static_cast<int>(std::max<int64_t>(
-          1, std::min<int64_t>({average / kEvictWindow, 8ll * sms / units, 64})));
+          1, std::min<int64_t>({average / kEvictChunk, 8ll * sms / units, 64})));
     if (static_cast<double>(units) * p.spans >= 2147483648.0) return KVCS_EUNSUPPORTED;
-    p.bits = static_cast<u32 *>(ev->workspace);
-    p.ahead = p.bits + l.rows * sizes.words;
+    p.list = static_cast<int *>(ev->workspace);
     // large CTAs where the rows are few
     const int threads = rows < 4ll * sms ? kEvictSelectThreads : kEvictSelectThreads / 4;
     kvcs_evict_select_kernel<<<static_cast<unsigned>(rows), threads, p.smem_tokens * 4, st>>>(p);

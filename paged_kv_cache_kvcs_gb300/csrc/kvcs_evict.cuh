@@ -14,11 +14,12 @@
 // tokens: scores (held in shared memory where they fit) become 32-bit keys
 // whose unsigned order is the scores' order, four counting passes over 8-bit
 // digits find the least key kept and how many tokens of exactly that key are,
-// and one pass leaves a bit per token, the count of kept tokens ahead of each
-// window, and the moved scores.  kvcs_evict_move_kernel moves the bytes.  Each
-// 16-byte piece of a token moves independently of the others, so a row is
-// split by halves and columns where rows are few (and, into fresh blocks, by
-// windows); a CTA goes through the kept tokens of its columns in order.
+// and one pass leaves the list of kept tokens and the moved scores.
+// kvcs_evict_move_kernel moves the bytes.  Each 16-byte piece of a token moves
+// independently of the others, so a row is split by halves and columns where
+// rows are few (and, into fresh blocks, by runs of the list); a CTA goes
+// through the kept tokens of its columns in order, the addresses of the next
+// kEvictChunk tokens being worked out while the current ones move.
 //
 // In place: the new token j comes from token src(j) >= j, both growing, so a
 // write never lands on a token that a later step still reads.  A step's
@@ -35,8 +36,8 @@ namespace kvcs {
 
 constexpr int kEvictThreads = 256;
 constexpr int kEvictSelectThreads = 1024;   // at most
-constexpr int kEvictWindow = 1024;   // tokens a step of either kernel looks over
-constexpr int kEvictPieces = 8;      // pieces a thread moves at once
+constexpr int kEvictChunk = 512;     // kept tokens whose addresses are held at once
+constexpr int kEvictPieces = 4;      // pieces a thread moves at once
 
 struct EvictCache {
   PageMap map;
@@ -55,9 +56,7 @@ struct EvictParams {
   const long long *keep;
   const int *new_block_ids;   // or null: in place
   u64 *block_sums;            // or null
-  u32 *bits;                  // [rows][bit_words]: kept tokens
-  u32 *ahead;                 // [rows][windows]: kept tokens before each window
-  long long bit_words, windows;
+  int *list;                  // [rows][total_positions * block_size]: kept tokens
   long long num_blocks;       // smallest pool of the call
   int block_size;
   FastDiv by_block;
@@ -66,7 +65,7 @@ struct EvictParams {
   int rows;                   // (cache, head) pairs of the launch
   int smem_tokens;            // scores that shared memory holds
   int halves_parts;           // most column groups of a row, over both halves
-  int spans;                  // fresh blocks: CTAs that share a row's windows
+  int spans;                  // fresh blocks: CTAs that share a row's list
   EvictCache c[kMaxCachesPerLaunch];
 };
 
@@ -133,12 +132,9 @@ __device__ __forceinline__ const EvictCache &cache_of_row(const EvictParams &p, 
   return p.c[lo];
 }
 
-// Where a request's bits and window counts start.
-__device__ __forceinline__ long long first_word(const EvictParams &p, long long r, const Request &q) {
-  return q.pos0 * p.block_size / 32 + r;
-}
-__device__ __forceinline__ long long first_window(const EvictParams &p, long long r, const Request &q) {
-  return q.pos0 * p.block_size / kEvictWindow + r;
+// Where the list of a row's kept tokens starts.
+__device__ __forceinline__ int *row_list(const EvictParams &p, int row, const Request &q) {
+  return p.list + (row * p.tab.total_positions + q.pos0) * p.block_size;
 }
 
 // Sum of a value over the CTA's threads before this one; *total: over all.
@@ -249,8 +245,7 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
   // counting, then, from the counts before it, marking and moving scores.
   // (Scores that are not held in shared memory are moved by one warp alone,
   // word after word: it reads a word's scores before it writes behind them.)
-  u32 *const bits = p.bits + row * p.bit_words + first_word(p, r, q);
-  u32 *const ahead = p.ahead + row * p.windows + first_window(p, r, q);
+  int *const list = row_list(p, row, q);
   const int words = (N + 31) / 32;
   const int run = held ? (words + warps - 1) / warps : words;
   const int w0 = min(words, held ? warp * run : warp == 0 ? 0 : words), w1 = min(words, w0 + run);
@@ -293,11 +288,11 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
     for (int extra = n - taken(seen, n); extra > 0; --extra) take &= ~(1u << (31 - __clz(take)));
     keep |= take;
     seen += n;
-    if (lane == 0) {
-      bits[w] = keep;
-      if (w % (kEvictWindow / 32) == 0) ahead[w / (kEvictWindow / 32)] = done;
+    if (keep >> lane & 1u) {
+      const int j = done + __popc(keep & ((1u << lane) - 1u));
+      list[j] = w * 32 + lane;
+      *place(to_ids, j) = value;
     }
-    if (keep >> lane & 1u) *place(to_ids, done + __popc(keep & ((1u << lane) - 1u))) = value;
     done += __popc(keep);
     if (!held) __syncwarp();
   }
@@ -306,10 +301,10 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
 template <bool kWords, bool kUnit16>
 __global__ void __launch_bounds__(kEvictThreads)
     kvcs_evict_move_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ long long s_from[kEvictWindow], s_to[kEvictWindow];   // kept tokens' byte offsets
-  __shared__ int s_block[kWords ? kEvictWindow : 1];               // and target blocks
-  __shared__ int s_before[kEvictWindow / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // two chunks' byte offsets of the kept tokens and their targets
+  __shared__ long long s_from[2][kEvictChunk], s_to[2][kEvictChunk];
+  __shared__ int s_block[2][kWords ? kEvictChunk : 1];   // and target blocks
+  const int tid = threadIdx.x, lane = tid & 31;
   long long idx = blockIdx.x;
   const int span = static_cast<int>(idx % p.spans);
   idx /= p.spans;
@@ -324,13 +319,12 @@ __global__ void __launch_bounds__(kEvictThreads)
   Request q;
   int B;
   if (!evict_request(p, r, &q, &B, false)) return;
-  const int bs = p.block_size, N = q.keys;
+  const int bs = p.block_size;
   const int *ids = p.tab.block_ids + q.pos0;
   const int *to_ids = p.new_block_ids ? p.new_block_ids + q.pos0 : ids;
   const bool in_place = to_ids == ids;
-  if (B == 0 || (B == N && in_place && !kWords)) return;
-  const u32 *const bits = p.bits + row * p.bit_words + first_word(p, r, q);
-  const u32 *const ahead = p.ahead + row * p.windows + first_window(p, r, q);
+  if (B == 0 || (B == q.keys && in_place && !kWords)) return;
+  const int *const list = row_list(p, row, q);
   constexpr int kUnit = kUnit16 ? 16 : 8;
   const int piece0 = part * c.part_pieces;
   const int pieces = min(c.part_pieces, c.head_bytes / kUnit - piece0);   // of a token, here
@@ -346,38 +340,46 @@ __global__ void __launch_bounds__(kEvictThreads)
   const u64 piece = static_cast<u64>(half) * (c.head_bytes / 8) + x / 8;
   const PageMap &map = c.map;
 
-  for (int w0 = span * kEvictWindow; w0 < N; w0 += p.spans * kEvictWindow) {
-    // the window's kept tokens: where they are and where they go
-    __syncthreads();   // the lists of the window before are read
-    const int words = min(kEvictWindow / 32, (N - w0 + 31) / 32);
-    if (warp == 0) {
-      const int n = lane < words ? __popc(bits[(w0 >> 5) + lane]) : 0;
-      int sum = n;
+  // addresses of a chunk, in the steps between which other work goes on: the
+  // list, the blocks, and the offsets
+  constexpr int kOwn = kEvictChunk / kEvictThreads;
+  int src[kOwn], from_id[kOwn], to_id[kOwn];
+  auto look_list = [&](int j0) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += u;
-      }
-      s_before[lane] = sum - n;
+    for (int i = 0; i < kOwn; ++i) {
+      const int j = j0 + i * kEvictThreads + tid;
+      src[i] = j < B ? list[j] : -1;
     }
-    __syncthreads();
-    const int done = static_cast<int>(ahead[w0 / kEvictWindow]);
+  };
+  auto look_blocks = [&](int j0) {
 #pragma unroll
-    for (int i = 0; i < kEvictWindow / kEvictThreads; ++i) {
-      const int g = i * (kEvictThreads / 32) + warp;
-      const u32 k = g < words ? bits[(w0 >> 5) + g] : 0u;
-      if (k >> lane & 1u) {
-        const int at = s_before[g] + __popc(k & ((1u << lane) - 1u));
-        const int src = w0 + g * 32 + lane, sp = p.by_block(src);
-        const int j = done + at, dp = p.by_block(j);
-        const int to = to_ids[dp];
-        s_from[at] = token_offset(map, ids[sp], src - sp * bs, head);
-        s_to[at] = token_offset(map, to, j - dp * bs, head);
-        if (kWords) s_block[at] = to;
-      }
+    for (int i = 0; i < kOwn; ++i) {
+      if (src[i] < 0) continue;
+      from_id[i] = ids[p.by_block(src[i])];
+      to_id[i] = to_ids[p.by_block(j0 + i * kEvictThreads + tid)];
     }
-    const int kept = s_before[words - 1] + __popc(bits[(w0 >> 5) + words - 1]);
-    __syncthreads();
+  };
+  auto note = [&](int buf, int j0) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      if (src[i] < 0) continue;
+      const int at = i * kEvictThreads + tid, j = j0 + at;
+      s_from[buf][at] = token_offset(map, from_id[i], src[i] - p.by_block(src[i]) * bs, head);
+      s_to[buf][at] = token_offset(map, to_id[i], j - p.by_block(j) * bs, head);
+      if (kWords) s_block[buf][at] = to_id[i];
+    }
+  };
+  const int stride = p.spans * kEvictChunk;
+  int buf = 0;
+  look_list(span * kEvictChunk);
+  look_blocks(span * kEvictChunk);
+  note(0, span * kEvictChunk);
+  for (int j0 = span * kEvictChunk; j0 < B; j0 += stride, buf ^= 1) {
+    const int kept = min(kEvictChunk, B - j0), done = j0;
+    __syncthreads();   // the chunk's addresses are there
+    look_list(j0 + stride);
+    const long long *const from_at = s_from[buf], *const to_at = s_to[buf];
+    const int *const block_at = s_block[buf];
     uint4 v[2][kEvictPieces];
     auto fetch = [&](uint4 (&d)[kEvictPieces], int t0) {
       const int t = t0 + slot * kEvictPieces;
@@ -385,8 +387,8 @@ __global__ void __launch_bounds__(kEvictThreads)
       for (int i = 0; i < kEvictPieces; ++i) {
         if (!active || t + i >= kept) continue;
         // tokens that stay where they are pass through only for their words
-        if (!kWords && s_from[t + i] == s_to[t + i]) continue;
-        const unsigned char *from = base + s_from[t + i];
+        if (!kWords && from_at[t + i] == to_at[t + i]) continue;
+        const unsigned char *from = base + from_at[t + i];
         if (kUnit16) {
           d[i] = *reinterpret_cast<const uint4 *>(from);
         } else {
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(kEvictThreads)
       const int t = t0 + slot * kEvictPieces;
 #pragma unroll
       for (int i = 0; i < kEvictPieces; ++i) {
-        if (!active || t + i >= kept || s_from[t + i] == s_to[t + i]) continue;
-        unsigned char *to = base + s_to[t + i];
+        if (!active || t + i >= kept || from_at[t + i] == to_at[t + i]) continue;
+        unsigned char *to = base + to_at[t + i];
         if (kUnit16)
           *reinterpret_cast<uint4 *>(to) = d[i];
         else
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kEvictThreads)
 #pragma unroll
         for (int i = 0; i < kEvictPieces; ++i) {
           const bool in = active && t + i < kept;
-          const int b = in ? s_block[t + i] : block;
+          const int b = in ? block_at[t + i] : block;
           if (__any_sync(0xffffffffu, b != block && block >= 0)) {
             flush();
             sum = 0;
@@ -442,14 +444,16 @@ __global__ void __launch_bounds__(kEvictThreads)
     };
     const int step = tokens * kEvictPieces;
     fetch(v[0], 0);
+    look_blocks(j0 + stride);
     for (int t0 = 0; t0 < kept; t0 += 2 * step) {
       fetch(v[1], t0 + step);
-      __syncthreads();
+      if (in_place) __syncthreads();
       put(v[0], t0);
       fetch(v[0], t0 + 2 * step);
-      __syncthreads();
+      if (in_place) __syncthreads();
       put(v[1], t0 + step);
     }
+    note(buf ^ 1, j0 + stride);
   }
 }
 
