@@ -549,7 +549,7 @@ typedef struct kvcs_eviction {
 /*
  * kvcs_eviction_workspace -- bytes of workspace a kvcs_evict call with these
  * caches and sizes needs: 4 bytes per listed token and KV head of the caches
- * that one launch takes (up to 128), as the scores take.
+ * that one launch takes (up to 32), as the scores take.
  * Returns the error codes of kvcs_evict for bad caches and sizes.
  */
 int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,

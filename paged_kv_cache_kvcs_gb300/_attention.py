@@ -24,18 +24,39 @@ def _stream_handle(stream, dev) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _checked(name: str, t, dtype, n: int, index: int):
+    """The address of ``t`` after ``_binding._check_tensor``'s checks (made
+    here first in the shortest way: a decode step makes a dozen of them)."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.numel() >= n and \
+            t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
+    B._check_tensor(name, t, (dtype,), n, torch.device("cuda", index))
+    return t.data_ptr()
+
+
+def _tables(pos_offsets, first_position, num_tokens, block_ids, total_positions):
+    """The checked request table, its request count and position count, and
+    the current device's index."""
+    total = _total(total_positions, pos_offsets)
+    index = B._current_device().index
+    R = pos_offsets.numel() - 1
+    if not (type(pos_offsets) is type(num_tokens) is type(first_position) is torch.Tensor
+            and num_tokens.numel() == R == first_position.numel() and total >= 0):
+        B._check_requests(pos_offsets, first_position, num_tokens, block_ids, total)
+    i64 = torch.int64
+    reqs = B.kvcs_requests(R, _checked("pos_offsets", pos_offsets, i64, max(R, 0) + 1, index),
+                           _checked("first_position", first_position, i64, R, index),
+                           _checked("num_tokens", num_tokens, i64, R, index),
+                           _checked("block_ids", block_ids, torch.int32, total, index))
+    return reqs, R, total, index
+
+
 def _total(total_positions, pos_offsets) -> int:
     if total_positions is not None:
         return total_positions
     if not getattr(pos_offsets, "is_cuda", False) or pos_offsets.numel() < 1:
         raise ValueError("pos_offsets must be a CUDA int64 tensor of num_requests + 1")
     return int(pos_offsets[-1].item())
-
-
-def _requests(pos_offsets, first_position, num_tokens, block_ids):
-    return B.kvcs_requests(pos_offsets.numel() - 1, pos_offsets.data_ptr(),
-                           first_position.data_ptr(), num_tokens.data_ptr(),
-                           block_ids.data_ptr())
 
 
 def _raise(rc: int, where: str) -> None:
@@ -55,48 +76,39 @@ def _workspace(given, n: int, stream, handle: int, dev):
         return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
-def _queries(cache, q, new_offsets, num_requests, kv_dtype, dev):
-    """Checks q and new_offsets; returns a kvcs_attention with their fields."""
+def _attention_args(cache, q, new_offsets, R, index, kv_dtype, scale, softcap, window, k_scale,
+                    v_scale, max_new, out=None, lse=None, observe=0):
+    """Checks q and new_offsets and packs a kvcs_attention."""
     if not (getattr(q, "is_cuda", False) and q.dim() == 3):
         raise ValueError("q must be a CUDA tensor [total_new, q_heads, head_dim]")
-    if q.dtype not in _Q_DTYPES:
+    q_dtype = _Q_DTYPES.get(q.dtype)
+    if q_dtype is None:
         raise ValueError("q must be a torch.bfloat16 or torch.float16 tensor")
-    if q.device != dev:
-        raise ValueError(f"q is on {q.device}, the call runs on {dev}")
+    if q.device.index != index:
+        raise ValueError(f"q is on {q.device}, the call runs on cuda:{index}")
     total_new, q_heads, dim = q.shape
     if kv_dtype is None:
         pool = getattr(cache.pool, "dtype", torch.uint8)
         kv_dtype = pool if pool in _KV_DTYPES else q.dtype
-    if kv_dtype not in _KV_DTYPES:
+    kv = _KV_DTYPES.get(kv_dtype)
+    if kv is None:
         raise ValueError("kv_dtype must be torch.bfloat16, torch.float16 or torch.float8_e4m3fn")
-    element = 1 if kv_dtype == torch.float8_e4m3fn else 2
+    element = 1 if kv == B.KVCS_DTYPE_FP8_E4M3 else 2
     if dim * element != cache.head_bytes:
         raise ValueError(f"q has heads of {dim} elements, the cache of "
                          f"{cache.head_bytes // element}")
-    if total_new > 0 and (q.stride(2) != 1 or (q_heads > 1 and q.stride(1) != dim)
-                          or (total_new > 1 and q.stride(0) < q_heads * dim)):
+    row, head, step = q.stride(0), q.stride(1), q.stride(2)
+    if total_new > 0 and (step != 1 or (q_heads > 1 and head != dim)
+                          or (total_new > 1 and row < q_heads * dim)):
         raise ValueError("q's heads must be packed within a token")
-    B._check_tensor("new_offsets", new_offsets, (torch.int64,), num_requests + 1, dev)
-    if new_offsets.numel() != num_requests + 1:
-        raise ValueError(f"new_offsets must hold num_requests + 1 elements ({num_requests + 1})")
-    a = B.kvcs_attention()
-    a.q = q.data_ptr()
-    a.q_stride = q.stride(0) if total_new > 1 else 0
-    a.new_offsets = new_offsets.data_ptr()
-    a.total_new = total_new
-    a.q_heads = q_heads
-    a.q_dtype = _Q_DTYPES[q.dtype]
-    a.kv_dtype = _KV_DTYPES[kv_dtype]
-    return a
-
-
-def _scores(a, dim, scale, softcap, window, k_scale, v_scale, max_new) -> None:
-    a.scale = dim ** -0.5 if scale is None else scale
-    a.softcap = softcap
-    a.window = window
-    a.k_scale = k_scale
-    a.v_scale = v_scale
-    a.max_new = min(max_new, a.total_new) if max_new is not None else 0
+    new = _checked("new_offsets", new_offsets, torch.int64, R + 1, index)
+    if new_offsets.numel() != R + 1:
+        raise ValueError(f"new_offsets must hold num_requests + 1 elements ({R + 1})")
+    return B.kvcs_attention(
+        q.data_ptr(), row if total_new > 1 else 0, new, total_new,
+        0 if max_new is None else min(max_new, total_new), q_heads, q_dtype, kv,
+        dim ** -0.5 if scale is None else scale, softcap, k_scale, v_scale, window, out, lse, None,
+        0, observe)
 
 
 def attention_workspace_bytes(cache, block_size: int, num_requests: int, total_positions: int, q,
@@ -106,8 +118,8 @@ def attention_workspace_bytes(cache, block_size: int, num_requests: int, total_p
     (``kvcs_attention_workspace``)."""
     dev = B._current_device()
     offsets = torch.empty(num_requests + 1, dtype=torch.int64, device=dev)
-    a = _queries(cache, q, offsets, num_requests, kv_dtype, dev)
-    _scores(a, q.shape[2], None, 0.0, 0, 1.0, 1.0, max_new)
+    a = _attention_args(cache, q, offsets, num_requests, dev.index, kv_dtype, None, 0.0, 0, 1.0, 1.0,
+                        max_new)
     n = ctypes.c_int64()
     _raise(B.load_library().kvcs_attention_workspace(
         B.cache_array([cache]), block_size, num_requests, total_positions, ctypes.byref(a), 0,
@@ -137,35 +149,33 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     ``[total_new, q_heads]``.
     """
     B._check_pool(cache, block_size)
-    total_positions = _total(total_positions, pos_offsets)
-    dev = B._check_requests(pos_offsets, first_position, num_tokens, block_ids, total_positions)
-    R = pos_offsets.numel() - 1
-    a = _queries(cache, q, new_offsets, R, kv_dtype, dev)
-    _scores(a, q.shape[2], scale, softcap, window, k_scale, v_scale, max_new)
+    reqs, R, total, index = _tables(pos_offsets, first_position, num_tokens, block_ids,
+                                    total_positions)
+    a = _attention_args(cache, q, new_offsets, R, index, kv_dtype, scale, softcap, window, k_scale,
+                        v_scale, max_new)
+    dev = q.device
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        a.out = out.data_ptr()
     else:
-        B._check_tensor("out", out, (q.dtype,), q.numel(), dev)
-    rows = q.shape[0] * q.shape[1]
+        a.out = _checked("out", out, q.dtype, q.numel(), index)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        a.lse = lse.data_ptr()
     else:
-        B._check_tensor("lse", lse, (torch.float32,), rows, dev)
+        a.lse = _checked("lse", lse, torch.float32, q.shape[0] * q.shape[1], index)
     B._check_status(status, dev)
-    a.out = out.data_ptr()
-    a.lse = lse.data_ptr()
     lib = B.load_library()
-    arr = B.cache_array([cache])
+    arr = B.cache_array((cache,))
     n = ctypes.c_int64()
     a_ref = ctypes.byref(a)
-    _raise(lib.kvcs_attention_workspace(arr, block_size, R, total_positions, a_ref, 0, ctypes.byref(n)),
+    _raise(lib.kvcs_attention_workspace(arr, block_size, R, total, a_ref, 0, ctypes.byref(n)),
            "kvcs_attention_workspace")
     handle = _stream_handle(stream, dev)
     workspace = _workspace(workspace, n.value, stream, handle, dev)
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel()
-    reqs = _requests(pos_offsets, first_position, num_tokens, block_ids)
-    _raise(lib.kvcs_paged_attention(arr, block_size, ctypes.byref(reqs), total_positions, a_ref,
+    _raise(lib.kvcs_paged_attention(arr, block_size, ctypes.byref(reqs), total, a_ref,
                                     B._ptr(status), handle), "kvcs_paged_attention")
     return out, lse
 
@@ -181,21 +191,16 @@ def attention_mass(cache, block_size: int, pos_offsets, first_position, num_toke
     ``q``, ``new_offsets`` and the score arguments as in ``paged_attention``,
     ``lse`` as that call returned it.  Returns ``mass``."""
     B._check_pool(cache, block_size)
-    total_positions = _total(total_positions, pos_offsets)
-    dev = B._check_requests(pos_offsets, first_position, num_tokens, block_ids, total_positions)
-    R = pos_offsets.numel() - 1
-    a = _queries(cache, q, new_offsets, R, kv_dtype, dev)
-    _scores(a, q.shape[2], scale, softcap, window, k_scale, 1.0, max_new)
-    a.observe = observe
-    B._check_tensor("lse", lse, (torch.float32,), q.shape[0] * q.shape[1], dev)
-    B._check_tensor("mass", mass, (torch.float32,),
-                    cache.num_blocks * cache.num_heads * block_size, dev)
-    B._check_status(status, dev)
-    a.lse = lse.data_ptr()
-    reqs = _requests(pos_offsets, first_position, num_tokens, block_ids)
+    reqs, R, total, index = _tables(pos_offsets, first_position, num_tokens, block_ids,
+                                    total_positions)
+    a = _attention_args(cache, q, new_offsets, R, index, kv_dtype, scale, softcap, window, k_scale,
+                        1.0, max_new, observe=observe)
+    a.lse = _checked("lse", lse, torch.float32, q.shape[0] * q.shape[1], index)
+    at = _checked("mass", mass, torch.float32, cache.num_blocks * cache.num_heads * block_size, index)
+    B._check_status(status, q.device)
     _raise(B.load_library().kvcs_attention_mass(
-        B.cache_array([cache]), block_size, ctypes.byref(reqs), total_positions, ctypes.byref(a),
-        mass.data_ptr(), B._ptr(status), _stream_handle(stream, dev)), "kvcs_attention_mass")
+        B.cache_array((cache,)), block_size, ctypes.byref(reqs), total, ctypes.byref(a), at,
+        B._ptr(status), _stream_handle(stream, q.device)), "kvcs_attention_mass")
     return mass
 
 
@@ -226,26 +231,28 @@ def evict(caches: Sequence, block_size: int, pos_offsets, first_position, num_to
         raise ValueError("scores must hold one tensor per cache")
     for c in caches:
         B._check_pool(c, block_size)
-    total_positions = _total(total_positions, pos_offsets)
-    dev = B._check_requests(pos_offsets, first_position, num_tokens, block_ids, total_positions)
-    for c, t in zip(caches, scores):
-        B._check_tensor("scores", t, (torch.float32,), c.num_blocks * c.num_heads * block_size, dev)
-    B._check_tensor("keep", keep, (torch.int64,), pos_offsets.numel() - 1, dev)
+    reqs, R, total, index = _tables(pos_offsets, first_position, num_tokens, block_ids,
+                                    total_positions)
+    dev = torch.device("cuda", index)
+    at = [_checked("scores", t, torch.float32, c.num_blocks * c.num_heads * block_size, index)
+          for c, t in zip(caches, scores)]
+    ev = B.kvcs_eviction((ctypes.c_void_p * max(1, len(caches)))(*at),
+                         _checked("keep", keep, torch.int64, R, index), sinks, recent, None, None,
+                         None, 0)
     if new_block_ids is not None:
-        B._check_tensor("new_block_ids", new_block_ids, (torch.int32,), total_positions, dev)
+        ev.new_block_ids = _checked("new_block_ids", new_block_ids, torch.int32, total, index)
     if block_sums is not None:
         B._check_tensor("block_sums", block_sums, B._words(),
                         min(c.num_blocks for c in caches), dev)
+        ev.block_sums = block_sums.data_ptr()
     B._check_status(status, dev)
-    ptrs = (ctypes.c_void_p * max(1, len(caches)))(*[t.data_ptr() for t in scores])
-    lib, arr, R = B.load_library(), B.cache_array(caches), pos_offsets.numel() - 1
+    lib, arr = B.load_library(), B.cache_array(caches)
     n = ctypes.c_int64()
-    _raise(lib.kvcs_eviction_workspace(arr, len(caches), block_size, R, total_positions,
-                                       ctypes.byref(n)), "kvcs_eviction_workspace")
+    _raise(lib.kvcs_eviction_workspace(arr, len(caches), block_size, R, total, ctypes.byref(n)),
+           "kvcs_eviction_workspace")
     handle = _stream_handle(stream, dev)
     workspace = _workspace(workspace, n.value, stream, handle, dev)
-    ev = B.kvcs_eviction(ptrs, keep.data_ptr(), sinks, recent, B._ptr(new_block_ids),
-                         B._ptr(block_sums), workspace.data_ptr(), workspace.numel())
-    reqs = _requests(pos_offsets, first_position, num_tokens, block_ids)
-    _raise(lib.kvcs_evict(arr, len(caches), block_size, ctypes.byref(reqs), total_positions,
-                          ctypes.byref(ev), B._ptr(status), handle), "kvcs_evict")
+    ev.workspace = workspace.data_ptr()
+    ev.workspace_bytes = workspace.numel()
+    _raise(lib.kvcs_evict(arr, len(caches), block_size, ctypes.byref(reqs), total, ctypes.byref(ev),
+                          B._ptr(status), handle), "kvcs_evict")

@@ -298,7 +298,7 @@ struct EvictLaunch {
 EvictLaunch evict_launch(const kvcs_cache *caches, int32_t lo, int32_t num_caches,
                          int64_t num_requests) {
   EvictLaunch l = {0, 0};
-  while (lo + l.caches < num_caches && l.caches < kMaxCachesPerLaunch) {
+  while (lo + l.caches < num_caches && l.caches < kEvictCaches) {
     const long long rows = l.rows + caches[lo + l.caches].num_heads;
     if (static_cast<double>(rows) * num_requests * 16.0 >= 2147483648.0) break;
     l.rows = rows;
@@ -334,6 +334,68 @@ int64_t evict_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t bl
     lo += l.caches;
   }
   return rows * total_positions * block_size * 4;
+}
+
+// The launches over one group of caches; returns how many, or an error code.
+template <int kCaches>
+int launch_evict(const EvictCall &call, const kvcs_cache *caches, float *const *scores,
+                 long long rows, int parts, int64_t average, int sms, cudaStream_t st) {
+  EvictParams<kCaches> p;
+  static_cast<EvictCall &>(p) = call;
+  p.halves_parts = 1;
+  long long first = 0;
+  for (int n = 0; n < p.num_caches; ++n) {
+    const kvcs_cache &c = caches[n];
+    EvictCache &e = p.c[n];
+    e.map = page_map(c, p.block_size);
+    e.scores = scores[n];
+    e.m0 = 2ull * (static_cast<u64>(c.layer) * KVCS_MAX_KV_HEADS_PER_LAYER + c.head_offset) + 1;
+    e.heads = c.num_heads;
+    e.head_bytes = c.head_bytes;
+    e.first_row = static_cast<int>(first);
+    e.unit = needs_8(c) ? 8 : 16;
+    const int pieces = c.head_bytes / e.unit;
+    const int least = std::max(1, 128 / e.unit);
+    // (at most a thread per piece)
+    e.part_pieces = std::min(kEvictThreads, std::max(std::min(least, pieces),
+                                                     (pieces + parts - 1) / parts));
+    e.parts = (pieces + e.part_pieces - 1) / e.part_pieces;
+    p.halves_parts = std::max(p.halves_parts, e.map.halves * e.parts);
+    first += c.num_heads;
+  }
+  const long long units = rows * p.halves_parts;
+  p.spans = 1;
+  if (p.new_block_ids)
+    p.spans = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>({average / kEvictChunk, 8ll * sms / units, 64})));
+  if (static_cast<double>(units) * p.spans >= 2147483648.0) return KVCS_EUNSUPPORTED;
+  // (short rows need no leave for more than the standard 48 KiB)
+  if (p.smem_tokens * 4 > 32768 &&
+      cudaFuncSetAttribute(reinterpret_cast<const void *>(kvcs_evict_select_kernel<kCaches>),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kEvictSmemTokens * 4) != cudaSuccess)
+    return KVCS_ECUDA;
+  // large CTAs where the rows are few
+  const int threads = rows < 4ll * sms ? kEvictSelectThreads : kEvictSelectThreads / 4;
+  kvcs_evict_select_kernel<kCaches>
+      <<<static_cast<unsigned>(rows), threads, p.smem_tokens * 4, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+  int launches = 1;
+  // a launch for the caches of either piece size
+  bool has[2] = {false, false};
+  for (int n = 0; n < p.num_caches; ++n) has[p.c[n].unit == 16] = true;
+  const dim3 grid(static_cast<unsigned>(units * p.spans));
+  for (int u = 0; u < 2; ++u) {
+    if (!has[u]) continue;
+    auto move = p.block_sums ? (u ? kvcs_evict_move_kernel<kCaches, true, true>
+                                  : kvcs_evict_move_kernel<kCaches, true, false>)
+                             : (u ? kvcs_evict_move_kernel<kCaches, false, true>
+                                  : kvcs_evict_move_kernel<kCaches, false, false>);
+    move<<<grid, kEvictThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
+    ++launches;
+  }
+  return launches;
 }
 
 __global__ void __launch_bounds__(1024) kvcs_tickets_kernel(u32 *tickets, int n) {
@@ -526,7 +588,7 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  EvictParams p;
+  EvictCall p;
   std::memset(&p, 0, sizeof(p));
   p.tab.pos_offsets = reinterpret_cast<const long long *>(reqs->pos_offsets);
   p.tab.first_position = reinterpret_cast<const long long *>(reqs->first_position);
@@ -559,10 +621,6 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
     ++launches;
   }
-  if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kvcs_evict_select_kernel),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kEvictSmemTokens * 4) != cudaSuccess)
-    return KVCS_ECUDA;
   for (int32_t lo = 0; lo < num_caches;) {
     const EvictLaunch l = evict_launch(caches, lo, num_caches, reqs->num_requests);
     if (l.caches == 0) return KVCS_EUNSUPPORTED;
@@ -573,52 +631,14 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
     while (parts < 8 && rows * 2 * parts < 2ll * sms) parts *= 2;
     p.num_caches = l.caches;
     p.rows = static_cast<int>(l.rows);
-    p.halves_parts = 1;
-    long long first = 0;
-    for (int n = 0; n < l.caches; ++n) {
-      const kvcs_cache &c = caches[lo + n];
-      EvictCache &e = p.c[n];
-      e.map = page_map(c, block_size);
-      e.scores = ev->scores[lo + n];
-      e.m0 = 2ull * (static_cast<u64>(c.layer) * KVCS_MAX_KV_HEADS_PER_LAYER + c.head_offset) + 1;
-      e.heads = c.num_heads;
-      e.head_bytes = c.head_bytes;
-      e.first_row = static_cast<int>(first);
-      e.unit = needs_8(c) ? 8 : 16;
-      const int pieces = c.head_bytes / e.unit;
-      const int least = std::max(1, 128 / e.unit);
-      // (at most a thread per piece)
-      e.part_pieces = std::min(kEvictThreads, std::max(std::min(least, pieces),
-                                                       (pieces + parts - 1) / parts));
-      e.parts = (pieces + e.part_pieces - 1) / e.part_pieces;
-      p.halves_parts = std::max(p.halves_parts, e.map.halves * e.parts);
-      first += c.num_heads;
-    }
-    const long long units = rows * p.halves_parts;
-    p.spans = 1;
-    if (ev->new_block_ids)
-      p.spans = static_cast<int>(std::max<int64_t>(
-          1, std::min<int64_t>({average / kEvictChunk, 8ll * sms / units, 64})));
-    if (static_cast<double>(units) * p.spans >= 2147483648.0) return KVCS_EUNSUPPORTED;
     p.list = static_cast<int *>(ev->workspace);
-    // large CTAs where the rows are few
-    const int threads = rows < 4ll * sms ? kEvictSelectThreads : kEvictSelectThreads / 4;
-    kvcs_evict_select_kernel<<<static_cast<unsigned>(rows), threads, p.smem_tokens * 4, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-    ++launches;
-    // a launch for the caches of either piece size
-    bool has[2] = {false, false};
-    for (int n = 0; n < l.caches; ++n) has[p.c[n].unit == 16] = true;
-    const dim3 grid(static_cast<unsigned>(units * p.spans));
-    for (int u = 0; u < 2; ++u) {
-      if (!has[u]) continue;
-      auto move = p.block_sums
-                      ? (u ? kvcs_evict_move_kernel<true, true> : kvcs_evict_move_kernel<true, false>)
-                      : (u ? kvcs_evict_move_kernel<false, true> : kvcs_evict_move_kernel<false, false>);
-      move<<<grid, kEvictThreads, 0, st>>>(p);
-      if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-      ++launches;
-    }
+    const int done = l.caches <= kEvictFewCaches
+                         ? launch_evict<kEvictFewCaches>(p, caches + lo, ev->scores + lo, rows, parts,
+                                                         average, sms, st)
+                         : launch_evict<kEvictCaches>(p, caches + lo, ev->scores + lo, rows, parts,
+                                                      average, sms, st);
+    if (done < 0) return done;
+    launches += done;
     lo += l.caches;
   }
   count_launches(launches);

@@ -1,11 +1,28 @@
 // kvcs_attend_type.cu -- the attention and attention-mass kernels of one
 // cache type (KVCS_KV_TYPE), compiled once per type.
 
+#include <atomic>
+
 #include "kvcs_attend_host.h"
 
 namespace kvcs {
 
 constexpr int kThisType = KVCS_KV_TYPE;
+
+// Lets a kernel use `bytes` of shared memory, once per device and kernel (a
+// failure is not remembered).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<u64> *done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done->load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
 
 // Everything is a template over the type: the three objects share one
 // namespace.
@@ -23,9 +40,8 @@ struct TypeLaunch {
   template <int kDim, bool kWide>
   static cudaError_t attend(const AttnParams &p, int grid, bool after_zero, cudaStream_t st) {
     constexpr int smem = AttendShape<kType, kDim>::kSmemBytes;
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void *>(kvcs_attend_kernel<kType, kDim, kWide>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<u64> done{0};
+    const cudaError_t e = allow_smem(kvcs_attend_kernel<kType, kDim, kWide>, smem, &done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -48,8 +64,8 @@ struct TypeLaunch {
     } else {
       auto kernel = kvcs_attend_tc_kernel<kType == kKvBf16, kDim, kPlain>;
       constexpr int smem = TcShape<kDim>::kSmemBytes;
-      const cudaError_t e = cudaFuncSetAttribute(
-          reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      static std::atomic<u64> done{0};
+      const cudaError_t e = allow_smem(kernel, smem, &done);
       if (e != cudaSuccess) return e;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -79,8 +95,8 @@ struct TypeLaunch {
     } else {
       auto kernel = kvcs_mass_tc_kernel<kType == kKvBf16, kDim, kPlain>;
       constexpr int smem = MtShape<kDim>::kSmemBytes;
-      const cudaError_t e = cudaFuncSetAttribute(
-          reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      static std::atomic<u64> done{0};
+      const cudaError_t e = allow_smem(kernel, smem, &done);
       if (e != cudaSuccess) return e;
       kernel<<<static_cast<unsigned>(grid), kTcThreads, smem, st>>>(p, k, q);
       return cudaGetLastError();

@@ -51,7 +51,12 @@ struct EvictCache {
   int part_pieces;    // pieces of a column group (the last may hold fewer)
 };
 
-struct EvictParams {
+// Caches of one launch, at most.  (The parameters travel with every launch:
+// 25 KB of them, room for 128 caches, took a launch 10 us on the host.)
+constexpr int kEvictCaches = 32;
+constexpr int kEvictFewCaches = 2;
+
+struct EvictCall {
   Tables tab;
   const long long *keep;
   const int *new_block_ids;   // or null: in place
@@ -66,7 +71,11 @@ struct EvictParams {
   int smem_tokens;            // scores that shared memory holds
   int halves_parts;           // most column groups of a row, over both halves
   int spans;                  // fresh blocks: CTAs that share a row's list
-  EvictCache c[kMaxCachesPerLaunch];
+};
+
+template <int kCaches>
+struct EvictParams : EvictCall {
+  EvictCache c[kCaches];
 };
 
 // Unsigned keys in the order of the scores; -0 equals 0, every NaN is the
@@ -80,7 +89,7 @@ __device__ __forceinline__ u32 score_key(u32 bits) {
 
 // Tokens and budget of a request; false when it is to be left alone (bad
 // tables or block ids, which are flagged if `report`).  Called by a whole CTA.
-__device__ inline bool evict_request(const EvictParams &p, long long r, Request *q, int *budget,
+__device__ inline bool evict_request(const EvictCall &p, long long r, Request *q, int *budget,
                                      bool report) {
   const long long a = p.tab.pos_offsets[r], b = p.tab.pos_offsets[r + 1];
   const bool speak = report && threadIdx.x == 0;
@@ -110,7 +119,7 @@ __device__ inline bool evict_request(const EvictParams &p, long long r, Request 
 
 // Zeroes the checksum words of the blocks the call fills (in place: of every
 // block that held a token).
-__global__ void __launch_bounds__(256) kvcs_evict_zero_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(256) kvcs_evict_zero_kernel(const __grid_constant__ EvictCall p) {
   for (long long r = blockIdx.x; r < p.tab.num_requests; r += gridDim.x) {
     Request q;
     int budget;
@@ -123,7 +132,8 @@ __global__ void __launch_bounds__(256) kvcs_evict_zero_kernel(const __grid_const
 }
 
 // The cache of a launch's (cache, head) row.
-__device__ __forceinline__ const EvictCache &cache_of_row(const EvictParams &p, int row) {
+template <int kCaches>
+__device__ __forceinline__ const EvictCache &cache_of_row(const EvictParams<kCaches> &p, int row) {
   int lo = 0, hi = p.num_caches - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -133,7 +143,7 @@ __device__ __forceinline__ const EvictCache &cache_of_row(const EvictParams &p, 
 }
 
 // Where the list of a row's kept tokens starts.
-__device__ __forceinline__ int *row_list(const EvictParams &p, int row, const Request &q) {
+__device__ __forceinline__ int *row_list(const EvictCall &p, int row, const Request &q) {
   return p.list + (row * p.tab.total_positions + q.pos0) * p.block_size;
 }
 
@@ -163,8 +173,9 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sums, int *total) {
 // Digits of the counting passes: 11, 11 and 10 bits from the top.
 constexpr int kEvictBins = 2048;
 
+template <int kCaches>
 __global__ void __launch_bounds__(kEvictSelectThreads)
-    kvcs_evict_select_kernel(const __grid_constant__ EvictParams p) {
+    kvcs_evict_select_kernel(const __grid_constant__ EvictParams<kCaches> p) {
   extern __shared__ u32 s_score[];   // the row's scores, if they fit
   __shared__ u32 s_hist[kEvictBins];
   __shared__ int s_sums[32];
@@ -298,9 +309,9 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
   }
 }
 
-template <bool kWords, bool kUnit16>
+template <int kCaches, bool kWords, bool kUnit16>
 __global__ void __launch_bounds__(kEvictThreads)
-    kvcs_evict_move_kernel(const __grid_constant__ EvictParams p) {
+    kvcs_evict_move_kernel(const __grid_constant__ EvictParams<kCaches> p) {
   // two chunks' byte offsets of the kept tokens and their targets
   __shared__ long long s_from[2][kEvictChunk], s_to[2][kEvictChunk];
   __shared__ int s_block[2][kWords ? kEvictChunk : 1];   // and target blocks
