@@ -128,6 +128,8 @@ AttnParams attn_params(const kvcs_cache *cache, int32_t block_size, const kvcs_r
   p.window = static_cast<int>(a->window < kMaxRequestTokens ? a->window : 0);
   p.observe = static_cast<int>(std::min<int64_t>(a->observe, kMaxRequestTokens));
   p.unit8 = needs_8(*cache) ? 1 : 0;
+  p.runs = !p.unit8 && p.map.kbs % 16 == 0 &&
+           (p.head_dim == 64 || p.head_dim == 128 || p.head_dim == 256);
   p.row_lo = 1;
   p.row_hi = 0x7fffffff;
   const float s = a->scale * a->k_scale;

@@ -138,21 +138,25 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int pg = (g >> 1) | ((g & 1) << 2);   // key (and V chunk) of lane group g
   float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // (two chains of products each)
+  // Piece 4 b + t of row pg (or pg + 8) lies at piece (4 b + t) ^ (row & mask):
+  // two places, for even and odd b, from which the others differ by constants.
+  const u32 k_even = ks + pg * S::kRowBytes + ((t ^ (pg & kMask)) << 4);
+  const u32 k_odd = ks + pg * S::kRowBytes + (((t + 4) ^ (pg & kMask)) << 4);
   if constexpr (kType == kKvFp8) {
 #pragma unroll
     for (int b = 0; b < kDim / 64; ++b) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = j * 8 + pg;
-        const uint4 k = lds128(ks + row * S::kRowBytes + (((4 * b + t) ^ (row & kMask)) << 4));
+        const uint4 k = lds128((b & 1 ? k_odd : k_even) + (b >> 1) * 128 + j * 8 * S::kRowBytes);
         const u32 w[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           u32 lo, hi;
           fp8x4_to_half(w[i], lo, hi);
           const int step = 4 * b + i;
-          mma16816<false>(s[j], qf[2 * step][0], qf[2 * step][1], qf[2 * step + 1][0],
-                          qf[2 * step + 1][1], lo, hi);
+          mma16816<false>(i & 1 ? s2[j] : s[j], qf[2 * step][0], qf[2 * step][1],
+                          qf[2 * step + 1][0], qf[2 * step + 1][1], lo, hi);
         }
       }
     }
@@ -161,11 +165,10 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
     for (int b = 0; b < kDim / 32; ++b) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = j * 8 + pg;
-        const uint4 k = lds128(ks + row * S::kRowBytes + (((4 * b + t) ^ (row & kMask)) << 4));
+        const uint4 k = lds128((b & 1 ? k_odd : k_even) + (b >> 1) * 128 + j * 8 * S::kRowBytes);
         mma16816<kBf16>(s[j], qf[4 * b][0], qf[4 * b][1], qf[4 * b + 1][0], qf[4 * b + 1][1], k.x,
                         k.y);
-        mma16816<kBf16>(s[j], qf[4 * b + 2][0], qf[4 * b + 2][1], qf[4 * b + 3][0],
+        mma16816<kBf16>(s2[j], qf[4 * b + 2][0], qf[4 * b + 2][1], qf[4 * b + 3][0],
                         qf[4 * b + 3][1], k.z, k.w);
       }
     }
@@ -173,7 +176,17 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[j][i] = score_of(p, s[j][i], rs[i >> 1]);
+    for (int i = 0; i < 4; ++i) s[j][i] += s2[j][i];
+  // scores = sc * s; capped ones, and those of a scale that would turn the
+  // maximum round or make 0 of a masked score, are made first
+  float sc[2] = {rs[0] * p.scale, rs[1] * p.scale};
+  if (p.cap != 0.0f || p.scale <= 0.0f) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[j][i] = score_of(p, s[j][i], rs[i >> 1]);
+    sc[0] = sc[1] = 1.0f;
+  }
   // s[j][2 r + i]: row g + 8 r, token j * 8 + t + 4 i
   const bool partly = valid != 0xffffu || key0 + kChunkKeys - 1 > at_min ||
                       (p.window > 0 && key0 <= at_max - p.window);
@@ -194,7 +207,7 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
     float v = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    mx[r] = fmaxf(st.m[r], v);
+    mx[r] = fmaxf(st.m[r], v * sc[r]);
     base[r] = mx[r] == kNegInf ? 0.0f : mx[r];
   }
   if (__any_sync(0xffffffffu, mx[0] != st.m[0] || mx[1] != st.m[1])) {
@@ -216,7 +229,7 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[j][i] = ex2(s[j][i] - base[i >> 1]);
+      s[j][i] = ex2(fmaf(s[j][i], sc[i >> 1], -base[i >> 1]));
       st.l[i >> 1] += s[j][i];
     }
   // the weights as the A operand, rounded to the cache's 16-bit type (fp16
@@ -225,20 +238,25 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
   const u32 a0 = pack2<kBf16>(s[0][0], s[0][1]), a1 = pack2<kBf16>(s[0][2], s[0][3]);
   const u32 a2 = pack2<kBf16>(s[1][0], s[1][1]), a3 = pack2<kBf16>(s[1][2], s[1][3]);
   u32 seen_bad = 0;   // a non-finite V value, in chunks that some row sees only partly
+  // pieces 8 jj + pg of rows t + 4 k, as above: two places, for even and odd k
+  // (fp8: 8-byte halves of pieces)
+  const int vp = kType == kKvFp8 ? pg >> 1 : pg, vh = kType == kKvFp8 ? (pg & 1) << 3 : 0;
+  const u32 v_even = vs + t * S::kRowBytes + ((vp ^ (t & kMask)) << 4) + vh;
+  const u32 v_odd = vs + (t + 4) * S::kRowBytes + ((vp ^ ((t + 4) & kMask)) << 4) + vh;
 #pragma unroll
   for (int jj = 0; jj < kDim / 64; ++jj) {
     u32 v[4][4];   // keys t + 4 k: eight values, as pairs
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int row = t + 4 * k;
+      const u32 at = (k & 1 ? v_odd : v_even) + (k >> 1) * 8 * S::kRowBytes;
       if constexpr (kType == kKvFp8) {
-        const int unit = 8 * jj + pg;
-        const uint2 w = lds64(vs + row * S::kRowBytes + (((unit >> 1) ^ (row & kMask)) << 4) +
-                              ((unit & 1) << 3));
+        // jj moves by 4 pieces: bit 2 of the XORed place
+        const u32 flip = ((jj & 1) << 6);
+        const uint2 w = lds64((S::kChunks >= 8 ? vs + (((at - vs) ^ flip)) : at) + (jj >> 1) * 128);
         fp8x4_to_half(w.x, v[k][0], v[k][1]);
         fp8x4_to_half(w.y, v[k][2], v[k][3]);
       } else {
-        const uint4 w = lds128(vs + row * S::kRowBytes + (((8 * jj + pg) ^ (row & kMask)) << 4));
+        const uint4 w = lds128(at + jj * 128);
         v[k][0] = w.x;
         v[k][1] = w.y;
         v[k][2] = w.z;
@@ -354,54 +372,105 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Request 
   }
 }
 
-// Copies of one chunk of 16 tokens (K, then V) into a warp's stage; returns
-// the chunk's mask of readable tokens.  Tokens outside [lo, hi) and tokens of
-// bad blocks become zeros.
+// How a warp's lanes share the 16-byte pieces of a chunk of 16 tokens: kAcross
+// lanes side by side on a row (128 bytes, or a shorter row), 32 / kAcross rows
+// at once.  A lane's pieces then differ by constants, in global memory and,
+// with the XOR of the row index, in shared memory too.
 template <int kType, int kDim>
-__device__ __forceinline__ u32 load_chunk(const AttnParams &p, const Request &q, int head, u32 dst,
-                                          int key0, int lo, int hi) {
+struct ChunkLanes {
   using S = AttendShape<kType, kDim>;
-  constexpr int kMask = (S::kChunks < 8 ? S::kChunks : 8) - 1;
-  const int lane = threadIdx.x & 31;
-  const int key = key0 + (lane & 15);
-  bool ok = key >= lo && key < hi;
-  long long off = 0;
-  if (ok) {
-    const int pos = p.map.by_block(key);
-    const int block = p.tab.block_ids[q.pos0 + pos];
-    if (block < 0 || block >= p.map.num_blocks) {
-      ok = false;
-      raise(p.tab, kStatusBadBlockId);
-    } else {
-      off = token_offset(p.map, block, key - pos * p.map.block_size, head);
-    }
+  static constexpr int kAcross = S::kChunks < 8 ? S::kChunks : 8;
+  static constexpr int kDown = 32 / kAcross;                // rows at once: 4 or 8
+  static constexpr int kTurns = kChunkKeys / kDown;         // groups of rows
+  static constexpr int kSpans = S::kChunks / kAcross;       // spans of kAcross pieces
+
+  // A lane's first piece, from the chunk's start; turn j, span k follow at
+  // (first ^ flip(j)) + place(j, k).
+  static __device__ __forceinline__ u32 first() {
+    const int lane = threadIdx.x & 31, r = lane / kAcross, a = lane % kAcross;
+    return r * S::kRowBytes + ((a ^ (r & (kAcross - 1))) << 4);
   }
-  const u32 mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+  static constexpr __device__ u32 flip(int j) { return kDown == 4 ? (j & 1) << 6 : 0; }
+  static constexpr __device__ u32 place(int j, int k) { return j * kDown * S::kRowBytes + k * 128; }
+};
+
+// A chunk whose 16 tokens lie in one page, one after another, all readable.
+template <int kType, int kDim>
+__device__ __forceinline__ void load_run(const AttnParams &p, u32 chunk, u32 first,
+                                         const unsigned char *src) {
+  using S = AttendShape<kType, kDim>;
+  using L = ChunkLanes<kType, kDim>;
+  const unsigned char *v = src + p.map.half_stride;
+  const long long down = static_cast<long long>(L::kDown) * p.map.slot_stride;
+  if (p.map.chunk_stride == 16) {   // (spans are then 128 bytes apart: no address arithmetic)
+#pragma unroll
+    for (int j = 0; j < L::kTurns; ++j, src += down, v += down)
+#pragma unroll
+      for (int k = 0; k < L::kSpans; ++k) {
+        const u32 d = chunk + (first ^ L::flip(j)) + L::place(j, k);
+        cp_async16(d, src + k * 128, 16);
+        cp_async16(d + S::kChunkBytes, v + k * 128, 16);
+      }
+  } else {
+    const long long step = static_cast<long long>(L::kAcross) * p.map.chunk_stride;
+#pragma unroll
+    for (int j = 0; j < L::kTurns; ++j, src += down, v += down)
+#pragma unroll
+      for (int k = 0; k < L::kSpans; ++k) {
+        const u32 d = chunk + (first ^ L::flip(j)) + L::place(j, k);
+        cp_async16(d, src + k * step, 16);
+        cp_async16(d + S::kChunkBytes, v + k * step, 16);
+      }
+  }
+}
+
+// Any chunk; returns its mask of readable tokens.  Tokens outside [lo, hi)
+// and tokens of bad blocks become zeros.
+template <int kType, int kDim>
+__device__ __noinline__ u32 load_any(const AttnParams &p, long long pos0, int head, u32 chunk,
+                                     int key0, int lo, int hi) {
+  using S = AttendShape<kType, kDim>;
+  using L = ChunkLanes<kType, kDim>;
+  const int lane = threadIdx.x & 31;
+  const u32 first = L::first();
   const int row_bytes = p.head_dim * S::kElem;
-  const bool rows_first = p.map.chunk_stride == 16;
+  u32 mask = 0;
+#pragma unroll 1
+  for (int j = 0; j < L::kTurns; ++j) {
+    const int row = j * L::kDown + lane / L::kAcross, key = key0 + row;
+    bool ok = key >= lo && key < hi;
+    long long off = 0;
+    if (ok) {
+      const int pos = p.map.by_block(key);
+      const int block = p.tab.block_ids[pos0 + pos];
+      if (block < 0 || block >= p.map.num_blocks) {
+        ok = false;
+        raise(p.tab, kStatusBadBlockId);
+      } else {
+        off = token_offset(p.map, block, key - pos * p.map.block_size, head);
+      }
+    }
+    const u32 good = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
-  for (int i = 0; i < kChunkKeys * S::kChunks / 32; ++i) {
-    const int u = i * 32 + lane;
-    // x-split pools keep a chunk of consecutive tokens together
-    const int row = rows_first ? u / S::kChunks : u % kChunkKeys;
-    const int c = rows_first ? u % S::kChunks : u / kChunkKeys;
-    const long long o = __shfl_sync(0xffffffffu, off, row);
-    const bool live = mask >> row & 1u;
-    const int left = live ? row_bytes - c * 16 : 0;
-    const u32 d = dst + row * S::kRowBytes + ((c ^ (row & kMask)) << 4);
-    const unsigned char *src =
-        p.map.base + (left > 0 ? o + static_cast<long long>(c) * p.map.chunk_stride : 0);
-    const long long vh = left > 0 ? p.map.half_stride : 0;
-    if (!p.unit8) {
-      const u32 bytes = left > 0 ? 16u : 0u;
-      cp_async16(d, src, bytes);
-      cp_async16(d + S::kChunkBytes, src + vh, bytes);
-    } else {
+    for (int r = 0; r < L::kDown; ++r) mask |= (good >> (r * L::kAcross) & 1u) << (j * L::kDown + r);
+#pragma unroll 1
+    for (int k = 0; k < L::kSpans; ++k) {
+      const int c = k * L::kAcross + lane % L::kAcross, left = ok ? row_bytes - c * 16 : 0;
+      const u32 d = chunk + (first ^ L::flip(j)) + L::place(j, k);
+      const unsigned char *src =
+          p.map.base + (left > 0 ? off + static_cast<long long>(c) * p.map.chunk_stride : 0);
+      const long long vh = left > 0 ? p.map.half_stride : 0;
+      if (!p.unit8) {
+        const u32 bytes = left > 0 ? 16u : 0u;
+        cp_async16(d, src, bytes);
+        cp_async16(d + S::kChunkBytes, src + vh, bytes);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32 bytes = left > 8 * h ? 8u : 0u;
-        cp_async8z(d + 8 * h, src + (bytes ? 8 * h : 0), bytes);
-        cp_async8z(d + S::kChunkBytes + 8 * h, src + vh + (bytes ? 8 * h : 0), bytes);
+        for (int e = 0; e < 2; ++e) {
+          const u32 bytes = left > 8 * e ? 8u : 0u;
+          cp_async8z(d + 8 * e, src + (bytes ? 8 * e : 0), bytes);
+          cp_async8z(d + S::kChunkBytes + 8 * e, src + vh + (bytes ? 8 * e : 0), bytes);
+        }
       }
     }
   }
@@ -430,7 +499,7 @@ template <int kType, int kDim, bool kWide>
 __global__ void __launch_bounds__(kAttendThreads)
     kvcs_attend_kernel(const __grid_constant__ AttnParams p) {
   using S = AttendShape<kType, kDim>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char attend_smem[];   // (pieces' places are XORed)
   __shared__ long long s_scan[4];
   __shared__ u32 s_mask[S::kStages][4];
   __shared__ int s_last;
@@ -473,7 +542,8 @@ __global__ void __launch_bounds__(kAttendThreads)
 
   Request q = read_request(p.tab, r, p.map.block_size, false);
   GroupSpan sp = span_of(p, q, kRows);
-  const u32 ring = ptx::smem_addr(smem);
+  const u32 ring = ptx::smem_addr(attend_smem);
+  const u32 lane_first = ChunkLanes<kType, kDim>::first();
   const bool out_bf16 = kType == kKvBf16 || (kType == kKvFp8 && p.q_bf16);
 
   for (long long x = a; x < b;) {
@@ -530,25 +600,50 @@ __global__ void __launch_bounds__(kAttendThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.o[n][i] = 0.0f;
 
-    auto stage_at = [&](int stage, int warp_of) {
-      return ring + stage * S::kStageBytes + warp_of * 2 * S::kChunkBytes;
+    // The ring: a stage holds a tile, in its chunks' order.  The block of a
+    // chunk is looked up a tile ahead of its copies.
+    auto stage_at = [&](int stage, int chunk) {
+      return ring + stage * S::kStageBytes + chunk * 2 * S::kChunkBytes;
     };
+    const bool runs = p.runs && lo <= (sp.lo + c0) * kTileKeys;
+    using L = ChunkLanes<kType, kDim>;
+    const long long lane_src = static_cast<long long>(lane / L::kAcross) * p.map.slot_stride +
+                               (lane % L::kAcross) * static_cast<long long>(p.map.chunk_stride) +
+                               head * p.map.head_stride;
+    auto block_of = [&](int k) {
+      const int key = (sp.lo + k) * kTileKeys + warp * kChunkKeys;
+      return runs && k < c1 && key + kChunkKeys <= hi ? p.tab.block_ids[q.pos0 + p.map.by_block(key)]
+                                                      : -1;
+    };
+    int ahead = block_of(c0), put = 0;
     auto fetch = [&](int k) {
       if (k < c1) {
-        const int stage = (k - c0) % S::kStages;
-        const u32 mask = load_chunk<kType, kDim>(p, q, head, stage_at(stage, warp),
-                                                 (sp.lo + k) * kTileKeys + warp * kChunkKeys, lo, hi);
-        if (lane == 0) s_mask[stage][warp] = mask;
+        const int key = (sp.lo + k) * kTileKeys + warp * kChunkKeys;
+        const int block = ahead;
+        ahead = block_of(k + 1);
+        const u32 dst = stage_at(put, warp);
+        u32 mask = 0xffffu;
+        if (block >= 0 && block < p.map.num_blocks) {
+          const int slot = key - p.map.by_block(key) * p.map.block_size, sub = p.map.by_sub(slot);
+          load_run<kType, kDim>(p, dst, lane_first, p.map.base + block * p.map.block_stride +
+                                            sub * p.map.sub_stride +
+                                            static_cast<long long>(slot - sub * p.map.kbs) *
+                                                p.map.slot_stride + lane_src);
+        } else {
+          mask = load_any<kType, kDim>(p, q.pos0, head, dst, key, lo, hi);
+        }
+        if (lane == 0) s_mask[put][warp] = mask;
+        put = put + 1 == S::kStages ? 0 : put + 1;
       }
       cp_async_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < S::kStages - 1; ++k) fetch(c0 + k);
+    int stage = 0;
     for (int k = c0; k < c1; ++k) {
       cp_async_wait<S::kStages - 2>();
       if (kWide) __syncthreads(); else __syncwarp();
       fetch(k + S::kStages - 1);
-      const int stage = (k - c0) % S::kStages;
       const int key0 = (sp.lo + k) * kTileKeys;
       if (kWide) {
         if (row0 < rows_all) {
@@ -556,17 +651,16 @@ __global__ void __launch_bounds__(kAttendThreads)
           for (int c = 0; c < 4; ++c) {
             const int kc = key0 + c * kChunkKeys;
             if (kc > at_max || (p.window > 0 && kc + kChunkKeys - 1 <= at_min - p.window)) continue;
-            attend_chunk<kType, kDim>(p, qf, st, stage_at(stage, c),
-                                               stage_at(stage, c) + S::kChunkBytes,
-                                               s_mask[stage][c], kc, at, at_min, at_max, rs);
+            attend_chunk<kType, kDim>(p, qf, st, stage_at(stage, c), stage_at(stage, c) + S::kChunkBytes,
+                                      s_mask[stage][c], kc, at, at_min, at_max, rs);
           }
         }
       } else {
         attend_chunk<kType, kDim>(p, qf, st, stage_at(stage, warp),
-                                           stage_at(stage, warp) + S::kChunkBytes,
-                                           s_mask[stage][warp], key0 + warp * kChunkKeys, at,
-                                           at_min, at_max, rs);
+                                  stage_at(stage, warp) + S::kChunkBytes, s_mask[stage][warp],
+                                  key0 + warp * kChunkKeys, at, at_min, at_max, rs);
       }
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
 #pragma unroll
@@ -609,7 +703,7 @@ __global__ void __launch_bounds__(kAttendThreads)
     } else {
       // join the four warps' (m, l, o) in shared memory (the ring is drained)
       __syncthreads();
-      float *js = reinterpret_cast<float *>(smem);
+      float *js = reinterpret_cast<float *>(attend_smem);
       constexpr int kJ = kDim + 4;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -664,28 +758,56 @@ __global__ void __launch_bounds__(kAttendThreads)
       }
       __syncthreads();
       if (s_last) {
+        // 16 rows at a time: the parts' (m, l), their factors, then the sums
+        // over the parts, whose loads do not wait for one another
         __threadfence();
         const int rows_here = min(kRows, rows_all - rt * kRows);
-        for (int u = tid; u < rows_here * (kDim / 2); u += kAttendThreads) {
-          const int lr = u / (kDim / 2), col = u % (kDim / 2) * 2;
-          float m = kNegInf, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-          for (long long c = first; c <= last; ++c) {
-            const float *src = p.part + ((c * 2 + (c == first ? 1 : 0)) * kRows + lr) *
-                                            static_cast<long long>(S::kPartFloats);
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + kDim));
-            const float2 o = __ldcg(reinterpret_cast<const float2 *>(src + col));
-            const float mn = fmaxf(m, ml.x);
-            const float mb = mn == kNegInf ? 0.0f : mn;
-            const float f0 = ex2(m - mb), f1 = ex2(ml.x - mb);
-            l = l * f0 + ml.y * f1;
-            o0 = o0 * f0 + o.x * f1;
-            o1 = o1 * f0 + o.y * f1;
-            m = mn;
+        const int parts = static_cast<int>(last - first) + 1;
+        float *const factor = reinterpret_cast<float *>(attend_smem);   // [16][parts]
+        __shared__ float2 s_ml[16];
+        auto part_at = [&](int c, int lr) {
+          return p.part + (((first + c) * 2 + (c == 0 ? 1 : 0)) * kRows + lr) *
+                              static_cast<long long>(S::kPartFloats);
+        };
+        for (int lr0 = 0; lr0 < rows_here; lr0 += 16) {
+          const int rows = min(16, rows_here - lr0);
+          __syncthreads();
+          for (int lr = warp; lr < rows; lr += kAttendThreads / 32) {
+            float m = kNegInf, l = 0.0f;
+            for (int c = lane; c < parts; c += 32) {
+              const float pm = __ldcg(part_at(c, lr0 + lr) + kDim);
+              factor[lr * parts + c] = pm;
+              m = fmaxf(m, pm);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float mb = m == kNegInf ? 0.0f : m;
+            for (int c = lane; c < parts; c += 32) {
+              const float f = ex2(factor[lr * parts + c] - mb);
+              factor[lr * parts + c] = f;
+              l += f * __ldcg(part_at(c, lr0 + lr) + kDim + 1);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) s_ml[lr] = make_float2(m, l);
           }
-          const float inv = l > 0.0f || l != l ? p.v_scale / l : 0.0f;
-          if (col < p.head_dim)
-            store_out(p, q, head, rt * kRows + lr, col, o0 * inv, o1 * inv, out_bf16);
-          if (col == 0) store_lse(p, q, head, rt * kRows + lr, m, l);
+          __syncthreads();
+          for (int u = tid; u < rows * (kDim / 2); u += kAttendThreads) {
+            const int lr = u / (kDim / 2), col = u % (kDim / 2) * 2;
+            const float *f = factor + lr * parts;
+            float o0 = 0.0f, o1 = 0.0f;
+#pragma unroll 8
+            for (int c = 0; c < parts; ++c) {
+              const float2 o = __ldcg(reinterpret_cast<const float2 *>(part_at(c, lr0 + lr) + col));
+              o0 += f[c] * o.x;
+              o1 += f[c] * o.y;
+            }
+            const float m = s_ml[lr].x, l = s_ml[lr].y;
+            const float inv = l > 0.0f || l != l ? p.v_scale / l : 0.0f;
+            if (col < p.head_dim)
+              store_out(p, q, head, rt * kRows + lr0 + lr, col, o0 * inv, o1 * inv, out_bf16);
+            if (col == 0) store_lse(p, q, head, rt * kRows + lr0 + lr, m, l);
+          }
         }
       }
     }

@@ -715,24 +715,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __threadfence();
           const int first = i * 128 + (warp & 3) * 32;
           const int rows = min(32, x.rows_all - x.row0 - first);
-          for (int e = lane; e < rows * (kDim / 2); e += 32) {
-            const int r = first + e / (kDim / 2), col = e % (kDim / 2) * 2;
-            float jm = kNegInf, jl = 0.0f, o0 = 0.0f, o1 = 0.0f;
-            for (int s = 0; s < p.splits; ++s) {
-              const float *src = a.part + ((x.index * p.splits + s) * kTcRows + r) *
-                                              static_cast<long long>(S::kPartFloats);
-              const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + kDim));
-              const float2 o = __ldcg(reinterpret_cast<const float2 *>(src + col));
-              const float mn = fmaxf(jm, ml.x), mb = mn == kNegInf ? 0.0f : mn;
-              const float f0 = ex2(jm - mb), f1 = ex2(ml.x - mb);
-              jl = jl * f0 + ml.y * f1;
-              o0 = o0 * f0 + o.x * f1;
-              o1 = o1 * f0 + o.y * f1;
-              jm = mn;
-            }
+          const float *const part0 =
+              a.part + (x.index * p.splits * kTcRows + first) * static_cast<long long>(S::kPartFloats);
+          constexpr long long kNext = static_cast<long long>(kTcRows) * S::kPartFloats;
+#pragma unroll 2
+          for (int r = 0; r < rows; ++r) {
+            // lane s: the factor of part s
+            const float *row_at = part0 + r * static_cast<long long>(S::kPartFloats);
+            float2 ml = make_float2(kNegInf, 0.0f);
+            if (lane < p.splits)
+              ml = __ldcg(reinterpret_cast<const float2 *>(row_at + lane * kNext + kDim));
+            float jm = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, o));
+            const float f = ex2(ml.x - (jm == kNegInf ? 0.0f : jm));
+            float jl = f * ml.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, o);
             const float inv = jl > 0.0f || jl != jl ? a.v_scale / jl : 0.0f;
-            store_out(a, x.q, x.head, x.row0 + r, col, o0 * inv, o1 * inv, kBf16);
-            if (col == 0) store_lse(a, x.q, x.head, x.row0 + r, jm, jl);
+            float2 o[kDim / 64];
+#pragma unroll
+            for (int c = 0; c < kDim / 64; ++c) o[c] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s) {
+              const float fs = __shfl_sync(0xffffffffu, f, s);
+#pragma unroll
+              for (int c = 0; c < kDim / 64; ++c) {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(row_at + s * kNext) + c * 32 + lane);
+                o[c].x += fs * v.x;
+                o[c].y += fs * v.y;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < kDim / 64; ++c)
+              store_out(a, x.q, x.head, x.row0 + first + r, c * 64 + lane * 2, o[c].x * inv,
+                        o[c].y * inv, kBf16);
+            if (lane == 0) store_lse(a, x.q, x.head, x.row0 + first + r, jm, jl);
           }
         }
       }

@@ -154,6 +154,8 @@ struct AttnParams {
   int window;             // 0: none
   int observe;            // mass: last new tokens observed (0: all)
   int unit8;              // pools only 8-byte aligned: copies of 8 bytes
+  int runs;               // 16 aligned tokens always lie in one page, one after
+                          // another, in whole 16-byte pieces of the full width
   int row_lo, row_hi;     // requests whose rows (new tokens * group) lie in
                           // [row_lo, row_hi] belong to this launch
   float scale;            // scale * k_scale * log2(e): scores in units of log 2
