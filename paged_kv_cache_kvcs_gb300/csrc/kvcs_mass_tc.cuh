@@ -245,28 +245,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
    } else if (warp == 11) {
     // ------------------------------------------------------ log-sum-exps
+    // read two query tiles ahead
     u32 n_l = 0;
+    int tok_of[4], head_of[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      tok_of[j] = a.by_group(lane + 32 * j);
+      head_of[j] = lane + 32 * j - tok_of[j] * a.group;
+    }
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const MtUnit x = finder.find(p, u);
-      for (int t = 0; t < x.steps && ok; ++t, ++n_l) {
-        const u32 slot = n_l % kMtLseStages;
-        float v[4];
+      auto read = [&](int t, float (&v)[4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int c = lane + 32 * j, tok = x.tok0 + t * p.tile_tokens + c / a.group;
-          v[j] = 0.0f;
-          if (c < p.tile_tokens * a.group && tok < x.q.n)
-            v[j] = kLog2e * __ldg(a.lse + (x.q.q0 + tok) * (a.group * a.kv_heads) + x.head * a.group +
-                                  c % a.group);
+          const int tok = x.tok0 + t * p.tile_tokens + tok_of[j];
+          v[j] = tok_of[j] < p.tile_tokens && tok < x.q.n
+                     ? __ldg(a.lse + (x.q.q0 + tok) * (a.group * a.kv_heads) + x.head * a.group +
+                             head_of[j])
+                     : 0.0f;
         }
-        if (n_l >= kMtLseStages)
-          ok = tc::wait(lse_empty + 8 * slot, (n_l / kMtLseStages - 1) & 1, limit);
-        if (!ok) break;
+      };
+      float v[3][4];
+      read(0, v[0]);
+      read(1, v[1]);
+      for (int t0 = 0; t0 < x.steps && ok; t0 += 3)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sh.lse[slot][lane + 32 * j] = -v[j];
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(lse_full + 8 * slot);
-      }
+        for (int e = 0; e < 3; ++e) {
+          const int t = t0 + e;
+          if (t >= x.steps || !ok) break;
+          read(t + 2, v[(e + 2) % 3]);
+          const u32 slot = n_l % kMtLseStages;
+          if (n_l >= kMtLseStages)
+            ok = tc::wait(lse_empty + 8 * slot, (n_l / kMtLseStages - 1) & 1, limit);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sh.lse[slot][lane + 32 * j] = -kLog2e * v[e][j];
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(lse_full + 8 * slot);
+          ++n_l;
+        }
     }
    } else {
     // -------------------------------------------------------------- products
