@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ TcShared sh;
   __shared__ long long s_sum[kTcThreads / 32];
   const AttnParams &a = p.a;
+  if (blockDim.x != kTcThreads) return;   // (the registers' split counts on every warp)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const u32 smem = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;   // swizzled tiles: 1 KiB
   const u32 q_smem = smem, ring = smem + 2 * S::kTileBytes;

@@ -98,7 +98,7 @@ struct TypeLaunch {
       static std::atomic<u64> done{0};
       const cudaError_t e = allow_smem(kernel, smem, &done);
       if (e != cudaSuccess) return e;
-      kernel<<<static_cast<unsigned>(grid), kTcThreads, smem, st>>>(p, k, q);
+      kernel<<<static_cast<unsigned>(grid), kMtThreads, smem, st>>>(p, k, q);
       return cudaGetLastError();
     }
   }

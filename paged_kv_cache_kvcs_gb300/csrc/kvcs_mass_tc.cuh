@@ -12,9 +12,10 @@
 // sum to memory once: no exchange between threads, and a sum whose order does
 // not depend on timing.
 //
-// Roles: warps 0-3 and 4-7 sum a token tile each; warps 8 and 10 issue its
-// products into two buffers of tensor memory in turn; warp 9 loads K pages
-// and query tiles with TMA; warp 11 the rows' log-sum-exps.
+// Roles: warps 0-7 and 8-15 sum a token tile each (four of them the first half
+// of the columns, four the second); warps 16 and 18 issue its products into
+// two buffers of tensor memory in turn; warp 17 loads K pages and query tiles
+// with TMA; warp 19 the rows' log-sum-exps.
 #pragma once
 
 #include <type_traits>
@@ -26,8 +27,16 @@ namespace kvcs {
 
 constexpr int kMtKeys = 256;       // tokens of a unit
 constexpr int kMtQStages = 3;      // query tiles in flight
-constexpr int kMtLseStages = 4;
+constexpr int kMtLseStages = 3;
 constexpr int kMtControl = 3072;   // bytes ahead of the tiles
+// Five warpgroups: four for the sums (two per token tile, each for one half of
+// a query tile's rows: with one, a scheduler had two warps to hide each step's
+// latencies with, and 4 x 2048 queries over 8192 tokens took 435 us, not XXX),
+// one for the rest.  96 registers a thread at launch, 5 * 96 = 4 * 104 + 64.
+constexpr int kMtThreads = 640;
+constexpr int kMtSumWarps = 16;
+constexpr int kMtRegsSum = 104;
+constexpr int kMtRegsOther = 64;
 
 template <int kDim>
 struct MtShape {
@@ -50,9 +59,11 @@ struct MtShared {
   u64 q_full[kMtQStages], q_empty[kMtQStages];
   u64 lse_full[kMtLseStages], lse_empty[kMtLseStages];
   u64 s_full[2][2], s_empty[2][2];   // by token tile and buffer
+  u64 half_done[2], half_free[2];    // by token tile: the second half's sums
   u64 drain;
   u32 tmem;
-  long long sum[kTcThreads / 32];
+  float half[2][128];
+  long long sum[kMtThreads / 32];
   float lse[kMtLseStages][128];      // in units of log 2
 };
 static_assert(sizeof(MtShared) <= kMtControl, "control block");
@@ -133,19 +144,21 @@ struct MtFinder {
 };
 
 template <bool kBf16, int kDim, bool kPlain>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kMtThreads, 1)
     kvcs_mass_tc_kernel(const __grid_constant__ MtParams p, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_q) {
   using S = MtShape<kDim>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   MtShared &sh = *reinterpret_cast<MtShared *>(smem_raw);
   const AttnParams &a = p.a;
+  if (blockDim.x != kMtThreads) return;   // (the registers' split counts on every warp)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const u32 k_smem = ptx::smem_addr(smem_raw) + kMtControl, q_smem = k_smem + 4 * S::kTileBytes;
   const u32 k_full = ptx::smem_addr(sh.k_full), k_empty = ptx::smem_addr(sh.k_empty);
   const u32 q_full = ptx::smem_addr(sh.q_full), q_empty = ptx::smem_addr(sh.q_empty);
   const u32 lse_full = ptx::smem_addr(sh.lse_full), lse_empty = ptx::smem_addr(sh.lse_empty);
   const u32 s_full = ptx::smem_addr(sh.s_full), s_empty = ptx::smem_addr(sh.s_empty);
+  const u32 half_done = ptx::smem_addr(sh.half_done), half_free = ptx::smem_addr(sh.half_free);
   const u32 drain = ptx::smem_addr(&sh.drain);
   const u64 limit = p.timeout_ns;
   if (k_smem & 1023u) {   // the swizzled tiles lie on 1 KiB boundaries (they always do)
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ptx::mbar_init(k_full + 8 * i, 1);
       ptx::mbar_init(k_empty + 8 * i, 1);
       ptx::mbar_init(s_full + 8 * i, 1);
-      ptx::mbar_init(s_empty + 8 * i, 4);
+      ptx::mbar_init(s_empty + 8 * i, 8);
     }
     for (int i = 0; i < kMtQStages; ++i) {
       ptx::mbar_init(q_full + 8 * i, 1);
@@ -165,14 +178,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kMtLseStages; ++i) {
       ptx::mbar_init(lse_full + 8 * i, 1);
-      ptx::mbar_init(lse_empty + 8 * i, 8);
+      ptx::mbar_init(lse_empty + 8 * i, kMtSumWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(half_done + 8 * i, 4);
+      ptx::mbar_init(half_free + 8 * i, 4);
     }
     ptx::mbar_init(drain, 2);
     ptx::fence_barrier_init();
   }
-  if (warp == 8) tc::tmem_alloc(ptx::smem_addr(&sh.tmem), 512);
+  if (warp == 16) tc::tmem_alloc(ptx::smem_addr(&sh.tmem), 512);
   long long mine = 0;
-  for (long long r = tid; r < a.tab.num_requests; r += kTcThreads) {
+  for (long long r = tid; r < a.tab.num_requests; r += kMtThreads) {
     const Request q = read_request(a.tab, r, a.map.block_size, blockIdx.x == 0);
     int fk, ft, ek;
     mine += mt_units(a, q, &fk, &ft, &ek);
@@ -184,15 +201,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc::fence_after();
   long long units = 0;
-  for (int w = 0; w < kTcThreads / 32; ++w) units += sh.sum[w];
+  for (int w = 0; w < kMtThreads / 32; ++w) units += sh.sum[w];
   units *= a.kv_heads;
   const u32 tmem = sh.tmem;   // columns: buffers (tile 0: 0, 128; tile 1: 256, 384)
   bool ok = true;
   MtFinder finder;
 
-  if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcRegsOther));
-   if (warp == 9) {
+  if (warp >= kMtSumWarps) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMtRegsOther));
+   if (warp == 17) {
     // ------------------------------------------------- loads of K and queries
     const int boxes = 128 / p.box, bs = a.map.block_size;
     u32 n_k = 0, n_q = 0;
@@ -243,7 +260,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (u32 i = n_q > kMtQStages ? n_q - kMtQStages : 0; i < n_q; ++i)
         tc::wait(q_full + 8 * (i % kMtQStages), (i / kMtQStages) & 1, limit);
     }
-   } else if (warp == 11) {
+   } else if (warp == 19) {
     // ------------------------------------------------------ log-sum-exps
     // read two query tiles ahead
     u32 n_l = 0;
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
    } else {
     // -------------------------------------------------------------- products
     constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
-    const int i = warp == 8 ? 0 : 1;
+    const int i = warp == 16 ? 0 : 1;
     const u32 k_low = tc::desc_low(k_smem, 16), q_low = tc::desc_low(q_smem, 16);
     u32 n_k = 0, slot = 0, turn = 0, n_s = 0;
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -334,10 +351,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
    }
   } else {
     // ------------------------------------------------------------------ sums
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcRegsSoftmax));
-    const int i = warp >> 2, wq = warp & 3;
-    const u32 lanes = static_cast<u32>(wq * 32) << 16;
-    u32 n_s = 0, n_l = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMtRegsSum));
+    const int i = warp >> 3, hf = warp >> 2 & 1, wq = warp & 3;
+    const u32 lanes = (static_cast<u32>(wq * 32) << 16) + hf * 64;
+    u32 n_s = 0, n_l = 0, n_h = 0;
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const MtUnit x = finder.find(p, u);
       const bool work = i < x.tiles;
@@ -351,7 +368,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                           g0 + static_cast<long long>(a.window) * a.group)))
                                     : rows_end;
       float *dst = nullptr;
-      if (work && r_hi > r_lo && key < x.q.keys) {
+      if (hf == 0 && work && r_hi > r_lo && key < x.q.keys) {
         const int pos = a.map.by_block(key);
         const long long block = a.tab.block_ids[x.q.pos0 + pos];
         if (block < 0 || block >= a.map.num_blocks)
@@ -368,18 +385,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       u64 acc[4] = {0, 0, 0, 0};   // pairs of +0
       for (int t = 0; t < x.steps; ++t, ++n_l) {
         const u32 slot = n_l % kMtLseStages;
-        const u32 ls = ptx::smem_addr(sh.lse[slot]);
+        const u32 ls = ptx::smem_addr(sh.lse[slot]) + hf * 256;
         ok = tc::wait(lse_full + 8 * slot, (n_l / kMtLseStages) & 1, limit);
         if (work) ok = ok && tc::wait(s_full + 16 * i + 8 * (n_s & 1), (n_s / 2) & 1, limit);
         if (!ok) break;
         if (work) {
           tc::fence_after();
-          u32 s[128];
+          u32 s[64];
           const u32 ts = tmem + i * 256 + (n_s & 1) * 128 + lanes;
           tc::ld32(ts, s);
           tc::ld32(ts + 32, s + 32);
-          tc::ld32(ts + 64, s + 64);
-          tc::ld32(ts + 96, s + 96);
           tc::wait_ld();
           tc::fence_before();
           __syncwarp();
@@ -387,17 +402,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++n_s;
           if constexpr (!kPlain) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
+            for (int c = 0; c < 64; ++c)
               s[c] = __float_as_uint(score_of(a, __uint_as_float(s[c]), 1.0f));
           }
-          const int row0 = t * width;
-          const bool full = width == 128 && all_lo <= row0 && all_hi >= row0 + 128;
+          const int row0 = t * width + hf * 64;   // this half's first row
+          const bool full = width == 128 && all_lo <= row0 && all_hi >= row0 + 64;
           // weights, 0 where the row does not see the token (whatever the
           // row's scores and its log-sum-exp are)
           auto add = [&](auto masked) {
-            const int lo = r_lo - row0, hi = min(r_hi - row0, width);
+            const int lo = r_lo - row0, hi = min(r_hi - row0, width - hf * 64);
 #pragma unroll
-            for (int c = 0; c < 128; c += 4) {
+            for (int c = 0; c < 64; c += 4) {
               const uint4 v = lds128(ls + c * 4);   // -lse of four rows
               float y[4];
               tc::unpair(tc::fma2(tc::pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2,
@@ -422,16 +437,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) ptx::mbar_arrive(lse_empty + 8 * slot);
       }
       if (!ok) break;
+      if (!work || x.steps == 0) continue;
       float a0, a1;
       tc::unpair(tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3])), a0, a1);
-      if (dst) atomicAdd(dst, a0 + a1);
+      // the second half hands its sums to the first
+      if (hf) {
+        if (n_h > 0) ok = tc::wait(half_free + 8 * i, (n_h - 1) & 1, limit);
+        if (!ok) break;
+        sh.half[i][wq * 32 + lane] = a0 + a1;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(half_done + 8 * i);
+      } else {
+        ok = tc::wait(half_done + 8 * i, n_h & 1, limit);
+        if (!ok) break;
+        const float other = sh.half[i][wq * 32 + lane];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(half_free + 8 * i);
+        if (dst) atomicAdd(dst, a0 + a1 + other);
+      }
+      ++n_h;
     }
   }
   if (!ok && lane == 0) raise(a.tab, kStatusTimeout);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 8) tc::tmem_free(tmem, 512);
+  if (warp == 16) tc::tmem_free(tmem, 512);
 }
 
 }  // namespace kvcs
