@@ -64,16 +64,21 @@ def _raise(rc: int, where: str) -> None:
         raise B.KvcsError(rc, where)
 
 
-def _workspace(given, n: int, stream, handle: int, dev):
-    """The caller's workspace, checked, or one of ``n`` bytes."""
-    if given is not None:
-        B._check_tensor("workspace", given, (torch.uint8,), n, dev)
-        return given
+def _empty(shape, dtype, stream, handle: int, dev):
+    """A tensor that belongs to the stream the call writes it on."""
     if stream is None or handle == torch.cuda.current_stream(dev).cuda_stream:
-        return torch.empty(n, dtype=torch.uint8, device=dev)
-    # freed on return: it has to belong to the stream that uses it
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-        return torch.empty(n, dtype=torch.uint8, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(given, n: int, stream, handle: int, dev):
+    """The caller's workspace, checked, or one of ``n`` bytes (freed on
+    return: its memory goes back to the stream that uses it)."""
+    if given is None:
+        return _empty(n, torch.uint8, stream, handle, dev)
+    B._check_tensor("workspace", given, (torch.uint8,), n, dev)
+    return given
 
 
 def _attention_args(cache, q, new_offsets, R, index, kv_dtype, scale, softcap, window, k_scale,
@@ -141,9 +146,10 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     ``new_offsets`` (int64, num_requests + 1) gives each request's rows, its
     last tokens.  ``kv_dtype`` is what the pool holds: by default the pool's
     own dtype, or q's for a pool of raw bytes.  ``max_new``, the most new
-    tokens of a request, lets a decode step take a single launch.
-    ``workspace`` is a CUDA uint8 tensor of ``attention_workspace_bytes``
-    (by default allocated from the call's stream).
+    tokens of a request, lets a decode step take a single kernel.
+    ``workspace`` is a CUDA uint8 tensor of ``attention_workspace_bytes``.
+    What is not given (``out``, ``lse``, ``workspace``) is allocated on the
+    stream that the call runs on.
 
     Returns ``(out, lse)``: ``out`` like a packed ``q``, ``lse`` float32
     ``[total_new, q_heads]``.
@@ -154,13 +160,14 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     a = _attention_args(cache, q, new_offsets, R, index, kv_dtype, scale, softcap, window, k_scale,
                         v_scale, max_new)
     dev = q.device
+    handle = _stream_handle(stream, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = _empty(q.shape, q.dtype, stream, handle, dev)
         a.out = out.data_ptr()
     else:
         a.out = _checked("out", out, q.dtype, q.numel(), index)
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = _empty(q.shape[:2], torch.float32, stream, handle, dev)
         a.lse = lse.data_ptr()
     else:
         a.lse = _checked("lse", lse, torch.float32, q.shape[0] * q.shape[1], index)
@@ -171,7 +178,6 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     a_ref = ctypes.byref(a)
     _raise(lib.kvcs_attention_workspace(arr, block_size, R, total, a_ref, 0, ctypes.byref(n)),
            "kvcs_attention_workspace")
-    handle = _stream_handle(stream, dev)
     workspace = _workspace(workspace, n.value, stream, handle, dev)
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel()

@@ -271,6 +271,83 @@ def test_graph_replay_streams_and_determinism(new):
             assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+PAGES = [dict(bs=8), dict(bs=24), dict(bs=40), dict(bs=128), dict(bs=256),
+         dict(bs=32, kbs=8, layout=HND), dict(bs=48, kbs=16, layout=HND), dict(bs=4)]
+
+
+@pytest.mark.parametrize("pages", PAGES, ids=str)
+@pytest.mark.parametrize("group,dim", [(1, 128), (3, 64), (5, 128), (7, 64)])
+def test_chunks_of_any_page_and_group(pages, group, dim):
+    """Pages that end inside a tile, and query groups that do not divide one."""
+    case = A.Case(dim=dim, group=group, lengths=[333, 150, 129], new=[140, 150, 30], seed=30, **pages)
+    check(case)
+    check_mass(case)
+
+
+def test_more_units_than_the_gpu_holds():
+    """Every CTA goes through several units, some of them short."""
+    g = torch.Generator().manual_seed(31)
+    lengths = torch.randint(20, 420, (24,), generator=g).tolist()
+    new = [min(n, 17 + (7 * i) % 200) for i, n in enumerate(lengths)]
+    case = A.Case(dim=128, heads=4, group=4, lengths=lengths, new=new, seed=31)
+    check(case)
+    check(case, window=40)
+    check_mass(case, observe=100)
+    check_mass(case, window=40)
+
+
+def test_offsets_past_32_bits():
+    """Blocks beyond 4 GiB from the pool's base, and pools whose V lies further."""
+    nb, H, bs, D = 70000, 4, 16, 128
+    if torch.cuda.mem_get_info()[0] < 2 * nb * bs * H * D * 2 * 2:
+        pytest.skip("needs 5 GB")
+    big = torch.zeros((2, nb, bs, H, D), dtype=torch.bfloat16, device="cuda")
+    small = A.Case(dim=D, heads=H, group=4, lengths=[200, 77], new=[1, 1], seed=32, tail=0.0)
+    chunk = A.Case(dim=D, heads=H, group=4, lengths=[200, 77], new=[90, 77], seed=32, tail=0.0)
+    n = small.nb
+    big[:, nb - n:] = small.pool.view(torch.bfloat16).view(2, n, bs, H, D)
+    for case in (small, chunk):
+        assert torch.equal(case.pool, small.pool)
+        want = run(case, max_new=max(case.new))
+        mass = torch.zeros((n, H, bs), device="cuda")
+        K.attention_mass(case.cache, bs, *case.table, case.q, case.new_offsets, want[1], mass)
+        cache = W.CacheSpec(big, nb, NHD, 0, 0, H, 2 * D)
+        table = case.table[:3] + [case.table[3] + (nb - n)]
+        got = K.paged_attention(cache, bs, *table, case.q, case.new_offsets, max_new=max(case.new))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        far = torch.zeros((nb, H, bs), device="cuda")
+        K.attention_mass(cache, bs, *table, case.q, case.new_offsets, want[1], far)
+        assert torch.equal(far[nb - n:], mass) and not far[:nb - n].any()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace."""
+    cases = [A.Case(dim=128, lengths=[3000 + 500 * i, 900], new=new, seed=33 + i)
+             for i, new in enumerate(([1, 1], [120, 300], [1, 1], [64, 1]))]
+    alone = [run(c, max_new=max(c.new)) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [K.paged_attention(c.cache, c.bs, *c.table, c.q, c.new_offsets, max_new=max(c.new),
+                                 stream=s, total_positions=c.total) for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_nothing_to_do():
+    case = A.Case(dim=64, lengths=[0, 30], new=[0, 0], seed=34)
+    out, lse, status = run(case)
+    assert out.numel() == 0 and lse.numel() == 0 and status == 0
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+    q = torch.full((3, 8, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    K.paged_attention(case.cache, case.bs, zero, none, none, none.int(), q, zero, out=out)
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+
+
 # ---------------------------------------------------------------------------
 # attention mass
 # ---------------------------------------------------------------------------

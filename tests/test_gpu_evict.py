@@ -160,6 +160,53 @@ def test_words(layout, kw, fresh):
         assert int(words[b]) == 77
 
 
+def test_rows_longer_than_shared_memory():
+    """More tokens than a CTA holds scores of, beside short requests."""
+    lengths = (60000, 20, 700)
+    cases, sc = make(seed=9, layers=1, lengths=lengths, heads=1, dim=8, bs=64, spare=3,
+                     scores="ties")
+    want = expected(cases, sc, [31000, 7, 300], 4, 50)
+    assert evict(cases, sc, [31000, 7, 300], sinks=4, recent=50) == 0
+    same(cases, sc, want)
+
+
+def test_shared_source_blocks_into_fresh_ones():
+    """Two requests with a common prefix are thinned out into blocks of their own."""
+    cases, sc = make(seed=10, layers=2, lengths=(96, 96), spare=40)
+    c = cases[0]
+    half = c.offsets[1]
+    for x in cases:
+        x.ids[half:half + 3] = x.ids[:3]
+        x.table[3].copy_(x.ids)
+        x.values[1] = torch.cat([x.values[0][:, :48], x.values[1][:, 48:]], 1)
+    free = [b for b in range(c.nb) if b not in set(c.ids.tolist())]
+    to = torch.tensor(free[:c.total], dtype=torch.int32)
+    want = expected(cases, sc, [40, 70], 2, 8, to)
+    assert evict(cases, sc, [40, 70], sinks=2, recent=8, new_block_ids=to.cuda()) == 0
+    same(cases, sc, want)
+
+
+def test_offsets_past_32_bits():
+    cases, sc = make(seed=11, layers=1, lengths=(300, 90), heads=4, dim=128, spare=5)
+    c = cases[0]
+    nb, n = 70000, c.nb
+    if torch.cuda.mem_get_info()[0] < 8 * nb * c.bs * 4 * 128:
+        pytest.skip("needs 9 GB")
+    big = torch.zeros((2, nb, c.bs, 4, 128), dtype=torch.bfloat16, device="cuda")
+    big[:, nb - n:] = c.pool.view(torch.bfloat16).view(2, n, c.bs, 4, 128)
+    scores = torch.zeros((nb, 4, c.bs), device="cuda")
+    scores[nb - n:] = sc[0]
+    keep = torch.tensor([111, 40], dtype=torch.int64, device="cuda")
+    words = torch.zeros(nb, dtype=torch.int64, device="cuda")
+    want_words = torch.zeros(n, dtype=torch.int64, device="cuda")
+    K.evict(W.CacheSpec(big, nb, NHD, 0, 0, 4, 256), c.bs, *c.table[:3], c.table[3] + (nb - n), scores,
+            keep, sinks=2, recent=9, block_sums=words)
+    K.evict(c.cache, c.bs, *c.table, sc[0], keep, sinks=2, recent=9, block_sums=want_words)
+    assert torch.equal(big[:, nb - n:].reshape(-1).view(torch.uint8), c.pool.view(-1))
+    assert torch.equal(scores[nb - n:], sc[0]) and torch.equal(words[nb - n:], want_words)
+    assert not big[:, :nb - n].any() and not words[:nb - n].any()
+
+
 def test_bad_requests_are_left_untouched():
     cases, sc = make(seed=5, lengths=(100, 90, 80, 70))
     c = cases[0]
