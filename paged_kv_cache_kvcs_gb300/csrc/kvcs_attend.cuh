@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kAttendThreads)
   for (long long r = tid; r < R; r += kAttendThreads)
     sum += span_of(p, read_request(p.tab, r, p.map.block_size, blockIdx.x == 0), kRows).total;
   long long total;
-  block_scan(sum, &total, s_scan);
+  const long long ahead_of_me = block_scan(sum, &total, s_scan);
   const long long grid = min(static_cast<long long>(gridDim.x), total);
   if (blockIdx.x >= grid) {
     ptx::grid_dep_wait();
@@ -520,14 +520,15 @@ __global__ void __launch_bounds__(kAttendThreads)
   }
   const long long a = total * blockIdx.x / grid, b = total * (blockIdx.x + 1ll) / grid;
   long long before = 0, r = 0;
+  __shared__ long long s_req[2];
   for (long long c = 0;; c += kAttendThreads) {
     const long long rr = c + tid;
-    const long long v =
-        rr < R ? span_of(p, read_request(p.tab, rr, p.map.block_size, false), kRows).total : 0;
-    long long all;
-    const long long ex = before + block_scan(v, &all, s_scan);
+    long long v = sum, all = total, ex = ahead_of_me;
+    if (R > kAttendThreads) {   // (otherwise the first scan tells)
+      v = rr < R ? span_of(p, read_request(p.tab, rr, p.map.block_size, false), kRows).total : 0;
+      ex = before + block_scan(v, &all, s_scan);
+    }
     if (before + all > a) {
-      __shared__ long long s_req[2];
       if (v > 0 && ex <= a && a < ex + v) {
         s_req[0] = rr;
         s_req[1] = ex;

@@ -92,26 +92,42 @@ __device__ __forceinline__ void raise(const Tables &t, u32 bit) {
   if (t.status) atomicOr(t.status, bit);
 }
 
-// Tokens of request r; flagged tables hold none.  Reads only entries the
+// A request's raw table entries.  (Loaded together: a chain of dependent
+// loads at the start of every CTA would be most of a small call's time.)
+struct RawRequest {
+  long long a, b, first, tokens, new_a, new_b;
+};
+
+template <bool kNew>
+__device__ __forceinline__ RawRequest load_request(const Tables &t, long long r) {
+  RawRequest w;
+  w.a = t.pos_offsets[r];
+  w.b = t.pos_offsets[r + 1];
+  w.first = t.first_position[r];
+  w.tokens = t.num_tokens[r];
+  w.new_a = kNew ? t.new_offsets[r] : 0;
+  w.new_b = kNew ? t.new_offsets[r + 1] : 0;
+  return w;
+}
+
+// Tokens of a request; flagged tables hold none.  Reads only entries the
 // tables have, whatever these hold.
-__device__ inline Request read_tokens(const Tables &t, long long r, int block_size, bool report) {
+__device__ __forceinline__ Request tokens_of(const Tables &t, const RawRequest &w, int block_size,
+                                             bool report) {
   Request q;
   q.n = 0;
   q.q0 = 0;
   q.at = 0;
   q.keys = 0;
-  const long long a = t.pos_offsets[r], b = t.pos_offsets[r + 1];
-  const long long fp = t.first_position[r];
-  q.pos0 = a;
+  q.pos0 = w.a;
   q.base = 0;
-  const bool bad = a < 0 || b < a || b > t.total_positions || fp < 0 || fp > (1ll << 31);
-  if (bad) {
+  if (w.a < 0 || w.b < w.a || w.b > t.total_positions || w.first < 0 || w.first > (1ll << 31)) {
     if (report) raise(t, kStatusBadRequests);
     return q;
   }
-  q.base = fp * block_size;
-  long long keys = max(t.num_tokens[r], 0ll) - q.base;
-  const long long listed = (b - a) * block_size;
+  q.base = w.first * block_size;
+  long long keys = max(w.tokens, 0ll) - q.base;
+  const long long listed = (w.b - w.a) * block_size;
   if (keys > listed) keys = listed;
   if (keys > kMaxRequestTokens) {
     if (report) raise(t, kStatusBadRequests);
@@ -121,17 +137,23 @@ __device__ inline Request read_tokens(const Tables &t, long long r, int block_si
   return q;
 }
 
+__device__ __forceinline__ Request read_tokens(const Tables &t, long long r, int block_size,
+                                               bool report) {
+  return tokens_of(t, load_request<false>(t, r), block_size, report);
+}
+
 // As read_tokens, with the request's new tokens: they are its last ones.
-__device__ inline Request read_request(const Tables &t, long long r, int block_size, bool report) {
-  Request q = read_tokens(t, r, block_size, report);
-  const long long a = t.new_offsets[r], b = t.new_offsets[r + 1];
-  if (a < 0 || b < a || b > t.total_new || b - a > t.max_new) {
+__device__ __forceinline__ Request read_request(const Tables &t, long long r, int block_size,
+                                                bool report) {
+  const RawRequest w = load_request<true>(t, r);
+  Request q = tokens_of(t, w, block_size, report);
+  if (w.new_a < 0 || w.new_b < w.new_a || w.new_b > t.total_new || w.new_b - w.new_a > t.max_new) {
     if (report) raise(t, kStatusBadRequests);
     return q;
   }
-  q.q0 = a;
-  q.n = static_cast<int>(b - a);
-  long long at = max(t.num_tokens[r], 0ll) - q.n - q.base;
+  q.q0 = w.new_a;
+  q.n = static_cast<int>(w.new_b - w.new_a);
+  long long at = max(w.tokens, 0ll) - q.n - q.base;
   const long long lim = 1ll << 30;
   at = at < -lim ? -lim : at > lim ? lim : at;
   q.at = static_cast<int>(at);

@@ -54,16 +54,17 @@ __global__ void __launch_bounds__(kMassThreads)
   for (long long r = tid; r < R; r += kMassThreads)
     sum += mass_span(p, read_request(p.tab, r, p.map.block_size, blockIdx.x == 0)).total;
   long long total;
-  block_scan(sum, &total, s_scan);
+  const long long ahead_of_me = block_scan(sum, &total, s_scan);
   const long long a_cta = total * blockIdx.x / gridDim.x, b_cta = total * (blockIdx.x + 1ll) / gridDim.x;
   if (a_cta >= b_cta) return;
   long long before = 0, r = 0;
   for (long long c = 0;; c += kMassThreads) {
     const long long rr = c + tid;
-    const long long v =
-        rr < R ? mass_span(p, read_request(p.tab, rr, p.map.block_size, false)).total : 0;
-    long long all;
-    const long long ex = before + block_scan(v, &all, s_scan);
+    long long v = sum, all = total, ex = ahead_of_me;
+    if (R > kMassThreads) {   // (otherwise the first scan tells)
+      v = rr < R ? mass_span(p, read_request(p.tab, rr, p.map.block_size, false)).total : 0;
+      ex = before + block_scan(v, &all, s_scan);
+    }
     if (before + all > a_cta) {
       if (v > 0 && ex <= a_cta && a_cta < ex + v) {
         s_req[0] = rr;
