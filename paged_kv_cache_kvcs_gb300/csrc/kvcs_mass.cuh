@@ -79,7 +79,13 @@ __global__ void __launch_bounds__(kMassThreads)
   }
   Request q = read_request(p.tab, r, p.map.block_size, false);
   MassSpan sp = mass_span(p, q);
-  // the CTA's run goes round its warps
+  // The CTA's run goes round its warps.  A warp keeps the queries of a group
+  // that fits one tile of 16 rows (a decode step) from chunk to chunk.
+  u32 qf[kDim / 8][2];
+  float rs[2], lse[2];
+  int at[2];
+  long long held_r = -1;
+  int held_head = -1;
   for (long long x = a_cta + warp; x < b_cta; x += kMassThreads / 32) {
     while (x >= before + sp.total) {
       before += sp.total;
@@ -139,31 +145,33 @@ __global__ void __launch_bounds__(kMassThreads)
       }
     }
     float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};   // tokens j * 8 + t + 4 i
-    // observed tokens that see some key of the chunk
-    const int i0 = max(sp.first, key0 - q.at);
+    // observed tokens that see some key of the chunk (all of a small group)
+    const bool small = (q.n - sp.first) * p.group <= 16;
+    const int i0 = small ? sp.first : max(sp.first, key0 - q.at);
     int i1 = q.n;
-    if (p.window > 0)
+    if (p.window > 0 && !small)
       i1 = static_cast<int>(min(static_cast<long long>(i1),
                                 static_cast<long long>(key0) + kChunkKeys - 1 + p.window - q.at));
     const int rows_end = i1 * p.group;
 #pragma unroll 1
     for (int row0 = i0 * p.group; row0 < rows_end; row0 += 16) {
-      int row[2], at[2];
-      bool has[2];
-      float lse[2];
+      if (!small || r != held_r || head != held_head) {
+        int row[2];
+        bool has[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = row0 + g + 8 * i;
-        has[i] = rr < rows_end;
-        row[i] = has[i] ? rr : row0;
-        at[i] = has[i] ? q.at + p.by_group(row[i]) : -1;   // spare rows see nothing
-        const long long tok = q.q0 + p.by_group(row[i]);
-        lse[i] = kLog2e * __ldg(p.lse + tok * (p.group * p.kv_heads) + head * p.group +
-                                (row[i] - p.by_group(row[i]) * p.group));
+        for (int i = 0; i < 2; ++i) {
+          const int rr = row0 + g + 8 * i;
+          has[i] = rr < rows_end;
+          row[i] = has[i] ? rr : row0;
+          const int ti = p.by_group(row[i]);
+          at[i] = has[i] ? q.at + ti : -1;   // spare rows see nothing
+          lse[i] = kLog2e * __ldg(p.lse + (q.q0 + ti) * (p.group * p.kv_heads) + head * p.group +
+                                  row[i] - ti * p.group);
+        }
+        load_queries<kType, kDim>(p, q, head, row, has, qf, rs);
+        held_r = small ? r : -1;
+        held_head = head;
       }
-      u32 qf[kDim / 8][2];
-      float rs[2];
-      load_queries<kType, kDim>(p, q, head, row, has, qf, rs);
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int b = 0; b < kWords; ++b)
