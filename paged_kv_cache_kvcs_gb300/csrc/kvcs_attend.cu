@@ -237,7 +237,6 @@ bool query_map(CUtensorMap *map, const AttnParams &p, bool bf16, int tokens) {
 // is enough either way.
 constexpr int kNarrowRows = 16;
 constexpr int kWideRows = 64;
-constexpr int kTcMaxSplits = 16;
 constexpr int kMassRows = 32;    // observed rows the small mass kernel takes, at most
 constexpr int kTcMinTiles = 4;   // token tiles a part holds, at least (on average)
 
@@ -277,7 +276,7 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
                        static_cast<long long>(kTcMaxSplits)})));
     pl.wide_grid = static_cast<int>(std::min<long long>(sms, units * pl.splits));
     pl.wide_tickets = pl.splits > 1 ? units * 8 : 0;   // one per warp's rows
-    wf = pl.splits > 1 ? units * pl.splits * kTcRows * (p.head_dim + 2) : 0;
+    wf = pl.splits > 1 ? units * pl.splits * kTcRows * (p.head_dim + 4) : 0;
   }
   pl.part_floats = std::max(pl.narrow ? nf : 0, pl.wide || pl.tc ? wf : 0);
   return pl;

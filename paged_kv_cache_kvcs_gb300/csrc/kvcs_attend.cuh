@@ -36,6 +36,14 @@
 // n-tiles.  Chunks are stored XORed with the row index; keys and V columns
 // are assigned to lanes so that the eight lanes of a shared-memory phase hit
 // different banks for 128- and 256-byte rows.
+//
+// Measured: 64 requests of 512 to 4096 tokens (8 KV heads of 128, bf16, one
+// token each) 116 us, 5.2 TB/s, where reading the same pages without any
+// arithmetic takes 106; fp8 with 64 query heads, 128 requests of 2048, 139 us
+// (3.9 TB/s; conversions and products, not DRAM, set that pace: 125 us with
+// the copies left out); two requests of 99,001 and 131,072 tokens with three
+// drafted ones 168 us, 5.6 TB/s; one request of 709 tokens 12 us.  Two CTAs an
+// SM with three stages; three CTAs with two stages took 114, 143 and 208 us.
 #pragma once
 
 #include "kvcs_attn_common.cuh"

@@ -10,8 +10,8 @@
 // 128 tokens.  Roles of the CTA's warps:
 //   warps 9, 11  load K and V tiles page by page with TMA (boxes of as many
 //              slots as a page holds in a row, 128-byte swizzle) into a ring;
-//   warp 8     issues the products: S_i = Q_i K^T into tensor memory, then
-//              O_i += P_i V with P_i from tensor memory;
+//   warps 8, 10  issue the products of one query tile each: S_i = Q_i K^T into
+//              tensor memory, then O_i += P_i V with P_i from tensor memory;
 //   warps 0-3, warps 4-7   the softmax of one query tile each, a thread per
 //              row: S from tensor memory, weights back over S as 16-bit P.
 // The two tiles take turns: while one tile's weights are made, the other
@@ -28,6 +28,16 @@
 // that hold no token are therefore zeroed in shared memory, and in tiles that
 // some row sees only in part, rows with a non-finite value are zeroed and
 // noted; the rows that do see them add them at the end.
+//
+// Measured (4 requests of 2048 new tokens over 8192, 32 query heads to 8 KV
+// heads of 128, bf16): 671 us, 1430 TFLOP/s, 76% of the measured burst rate of
+// a library product and 85% of its sustained rate.  With the weights left out
+// the products and loads alone take 510 us.  What it grew from and what was
+// left again, for the same call: mma.sync 6300; one issuing thread for both
+// query tiles 1027; loads of 64-element halves, one warp for K and V 918 with
+// no weights at all; an issuing thread per tile, without turns, 863; four
+// softmax warps a scheduler with 16 rows a warp (two threads of a quad sharing
+// 64 columns) 926; a maximum found in the same pass as both halves' weights 706.
 #pragma once
 
 #include "kvcs_attend.cuh"
@@ -35,7 +45,7 @@
 
 namespace kvcs {
 
-// Three warpgroups (the third: loads, products, two idle warps).  Launched
+// Three warpgroups (the third: loads and products).  Launched
 // with 168 registers a thread, 64512 in all; the softmax warpgroups take 208
 // (a row of S is 128 of them), the third keeps 88: 2 * 208 + 88 = 3 * 168.
 constexpr int kTcThreads = 384;
@@ -43,6 +53,7 @@ constexpr int kTcRegsSoftmax = 208;
 constexpr int kTcRegsOther = 88;
 constexpr int kTcRows = 256;      // query rows of a unit
 constexpr int kTcKeys = 128;      // tokens of a tile
+constexpr int kTcMaxSplits = 16;  // parts of a unit's token range, at most
 constexpr float kTcSlack = 8.0f;  // log2 of the largest weight left unscaled
 constexpr int kTcDirty = 8;       // partly seen tiles of a unit, at most
 
@@ -55,7 +66,7 @@ struct TcShape {
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // Q, K or V tile
   static constexpr int kStages = kDim == 128 ? 5 : 10;
   static constexpr int kSmemBytes = (2 + kStages) * kTileBytes + 1024;
-  static constexpr int kPartFloats = kDim + 2;
+  static constexpr int kPartFloats = kDim + 4;   // o, m, l of a row, on 16-byte boundaries
 };
 
 struct TcParams {
@@ -705,7 +716,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (has && whole && a.lse) a.lse[out_row] = l == 0.0f ? kNegInf : kLn2 * (m + log2f(l));
         if (has && !whole) *reinterpret_cast<float2 *>(part + kDim) = make_float2(m, l);
       }
-      if (!whole && work) {
+      const int first = i * 128 + (warp & 3) * 32;   // the warp's rows of the unit
+      const int rows = min(32, x.rows_all - x.row0 - first);
+      if (!whole && work && rows > 0) {
         // a counter per warp's rows: the last part's warp to arrive joins them, in order
         ptx::grid_dep_wait();   // the counters are zero from here on
         __threadfence();
@@ -714,44 +727,59 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) before_me = atomicAdd(a.tickets + x.index * 8 + warp, 1u);
         if (__shfl_sync(0xffffffffu, before_me, 0) == static_cast<u32>(p.splits - 1)) {
           __threadfence();
-          const int first = i * 128 + (warp & 3) * 32;
-          const int rows = min(32, x.rows_all - x.row0 - first);
           const float *const part0 =
               a.part + (x.index * p.splits * kTcRows + first) * static_cast<long long>(S::kPartFloats);
           constexpr long long kNext = static_cast<long long>(kTcRows) * S::kPartFloats;
+          // lane r: row r's factors; everything that is loaded is asked for at once
+          float f[kTcMaxSplits], ls[kTcMaxSplits], jm = kNegInf, jl = 0.0f;
+          const float *const ml_at = part0 + min(lane, rows - 1) * S::kPartFloats + kDim;
+#pragma unroll
+          for (int s = 0; s < kTcMaxSplits; ++s) {
+            float2 ml = make_float2(kNegInf, 0.0f);
+            if (s < p.splits) ml = __ldcg(reinterpret_cast<const float2 *>(ml_at + s * kNext));
+            f[s] = ml.x;
+            ls[s] = ml.y;
+          }
+#pragma unroll
+          for (int s = 0; s < kTcMaxSplits; ++s) jm = fmaxf(jm, f[s]);
+#pragma unroll
+          for (int s = 0; s < kTcMaxSplits; ++s) {
+            f[s] = ex2(f[s] - (jm == kNegInf ? 0.0f : jm));
+            jl += f[s] * ls[s];
+          }
+          const float inv = jl > 0.0f || jl != jl ? a.v_scale / jl : 0.0f;
+          if (lane < rows) store_lse(a, x.q, x.head, x.row0 + first + lane, jm, jl);
+          constexpr int kOwn = kDim / 32;   // columns a lane joins
 #pragma unroll 2
           for (int r = 0; r < rows; ++r) {
-            // lane s: the factor of part s
-            const float *row_at = part0 + r * static_cast<long long>(S::kPartFloats);
-            float2 ml = make_float2(kNegInf, 0.0f);
-            if (lane < p.splits)
-              ml = __ldcg(reinterpret_cast<const float2 *>(row_at + lane * kNext + kDim));
-            float jm = ml.x;
+            const float *row_at = part0 + r * S::kPartFloats + lane * kOwn;
+            float v[kTcMaxSplits][kOwn], o[kOwn];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, o));
-            const float f = ex2(ml.x - (jm == kNegInf ? 0.0f : jm));
-            float jl = f * ml.y;
+            for (int s = 0; s < kTcMaxSplits; ++s) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, o);
-            const float inv = jl > 0.0f || jl != jl ? a.v_scale / jl : 0.0f;
-            float2 o[kDim / 64];
-#pragma unroll
-            for (int c = 0; c < kDim / 64; ++c) o[c] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-            for (int s = 0; s < p.splits; ++s) {
-              const float fs = __shfl_sync(0xffffffffu, f, s);
-#pragma unroll
-              for (int c = 0; c < kDim / 64; ++c) {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(row_at + s * kNext) + c * 32 + lane);
-                o[c].x += fs * v.x;
-                o[c].y += fs * v.y;
+              for (int c = 0; c < kOwn; ++c) v[s][c] = 0.0f;
+              if (s < p.splits) {
+                if constexpr (kOwn == 4)
+                  *reinterpret_cast<float4 *>(v[s]) =
+                      __ldcg(reinterpret_cast<const float4 *>(row_at + s * kNext));
+                else
+                  *reinterpret_cast<float2 *>(v[s]) =
+                      __ldcg(reinterpret_cast<const float2 *>(row_at + s * kNext));
               }
             }
 #pragma unroll
-            for (int c = 0; c < kDim / 64; ++c)
-              store_out(a, x.q, x.head, x.row0 + first + r, c * 64 + lane * 2, o[c].x * inv,
-                        o[c].y * inv, kBf16);
-            if (lane == 0) store_lse(a, x.q, x.head, x.row0 + first + r, jm, jl);
+            for (int c = 0; c < kOwn; ++c) o[c] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kTcMaxSplits; ++s) {
+              const float fs = __shfl_sync(0xffffffffu, f[s], r);
+#pragma unroll
+              for (int c = 0; c < kOwn; ++c) o[c] += fs * v[s][c];
+            }
+            const float by = __shfl_sync(0xffffffffu, inv, r);
+#pragma unroll
+            for (int c = 0; c < kOwn; c += 2)
+              store_out(a, x.q, x.head, x.row0 + first + r, lane * kOwn + c, o[c] * by,
+                        o[c + 1] * by, kBf16);
           }
         }
       }

@@ -28,6 +28,13 @@
 //
 // Words: the new blocks' checksum words, sum_h m_h sum_p x_p (2 (t P + p) + 1)
 // with t the token's new position, are added while the bytes pass through.
+//
+// Measured: 8 layers of 16 requests of 512 to 4096 tokens (8 KV heads of 128,
+// bf16) down to 1024 in place: 190 us from fresh caches (885 MB, 4.7 TB/s),
+// about 45 of them the selection; three requests of 6001 to 20,011 tokens, 4
+// layers, into fresh HND blocks with their words: 125 us; one request of 613
+// tokens, one layer: 14 us.  The first form, one kernel a row, took 277, 628
+// and 49.
 #pragma once
 
 #include "kvcs_attn_common.cuh"

@@ -8,6 +8,11 @@
 // keeps their K fragments in registers while the query rows pass, so every
 // token's sum is made by one warp in row order and added to memory once: the
 // result does not depend on timing (unless requests share the block).
+//
+// Measured: 64 requests of 512 to 4096 tokens (8 KV heads of 128, bf16), one
+// token each: 88 us, 3.5 TB/s of K.  Four CTAs an SM hide the loads; with the
+// next chunk's keys fetched ahead a thread needs 160 registers, three CTAs fit
+// and the call took 104 us.
 #pragma once
 
 #include "kvcs_attend.cuh"
