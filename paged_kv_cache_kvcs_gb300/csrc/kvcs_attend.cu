@@ -244,6 +244,7 @@ struct AttendPlan {
   bool narrow, wide, tc;
   int narrow_grid, wide_grid;      // wide_grid: the wide or the tensor-memory kernel's
   int splits;                      // tensor-memory kernel: parts per unit
+  long long units;                 // and units, at most
   long long wide_tickets;
   long long part_floats;
 };
@@ -270,6 +271,7 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
                                   : p.tab.total_new * p.group / kTcRows + std::min(R, p.tab.total_new);
     const long long units = tiles * p.kv_heads;
     // few units: the token ranges are split, as far as their parts stay long
+    pl.units = units;
     const long long key_tiles = p.tab.total_positions * p.map.block_size / std::max(1ll, R) / kTcKeys;
     pl.splits = static_cast<int>(std::max(
         1ll, std::min({sms / std::max(1ll, units), key_tiles / kTcMinTiles,
@@ -489,6 +491,7 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
     t.box = tc_box(*cache, block_size);
     t.heads_in_groups = cache->layout == KVCS_LAYOUT_HND;
     t.splits = pl.splits;
+    t.most_units = pl.units;
     t.timeout_ns = kAttendTimeoutNs;
     const bool bf16 = att->kv_dtype == KVCS_DTYPE_BF16;
     CUtensorMap mk, mv;

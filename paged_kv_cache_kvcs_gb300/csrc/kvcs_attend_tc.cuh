@@ -74,6 +74,8 @@ struct TcParams {
   int box;        // slots a TMA box takes
   int heads_in_groups;   // HND: the maps' groups of 8 slots run through the heads
   int splits;     // parts of the token range per unit
+  long long most_units;  // units that sound tables can have: partial results and
+                         // counters are there for no more
   u64 timeout_ns;
 };
 
@@ -235,7 +237,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_after();
   long long units = 0;
   for (int w = 0; w < kTcThreads / 32; ++w) units += s_sum[w];
-  units *= static_cast<long long>(a.kv_heads) * p.splits;
+  // (more than that only with requests that share rows, where offsets decrease
+  // somewhere, which the request there has flagged)
+  units = min(units * a.kv_heads, p.most_units) * p.splits;
   const u32 tmem = sh.tmem;
   // columns: S0, S1 (weights over their first half), O0, O1
   const u64 limit = p.timeout_ns;

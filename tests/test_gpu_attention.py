@@ -431,3 +431,18 @@ def test_mass_repeats_bit_for_bit(new):
                          max_new=max(new))
         got.append(mass)
     assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("R", [4, 12, 40])
+def test_requests_that_share_rows_stay_within_the_workspace(R):
+    """Offsets that decrease somewhere let requests share rows: more units
+    than sound tables have.  They are flagged, and nothing is written behind
+    the workspace that sound tables need, or in rows that no request owns."""
+    case = A.Case(dim=64, lengths=[2048] * R, new=[0] * (R - 1) + [264], seed=31)
+    case.new_offsets.copy_(torch.tensor([(r % 2) * 256 for r in range(R)] + [256]))
+    n = K.attention_workspace_bytes(case.cache, case.bs, R, case.total, case.q)
+    space = torch.full((n + (8 << 20),), 171, dtype=torch.uint8, device="cuda")
+    out = torch.full(case.q.shape, 7.0, dtype=case.q.dtype, device="cuda")
+    _, _, status = run(case, workspace=space, out=out)
+    assert status == K.KVCS_STATUS_BAD_REQUESTS
+    assert (space[n:] == 171).all() and (out[256:] == 7).all()
