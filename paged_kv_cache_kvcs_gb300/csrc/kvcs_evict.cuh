@@ -359,14 +359,16 @@ __global__ void __launch_bounds__(kEvictThreads)
   const PageMap &map = c.map;
 
   // addresses of a chunk, in the steps between which other work goes on: the
-  // list, the blocks, and the offsets
+  // list, the blocks, and the offsets.  (Requests that share positions, which
+  // is flagged, share their lists: an entry may be another request's.)
   constexpr int kOwn = kEvictChunk / kEvictThreads;
   int src[kOwn], from_id[kOwn], to_id[kOwn];
   auto look_list = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       const int j = j0 + i * kEvictThreads + tid;
-      src[i] = j < B ? list[j] : -1;
+      src[i] = j < B ? static_cast<int>(min(static_cast<u32>(list[j]), static_cast<u32>(q.keys - 1)))
+                     : -1;
     }
   };
   auto look_blocks = [&](int j0) {

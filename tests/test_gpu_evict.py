@@ -321,3 +321,24 @@ def test_a_cache_from_write_to_eviction():
                 # two roundings to bf16 (weights, output) and the sums' 2^-15
                 tol = (w @ v.abs()) * (2 ** -8 + 2 ** -13) + want.abs() * 2 ** -8 + 1e-6
                 assert ((out[r, h].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fresh", [False, True])
+def test_requests_that_share_positions_move_only_their_blocks(fresh):
+    """Positions that decrease somewhere let requests share them, and the
+    space of their lists: flagged, and only bytes of their blocks change."""
+    cases, sc = make(seed=41, layers=1, lengths=(160, 160, 400), spare=60)
+    c = cases[0]
+    c.table[0].copy_(torch.tensor([0, 10, 4, 10]))
+    used = [int(b) for b in c.ids[:10]]
+    kw = {}
+    if fresh:
+        spare = sorted(set(range(c.nb)) - set(c.ids.tolist()))
+        to = torch.tensor((spare * 2)[:c.total], dtype=torch.int32)
+        kw["new_block_ids"] = to.cuda()
+        used = to[:10].tolist()
+    before = c.pool.clone()
+    assert evict(cases, sc, [150, 150, 90], **kw) == K.KVCS_STATUS_BAD_REQUESTS
+    keep = torch.ones(before.numel(), dtype=torch.bool)
+    keep[c.offsets_map[:, used].flatten()] = False
+    assert torch.equal(c.pool.cpu()[keep], before.cpu()[keep])
