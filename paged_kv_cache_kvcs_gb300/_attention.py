@@ -160,16 +160,9 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     a = _attention_args(cache, q, new_offsets, R, index, kv_dtype, scale, softcap, window, k_scale,
                         v_scale, max_new)
     dev = q.device
-    handle = _stream_handle(stream, dev)
-    if out is None:
-        out = _empty(q.shape, q.dtype, stream, handle, dev)
-        a.out = out.data_ptr()
-    else:
+    if out is not None:
         a.out = _checked("out", out, q.dtype, q.numel(), index)
-    if lse is None:
-        lse = _empty(q.shape[:2], torch.float32, stream, handle, dev)
-        a.lse = lse.data_ptr()
-    else:
+    if lse is not None:
         a.lse = _checked("lse", lse, torch.float32, q.shape[0] * q.shape[1], index)
     B._check_status(status, dev)
     lib = B.load_library()
@@ -178,6 +171,13 @@ def paged_attention(cache, block_size: int, pos_offsets, first_position, num_tok
     a_ref = ctypes.byref(a)
     _raise(lib.kvcs_attention_workspace(arr, block_size, R, total, a_ref, 0, ctypes.byref(n)),
            "kvcs_attention_workspace")
+    handle = _stream_handle(stream, dev)
+    if out is None:
+        out = _empty(q.shape, q.dtype, stream, handle, dev)
+        a.out = out.data_ptr()
+    if lse is None:
+        lse = _empty(q.shape[:2], torch.float32, stream, handle, dev)
+        a.lse = lse.data_ptr()
     workspace = _workspace(workspace, n.value, stream, handle, dev)
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel()

@@ -231,21 +231,30 @@ bool query_map(CUtensorMap *map, const AttnParams &p, bool bf16, int tokens) {
 // The launches of one attention call.  A request's rows are its new tokens
 // times the query heads per KV head: up to 16 rows go to the narrow kernel,
 // more to the tensor-memory kernel, or to the wide one where that does not
-// take the cache or no request can have more than 64 rows.  max_new bounds
-// the rows, so a decode step launches only the narrow kernel; when total_new
-// = num_requests * max_new every request has max_new tokens and one kernel
-// is enough either way.
+// take the cache.  max_new bounds the rows, so a decode step launches only
+// the narrow kernel; when total_new = num_requests * max_new every request
+// has max_new tokens and one kernel is enough either way.
+//
+// 16 rows are one warp's product rows.  Beyond, with 32 query heads to 8 KV
+// heads of 128, bf16, the wide kernel against the tensor-memory one: 64
+// requests of 2048 tokens, 20 rows 197 and 122 us, 64 rows 247 and 127; one of
+// 32,768 tokens 93 and 35, 197 and 38; one of 1024 tokens, 32 rows, 37 and 16.
 constexpr int kNarrowRows = 16;
-constexpr int kWideRows = 64;
-constexpr int kMassRows = 32;    // observed rows the small mass kernel takes, at most
-constexpr int kTcMinTiles = 4;   // token tiles a part holds, at least (on average)
+// Observed rows the small mass kernel takes, at most (it against the
+// tensor-memory one, 64 requests of 2048 tokens: 16 rows 77 and 107 us, 32
+// rows 110 and 108, 64 rows 164 and 110; 4 of 8192: 20 and 31, 28 and 31, 42
+// and 31).
+constexpr int kMassRows = 32;
+// Token tiles a part holds, at least (on average).  256 rows over 1024, 512 and
+// 2048 tokens: at least 2 tiles 23, 23 and 23 us; 4 tiles 26, 18 and 26; 8
+// tiles 23, 18 and 31.
+constexpr int kTcMinTiles = 4;
 
 struct AttendPlan {
   bool narrow, wide, tc;
   int narrow_grid, wide_grid;      // wide_grid: the wide or the tensor-memory kernel's
   int splits;                      // tensor-memory kernel: parts per unit
   long long units;                 // and units, at most
-  long long wide_tickets;
   long long part_floats;
 };
 
@@ -256,7 +265,7 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
   const long long R = p.tab.num_requests;
   const bool alike = p.tab.total_new == R * p.tab.max_new;
   const bool more = rows > kNarrowRows;
-  pl.tc = rows > kWideRows && tc_takes(c, p.map.block_size, a);
+  pl.tc = more && tc_takes(c, p.map.block_size, a);
   pl.wide = more && !pl.tc;
   pl.narrow = !more || (!alike && p.group <= kNarrowRows);
   long long nf = 0, wf = 0;
@@ -265,7 +274,6 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
                                                : &AttendLaunch<kKvFp8>::shape;
   shape(p.head_dim, false, sms, &pl.narrow_grid, &nf);
   shape(p.head_dim, true, sms, &pl.wide_grid, &wf);
-  pl.wide_tickets = pl.wide_grid;
   if (pl.tc) {
     const long long tiles = alike ? R * ((rows + kTcRows - 1) / kTcRows)
                                   : p.tab.total_new * p.group / kTcRows + std::min(R, p.tab.total_new);
@@ -277,7 +285,6 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
         1ll, std::min({sms / std::max(1ll, units), key_tiles / kTcMinTiles,
                        static_cast<long long>(kTcMaxSplits)})));
     pl.wide_grid = static_cast<int>(std::min<long long>(sms, units * pl.splits));
-    pl.wide_tickets = pl.splits > 1 ? units * 8 : 0;   // one per warp's rows
     wf = pl.splits > 1 ? units * pl.splits * kTcRows * (p.head_dim + 4) : 0;
   }
   pl.part_floats = std::max(pl.narrow ? nf : 0, pl.wide || pl.tc ? wf : 0);
@@ -285,9 +292,11 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
 }
 
 // Counters first (both launches'), then the partial results.
-long long attend_tickets(const AttendPlan &pl) { return pl.narrow_grid + pl.wide_tickets; }
+long long attend_tickets(const AttendPlan &pl) {
+  return (pl.narrow ? pl.narrow_grid : 0) + (pl.wide ? pl.wide_grid : 0);
+}
 int64_t attend_workspace(const AttendPlan &pl) {
-  return (attend_tickets(pl) * 4 + 255) / 256 * 256 + pl.part_floats * 4;
+  return std::max((attend_tickets(pl) * 4 + 255) / 256 * 256, 256ll) + pl.part_floats * 4;
 }
 
 constexpr int kEvictSmemTokens = 49152;   // 192 KiB of scores
@@ -451,7 +460,7 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
   const int n_tickets = static_cast<int>(attend_tickets(pl));
   p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(att->workspace) +
                                      (n_tickets * 4ll + 255) / 256 * 256);
-  {
+  if (n_tickets > 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(1024);
@@ -478,7 +487,7 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
   if (pl.wide) {
     p.row_lo = pl.narrow ? kNarrowRows + 1 : 1;
     p.row_hi = 0x7fffffff;
-    p.tickets = tickets + pl.narrow_grid;
+    p.tickets = tickets + (pl.narrow ? pl.narrow_grid : 0);
     if (attend(p, true, pl.wide_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;
   }
   if (pl.tc) {
@@ -487,7 +496,6 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
     t.a = p;
     t.a.row_lo = pl.narrow ? kNarrowRows + 1 : 1;
     t.a.row_hi = 0x7fffffff;
-    t.a.tickets = tickets + pl.narrow_grid;
     t.box = tc_box(*cache, block_size);
     t.heads_in_groups = cache->layout == KVCS_LAYOUT_HND;
     t.splits = pl.splits;
@@ -500,10 +508,11 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
         !half_map(&mv, p.map, 1, p.kv_heads, p.head_dim, bf16, t.box, hig))
       return KVCS_ECUDA;
     auto run = bf16 ? &AttendLaunch<kKvBf16>::attend_tc : &AttendLaunch<kKvFp16>::attend_tc;
-    if (run(t, mk, mv, pl.wide_grid, after_zero, st) != cudaSuccess) return KVCS_ECUDA;
+    if (run(t, mk, mv, pl.wide_grid, st) != cudaSuccess) return KVCS_ECUDA;
   }
   if (cudaGetLastError() != cudaSuccess) return KVCS_ECUDA;
-  count_launches(1 + (pl.narrow ? 1 : 0) + (pl.wide ? 1 : 0) + (pl.tc ? 1 : 0));
+  count_launches((n_tickets > 0 ? 1 : 0) + (pl.narrow ? 1 : 0) + (pl.wide ? 1 : 0) +
+                 (pl.tc ? (pl.splits > 1 ? 2 : 1) : 0));
   return KVCS_OK;
 }
 

@@ -22,9 +22,10 @@ struct AttendLaunch {
   static void shape(int dim, bool wide, int sms, int *grid, long long *part_floats);
   static cudaError_t attend(const AttnParams &p, bool wide, int grid, bool after_zero,
                             cudaStream_t st);
-  // the tensor-memory kernel (16-bit caches, heads of 64 or 128)
+  // the tensor-memory kernel (16-bit caches, heads of 64 or 128), and the
+  // joining of its parts
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
-                               int grid, bool after_zero, cudaStream_t st);
+                               int grid, cudaStream_t st);
   static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st);
   static cudaError_t mass_tc(const MtParams &p, const CUtensorMap &k, const CUtensorMap &q, int grid,
                              cudaStream_t st);

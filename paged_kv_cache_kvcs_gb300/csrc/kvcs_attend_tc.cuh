@@ -74,8 +74,8 @@ struct TcParams {
   int box;        // slots a TMA box takes
   int heads_in_groups;   // HND: the maps' groups of 8 slots run through the heads
   int splits;     // parts of the token range per unit
-  long long most_units;  // units that sound tables can have: partial results and
-                         // counters are there for no more
+  long long most_units;  // units that sound tables can have: partial results
+                         // are there for no more
   u64 timeout_ns;
 };
 
@@ -134,6 +134,10 @@ struct TcFinder {
       }
       before += all;
       chunk += 32;
+      if (chunk >= a.tab.num_requests) {   // beyond the last unit
+        x.tiles = 0;
+        return x;
+      }
     }
     x.rows_all = x.q.n * a.group;
     x.tiles = x.rows_all - x.row0 > 128 ? 2 : 1;
@@ -720,83 +724,95 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (has && whole && a.lse) a.lse[out_row] = l == 0.0f ? kNegInf : kLn2 * (m + log2f(l));
         if (has && !whole) *reinterpret_cast<float2 *>(part + kDim) = make_float2(m, l);
       }
-      const int first = i * 128 + (warp & 3) * 32;   // the warp's rows of the unit
-      const int rows = min(32, x.rows_all - x.row0 - first);
-      if (!whole && work && rows > 0) {
-        // a counter per warp's rows: the last part's warp to arrive joins them, in order
-        ptx::grid_dep_wait();   // the counters are zero from here on
-        __threadfence();
-        __syncwarp();
-        u32 before_me = 0;
-        if (lane == 0) before_me = atomicAdd(a.tickets + x.index * 8 + warp, 1u);
-        if (__shfl_sync(0xffffffffu, before_me, 0) == static_cast<u32>(p.splits - 1)) {
-          __threadfence();
-          const float *const part0 =
-              a.part + (x.index * p.splits * kTcRows + first) * static_cast<long long>(S::kPartFloats);
-          constexpr long long kNext = static_cast<long long>(kTcRows) * S::kPartFloats;
-          // lane r: row r's factors; everything that is loaded is asked for at once
-          float f[kTcMaxSplits], ls[kTcMaxSplits], jm = kNegInf, jl = 0.0f;
-          const float *const ml_at = part0 + min(lane, rows - 1) * S::kPartFloats + kDim;
-#pragma unroll
-          for (int s = 0; s < kTcMaxSplits; ++s) {
-            float2 ml = make_float2(kNegInf, 0.0f);
-            if (s < p.splits) ml = __ldcg(reinterpret_cast<const float2 *>(ml_at + s * kNext));
-            f[s] = ml.x;
-            ls[s] = ml.y;
-          }
-#pragma unroll
-          for (int s = 0; s < kTcMaxSplits; ++s) jm = fmaxf(jm, f[s]);
-#pragma unroll
-          for (int s = 0; s < kTcMaxSplits; ++s) {
-            f[s] = ex2(f[s] - (jm == kNegInf ? 0.0f : jm));
-            jl += f[s] * ls[s];
-          }
-          const float inv = jl > 0.0f || jl != jl ? a.v_scale / jl : 0.0f;
-          if (lane < rows) store_lse(a, x.q, x.head, x.row0 + first + lane, jm, jl);
-          constexpr int kOwn = kDim / 32;   // columns a lane joins
-#pragma unroll 2
-          for (int r = 0; r < rows; ++r) {
-            const float *row_at = part0 + r * S::kPartFloats + lane * kOwn;
-            float v[kTcMaxSplits][kOwn], o[kOwn];
-#pragma unroll
-            for (int s = 0; s < kTcMaxSplits; ++s) {
-#pragma unroll
-              for (int c = 0; c < kOwn; ++c) v[s][c] = 0.0f;
-              if (s < p.splits) {
-                if constexpr (kOwn == 4)
-                  *reinterpret_cast<float4 *>(v[s]) =
-                      __ldcg(reinterpret_cast<const float4 *>(row_at + s * kNext));
-                else
-                  *reinterpret_cast<float2 *>(v[s]) =
-                      __ldcg(reinterpret_cast<const float2 *>(row_at + s * kNext));
-              }
-            }
-#pragma unroll
-            for (int c = 0; c < kOwn; ++c) o[c] = 0.0f;
-#pragma unroll
-            for (int s = 0; s < kTcMaxSplits; ++s) {
-              const float fs = __shfl_sync(0xffffffffu, f[s], r);
-#pragma unroll
-              for (int c = 0; c < kOwn; ++c) o[c] += fs * v[s][c];
-            }
-            const float by = __shfl_sync(0xffffffffu, inv, r);
-#pragma unroll
-            for (int c = 0; c < kOwn; c += 2)
-              store_out(a, x.q, x.head, x.row0 + first + r, lane * kOwn + c, o[c] * by,
-                        o[c + 1] * by, kBf16);
-          }
-        }
-      }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(released);
     }
   }
   if (!ok && lane == 0) raise(a.tab, kStatusTimeout);
-  ptx::grid_dep_wait();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (warp == 8) tc::tmem_free(tmem, 512);
+}
+
+// Joins the parts of split units: a warp per two rows, all their loads in
+// flight at once.  It waits for the parts' kernel as its programmatic
+// dependent, its tables read by then.  (Joined by the last part to arrive, as
+// kvcs_attend_kernel does, a warp had 32 rows one after another: 32 rows over
+// 32,768 tokens took 91 us, 142 with fewer loads in flight; now 37.)
+constexpr int kTcJoinThreads = 256;
+constexpr int kTcJoinRows = kTcJoinThreads / 16;   // a CTA
+
+template <bool kBf16, int kDim>
+__global__ void __launch_bounds__(kTcJoinThreads)
+    kvcs_attend_join_kernel(const __grid_constant__ TcParams p) {
+  using S = TcShape<kDim>;
+  constexpr int kCtas = kTcRows / kTcJoinRows;   // per unit
+  const AttnParams &a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long unit = blockIdx.x / kCtas;
+  const int first = static_cast<int>(blockIdx.x % kCtas) * kTcJoinRows + warp * 2;
+  TcFinder finder;
+  const TcUnit x = finder.find(p, unit * p.splits);
+  ptx::grid_dep_wait();
+  const int rows = min(2, x.tiles == 0 ? 0 : x.rows_all - x.row0 - first);
+  if (rows <= 0) return;
+  const float *const part0 =
+      a.part + (unit * p.splits * kTcRows + first) * static_cast<long long>(S::kPartFloats);
+  constexpr long long kNext = static_cast<long long>(kTcRows) * S::kPartFloats;
+  constexpr int kOwn = kDim / 32;   // columns a lane joins
+  // lane: row lane / 16, part lane % 16
+  const int mine = min(lane >> 4, rows - 1), s_mine = lane & 15;
+  static_assert(kTcMaxSplits == 16, "half a warp's lanes hold a row's parts");
+  float2 ml = make_float2(kNegInf, 0.0f);
+  if (s_mine < p.splits)
+    ml = __ldcg(reinterpret_cast<const float2 *>(part0 + mine * S::kPartFloats + s_mine * kNext + kDim));
+  float v[2][kTcMaxSplits][kOwn];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float *row_at = part0 + min(r, rows - 1) * S::kPartFloats + lane * kOwn;
+#pragma unroll
+    for (int s = 0; s < kTcMaxSplits; ++s) {
+#pragma unroll
+      for (int c = 0; c < kOwn; ++c) v[r][s][c] = 0.0f;
+      if (s < p.splits) {
+        if constexpr (kOwn == 4)
+          *reinterpret_cast<float4 *>(v[r][s]) =
+              __ldcg(reinterpret_cast<const float4 *>(row_at + s * kNext));
+        else
+          *reinterpret_cast<float2 *>(v[r][s]) =
+              __ldcg(reinterpret_cast<const float2 *>(row_at + s * kNext));
+      }
+    }
+  }
+  float jm = ml.x;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) jm = fmaxf(jm, __shfl_xor_sync(0xffffffffu, jm, o));
+  const float f = ex2(ml.x - (jm == kNegInf ? 0.0f : jm));
+  float jl = f * ml.y;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) jl += __shfl_xor_sync(0xffffffffu, jl, o);
+  const float inv = jl > 0.0f || jl != jl ? a.v_scale / jl : 0.0f;
+  if (s_mine == 0 && lane >> 4 < rows) store_lse(a, x.q, x.head, x.row0 + first + mine, jm, jl);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    float o[kOwn];
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c) o[c] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kTcMaxSplits; ++s) {
+      const float fs = __shfl_sync(0xffffffffu, f, r * 16 + s);
+#pragma unroll
+      for (int c = 0; c < kOwn; ++c) o[c] += fs * v[r][s][c];
+    }
+    const float by = __shfl_sync(0xffffffffu, inv, r * 16);
+    if (r < rows) {
+#pragma unroll
+      for (int c = 0; c < kOwn; c += 2)
+        store_out(a, x.q, x.head, x.row0 + first + r, lane * kOwn + c, o[c] * by, o[c + 1] * by,
+                  kBf16);
+    }
+  }
 }
 
 }  // namespace kvcs

@@ -58,7 +58,7 @@ struct TypeLaunch {
 
   template <int kDim, bool kPlain>
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
-                               int grid, bool after_zero, cudaStream_t st) {
+                               int grid, cudaStream_t st) {
     if constexpr (kType == kKvFp8) {
       return cudaErrorNotSupported;
     } else {
@@ -67,17 +67,18 @@ struct TypeLaunch {
       static std::atomic<u64> done{0};
       const cudaError_t e = allow_smem(kernel, smem, &done);
       if (e != cudaSuccess) return e;
+      kernel<<<static_cast<unsigned>(grid), kTcThreads, smem, st>>>(p, k, v);
+      if (p.splits == 1) return cudaGetLastError();
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(grid));
-      cfg.blockDim = dim3(kTcThreads);
-      cfg.dynamicSmemBytes = smem;
+      cfg.gridDim = dim3(static_cast<unsigned>(p.most_units * (kTcRows / kTcJoinRows)));
+      cfg.blockDim = dim3(kTcJoinThreads);
       cfg.stream = st;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attr[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = attr;
-      cfg.numAttrs = after_zero ? 1 : 0;
-      return cudaLaunchKernelEx(&cfg, kernel, p, k, v);
+      cfg.numAttrs = 1;
+      return cudaLaunchKernelEx(&cfg, kvcs_attend_join_kernel<kType == kKvBf16, kDim>, p);
     }
   }
 
@@ -132,12 +133,11 @@ cudaError_t AttendLaunch<kThisType>::attend(const AttnParams &p, bool wide, int 
 
 template <>
 cudaError_t AttendLaunch<kThisType>::attend_tc(const TcParams &p, const CUtensorMap &k,
-                                               const CUtensorMap &v, int grid, bool after_zero,
-                                               cudaStream_t st) {
+                                               const CUtensorMap &v, int grid, cudaStream_t st) {
   const bool plain = p.a.cap == 0.0f && p.a.scale > 0.0f;
   auto run = p.a.head_dim == 64 ? (plain ? &This::attend_tc<64, true> : &This::attend_tc<64, false>)
                                 : (plain ? &This::attend_tc<128, true> : &This::attend_tc<128, false>);
-  return run(p, k, v, grid, after_zero, st);
+  return run(p, k, v, grid, st);
 }
 
 template <>
