@@ -210,11 +210,11 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
     const int pos = p.by_block(j);
     return scores + blocks[pos] * per_block + at_head + (j - pos * bs);
   };
-  if (held) {
+  const int n_held = min(N, p.smem_tokens);
 #pragma unroll 4
-    for (int j = tid; j < N; j += threads) s_score[j] = *place(ids, j);
-  }
-  auto score = [&](int j) { return held ? s_score[j] : *place(ids, j); };
+  for (int j = tid; j < n_held; j += threads) s_score[j] = *place(ids, j);
+  auto score = [&](int j) { return j < n_held ? s_score[j] : *place(ids, j); };
+  constexpr int kAhead = 8;   // scores a thread asks for at once
 
   // the least key kept, and how many tokens of that key are
   u32 least = 0xffffffffu, ties = 0;
@@ -226,11 +226,18 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
       __syncthreads();
       for (u32 i = tid; i < bins; i += threads) s_hist[i] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int j = lo + tid; j < hi; j += threads) {
-        const u32 k = score_key(score(j));
-        if (shift == 21 || (k >> (shift + above)) == prefix)
-          atomicAdd(&s_hist[k >> shift & (bins - 1)], 1u);
+      for (int j0 = lo + tid; j0 < hi; j0 += kAhead * threads) {
+        u32 v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (j0 + i * threads < hi) v[i] = score(j0 + i * threads);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (j0 + i * threads >= hi) continue;
+          const u32 k = score_key(v[i]);
+          if (shift == 21 || (k >> (shift + above)) == prefix)
+            atomicAdd(&s_hist[k >> shift & (bins - 1)], 1u);
+        }
       }
       __syncthreads();
       // digits from the greatest down: the one where the count reaches `left`
@@ -260,19 +267,24 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
   }
 
   // Kept tokens in order.  A warp takes a run of words of 32 tokens, first
-  // counting, then, from the counts before it, marking and moving scores.
-  // (Scores that are not held in shared memory are moved by one warp alone,
-  // word after word: it reads a word's scores before it writes behind them.)
+  // counting, then, from the counts before it, marking.  Scores that are held
+  // move on the way; others follow behind, in steps.
   int *const list = row_list(p, row, q);
   const int words = (N + 31) / 32;
-  const int run = held ? (words + warps - 1) / warps : words;
-  const int w0 = min(words, held ? warp * run : warp == 0 ? 0 : words), w1 = min(words, w0 + run);
-  auto look = [&](int w, u32 *value, u32 *tie) {
+  const int run = (words + warps - 1) / warps;
+  const int w0 = min(words, warp * run), w1 = min(words, w0 + run);
+  auto read = [&](int w, u32 (&v)[kAhead]) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = (w + i) * 32 + lane;
+      v[i] = w + i < w1 && j < N ? score(j) : 0u;
+    }
+  };
+  auto look = [&](int w, u32 value, u32 *tie) {
     const int j = w * 32 + lane;
     bool stay = j < N && (all || j < lo || j >= hi), equal = false;
-    *value = j < N ? score(j) : 0u;
     if (j < N && !stay && want > 0) {
-      const u32 k = score_key(*value);
+      const u32 k = score_key(value);
       stay = k > least;
       equal = k == least;
     }
@@ -280,12 +292,17 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
     return __ballot_sync(0xffffffffu, stay);
   };
   int sure = 0, equal = 0;
-  if (held)
-    for (int w = w0; w < w1; ++w) {
-      u32 value, tie;
-      sure += __popc(look(w, &value, &tie));
+  for (int w = w0; w < w1; w += kAhead) {
+    u32 v[kAhead];
+    read(w, v);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (w + i >= w1) break;
+      u32 tie;
+      sure += __popc(look(w + i, v[i], &tie));
       equal += __popc(tie);
     }
+  }
   int total;
   const int tie0 = cta_scan(lane == 0 ? equal : 0, s_sums, &total);
   // of the equal ones the first are kept, as far as they are wanted
@@ -298,21 +315,45 @@ __global__ void __launch_bounds__(kEvictSelectThreads)
   const int kept = sure + taken(seen, equal);
   int done = cta_scan(lane == 0 ? kept : 0, s_sums, &total);
   done = __shfl_sync(0xffffffffu, done, 0);
-  for (int w = w0; w < w1; ++w) {
-    u32 value, tie;
-    u32 keep = look(w, &value, &tie);
-    const int n = __popc(tie);
-    u32 take = tie;
-    for (int extra = n - taken(seen, n); extra > 0; --extra) take &= ~(1u << (31 - __clz(take)));
-    keep |= take;
-    seen += n;
-    if (keep >> lane & 1u) {
-      const int j = done + __popc(keep & ((1u << lane) - 1u));
-      list[j] = w * 32 + lane;
-      *place(to_ids, j) = value;
+  for (int w = w0; w < w1; w += kAhead) {
+    u32 v[kAhead];
+    read(w, v);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (w + i >= w1) break;
+      u32 tie;
+      u32 keep = look(w + i, v[i], &tie);
+      const int n = __popc(tie);
+      u32 take = tie;
+      for (int extra = n - taken(seen, n); extra > 0; --extra) take &= ~(1u << (31 - __clz(take)));
+      keep |= take;
+      seen += n;
+      if (keep >> lane & 1u) {
+        const int j = done + __popc(keep & ((1u << lane) - 1u));
+        list[j] = (w + i) * 32 + lane;
+        if (held) *place(to_ids, j) = v[i];
+      }
+      done += __popc(keep);
     }
-    done += __popc(keep);
-    if (!held) __syncwarp();
+  }
+  if (held) return;
+  // The score of new token j comes from list[j] >= j: a step reads all of its
+  // scores before it writes any, and no later step reads what it wrote.
+  for (int j0 = 0; j0 < B; j0 += kAhead * threads) {
+    u32 v[kAhead];
+    __syncthreads();   // the list is there, the step before has written
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * threads + tid;
+      if (j < B)
+        v[i] = *place(ids, static_cast<int>(min(static_cast<u32>(list[j]), static_cast<u32>(N - 1))));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * threads + tid;
+      if (j < B) *place(to_ids, j) = v[i];
+    }
   }
 }
 

@@ -342,3 +342,24 @@ def test_requests_that_share_positions_move_only_their_blocks(fresh):
     keep = torch.ones(before.numel(), dtype=torch.bool)
     keep[c.offsets_map[:, used].flatten()] = False
     assert torch.equal(c.pool.cpu()[keep], before.cpu()[keep])
+
+
+@pytest.mark.parametrize("scores", ["random", "odd"])
+@pytest.mark.parametrize("keep", [1, 1000, 8192, 8193, 16000, 20011])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_one_long_request_among_short_ones(scores, keep, fresh):
+    """A row with more scores than the launch's shared memory holds (sized by
+    the average): part of them is read again, and they move in steps."""
+    lengths = [20011] + [5] * 40
+    cases, sc = make(seed=43, layers=1, lengths=lengths, heads=2, dim=8, bs=16, spare=1400,
+                     scores=scores)
+    c = cases[0]
+    kw, to = {}, None
+    if fresh:
+        spare = sorted(set(range(c.nb)) - set(c.ids.tolist()))
+        to = torch.tensor(spare[:c.total], dtype=torch.int32)
+        kw["new_block_ids"] = to.cuda()
+    keeps = [keep] + [3] * 40
+    want = expected(cases, sc, keeps, 7, 99, to)
+    assert evict(cases, sc, keeps, sinks=7, recent=99, **kw) == 0
+    same(cases, sc, want)
