@@ -367,7 +367,7 @@ int launch_evict(const EvictCall &call, const kvcs_cache *caches, float *const *
     e.first_row = static_cast<int>(first);
     e.unit = needs_8(c) ? 8 : 16;
     const int pieces = c.head_bytes / e.unit;
-    const int least = std::max(1, 128 / e.unit);
+    const int least = std::max(1, 32 / e.unit);
     // (at most a thread per piece)
     e.part_pieces = std::min(kEvictThreads, std::max(std::min(least, pieces),
                                                      (pieces + parts - 1) / parts));
@@ -376,6 +376,9 @@ int launch_evict(const EvictCall &call, const kvcs_cache *caches, float *const *
     first += c.num_heads;
   }
   const long long units = rows * p.halves_parts;
+  // into fresh blocks by runs of kept tokens too (one request, 40,011 tokens to
+  // 32,768: 128 us instead of 460; 20,011 to 4096: 61 instead of 95; with 96
+  // rows no difference: 130 and 126)
   p.spans = 1;
   if (p.new_block_ids)
     p.spans = static_cast<int>(std::max<int64_t>(
@@ -387,7 +390,8 @@ int launch_evict(const EvictCall &call, const kvcs_cache *caches, float *const *
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kEvictSmemTokens * 4) != cudaSuccess)
     return KVCS_ECUDA;
-  // large CTAs where the rows are few
+  // large CTAs where the rows are few (8 rows of 20,011 tokens: 98 us with 1024
+  // threads, 138 with 256; 1024 rows of 512 to 4096: 234 and 203)
   const int threads = rows < 4ll * sms ? kEvictSelectThreads : kEvictSelectThreads / 4;
   kvcs_evict_select_kernel<kCaches>
       <<<static_cast<unsigned>(rows), threads, p.smem_tokens * 4, st>>>(p);
@@ -622,7 +626,7 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   int launches = 0;
   p.by_block = FastDiv::of(static_cast<u32>(block_size));
   // scores in shared memory up to twice the average length; longer rows read
-  // them again in every pass
+  // the rest again in every pass (more would leave room for fewer rows an SM)
   const int64_t tokens = total_positions * block_size;
   const int64_t average = tokens / reqs->num_requests;
   p.smem_tokens = static_cast<int>(
@@ -637,11 +641,13 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   for (int32_t lo = 0; lo < num_caches;) {
     const EvictLaunch l = evict_launch(caches, lo, num_caches, reqs->num_requests);
     if (l.caches == 0) return KVCS_EUNSUPPORTED;
-    // few rows: each is split by halves and columns of at least 128 bytes, and
-    // into fresh blocks by runs of kept tokens too
+    // few rows: each is split by halves and columns of at least 32 bytes.  (One
+    // request, 8 rows, in place: 20,011 tokens to 4096 146 us unsplit, 102 with
+    // columns of 128 bytes, 74 of 64, 68 of 32; 131,072 to 65,536 1137, 706, 628
+    // from 128 on.  Four requests, 32 rows: 311, 212 of 64, 232 of 32.)
     const long long rows = l.rows * reqs->num_requests;
     int parts = 1;
-    while (parts < 8 && rows * 2 * parts < 2ll * sms) parts *= 2;
+    while (parts < 8 && rows * 2 * parts < sms) parts *= 2;
     p.num_caches = l.caches;
     p.rows = static_cast<int>(l.rows);
     p.list = static_cast<int *>(ev->workspace);

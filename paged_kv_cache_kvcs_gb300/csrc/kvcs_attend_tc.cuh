@@ -30,8 +30,8 @@
 // noted; the rows that do see them add them at the end.
 //
 // Measured (4 requests of 2048 new tokens over 8192, 32 query heads to 8 KV
-// heads of 128, bf16): 671 us, 1430 TFLOP/s, 76% of the measured burst rate of
-// a library product and 85% of its sustained rate.  With the weights left out
+// heads of 128, bf16): 664 us, 1445 TFLOP/s, 77% of the measured burst rate of
+// a library product and 86% of its sustained rate.  With the weights left out
 // the products and loads alone take 510 us.  What it grew from and what was
 // left again, for the same call: mma.sync 6300; one issuing thread for both
 // query tiles 1027; loads of 64-element halves, one warp for K and V 918 with
