@@ -550,7 +550,7 @@ int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_
     auto run = att->kv_dtype == KVCS_DTYPE_BF16   ? &AttendLaunch<kKvBf16>::mass
                : att->kv_dtype == KVCS_DTYPE_FP16 ? &AttendLaunch<kKvFp16>::mass
                                                   : &AttendLaunch<kKvFp8>::mass;
-    if (run(p, 4 * sms, st) != cudaSuccess) return KVCS_ECUDA;
+    if (run(p, sms, st) != cudaSuccess) return KVCS_ECUDA;
   }
   if (tc) {
     MtParams t;

@@ -26,7 +26,7 @@ struct AttendLaunch {
   // joining of its parts
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
                                int grid, cudaStream_t st);
-  static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st);
+  static cudaError_t mass(const AttnParams &p, int sms, cudaStream_t st);
   static cudaError_t mass_tc(const MtParams &p, const CUtensorMap &k, const CUtensorMap &q, int grid,
                              cudaStream_t st);
 };

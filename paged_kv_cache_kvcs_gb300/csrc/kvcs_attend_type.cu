@@ -83,8 +83,13 @@ struct TypeLaunch {
   }
 
   template <int kDim>
-  static cudaError_t mass(const AttnParams &p, int grid, cudaStream_t st) {
-    kvcs_mass_kernel<kType, kDim><<<static_cast<unsigned>(grid), kMassThreads, 0, st>>>(p);
+  static cudaError_t mass(const AttnParams &p, int sms, cudaStream_t st) {
+    using S = MassShape<kType, kDim>;
+    static std::atomic<u64> done{0};
+    const cudaError_t e = allow_smem(kvcs_mass_kernel<kType, kDim>, S::kSmemBytes, &done);
+    if (e != cudaSuccess) return e;
+    kvcs_mass_kernel<kType, kDim>
+        <<<static_cast<unsigned>(S::kCtas * sms), kMassThreads, S::kSmemBytes, st>>>(p);
     return cudaGetLastError();
   }
 
@@ -150,11 +155,11 @@ cudaError_t AttendLaunch<kThisType>::mass_tc(const MtParams &p, const CUtensorMa
 }
 
 template <>
-cudaError_t AttendLaunch<kThisType>::mass(const AttnParams &p, int grid, cudaStream_t st) {
+cudaError_t AttendLaunch<kThisType>::mass(const AttnParams &p, int sms, cudaStream_t st) {
   switch (This::width_of(p.head_dim)) {
-    case 64: return This::mass<64>(p, grid, st);
-    case 128: return This::mass<128>(p, grid, st);
-    default: return This::mass<256>(p, grid, st);
+    case 64: return This::mass<64>(p, sms, st);
+    case 128: return This::mass<128>(p, sms, st);
+    default: return This::mass<256>(p, sms, st);
   }
 }
 

@@ -4,15 +4,17 @@
 // with z and the visible (i, j) as in the attention, and lse from it.
 //
 // Bound: one product per (query row, token) and a read of K, so a decode
-// step is bound by the read of K.  A warp owns 16 tokens of one head and
-// keeps their K fragments in registers while the query rows pass, so every
-// token's sum is made by one warp in row order and added to memory once: the
-// result does not depend on timing (unless requests share the block).
+// step is bound by the read of K.  A warp owns 16 tokens of one head while the
+// query rows pass, so every token's sum is made by one warp in row order and
+// added to memory once: the result does not depend on timing (unless requests
+// share the block).  K comes through shared memory, each lane copying just
+// what it reads, two chunks ahead.
 //
 // Measured: 64 requests of 512 to 4096 tokens (8 KV heads of 128, bf16), one
-// token each: 88 us, 3.5 TB/s of K.  Four CTAs an SM hide the loads; with the
-// next chunk's keys fetched ahead a thread needs 160 registers, three CTAs fit
-// and the call took 104 us.
+// token each: 74 us, 4.2 TB/s of K; with the keys loaded to registers, 88 (a
+// chunk ahead 160 registers, three CTAs an SM, 104).  Four CTAs with three
+// stages; with two 74, three CTAs with four 83, five with two 81.  fp8 takes
+// 70: conversions and products, not DRAM.
 #pragma once
 
 #include "kvcs_attend.cuh"
@@ -20,6 +22,7 @@
 namespace kvcs {
 
 constexpr int kMassThreads = 128;
+constexpr int kMassStages = 3;   // chunks of a warp on their way or in use
 
 // A request's chunks of 16 tokens that some observed query may see.
 struct MassSpan {
@@ -45,11 +48,30 @@ __device__ __forceinline__ MassSpan mass_span(const AttnParams &p, const Request
 }
 
 template <int kType, int kDim>
-__global__ void __launch_bounds__(kMassThreads)
+struct MassShape {
+  static constexpr int kWords = kDim * (kType == kKvFp8 ? 1 : 2) / 64;   // 16-byte pieces of a key per lane
+  static constexpr int kStageBytes = 2 * kWords * 512;                   // a chunk of a warp
+  static constexpr int kStages = kWords > 4 ? 2 : kMassStages;
+  static constexpr int kSmemBytes = kMassThreads / 32 * kStages * kStageBytes;
+  static constexpr int kCtas = kDim > 128 ? 3 : 4;                       // per SM
+};
+
+// A chunk on its way: whose it is, and which of its tokens are there.
+struct MassChunk {
+  long long r;
+  int head, key0;
+  u32 valid;
+};
+
+template <int kType, int kDim>
+__global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
     kvcs_mass_kernel(const __grid_constant__ AttnParams p) {
+  using S = MassShape<kType, kDim>;
   constexpr int kElem = kType == kKvFp8 ? 1 : 2;
   constexpr bool kBf16 = kType == kKvBf16;
-  constexpr int kWords = kDim * kElem / 64;   // 16-byte pieces of a key per lane
+  constexpr int kWords = S::kWords;
+  extern __shared__ __align__(1024) unsigned char attend_smem[];
+  __shared__ MassChunk s_chunk[kMassThreads / 32][S::kStages];
   __shared__ long long s_scan[4];
   __shared__ long long s_req[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -84,27 +106,21 @@ __global__ void __launch_bounds__(kMassThreads)
   }
   Request q = read_request(p.tab, r, p.map.block_size, false);
   MassSpan sp = mass_span(p, q);
-  // The CTA's run goes round its warps.  A warp keeps the queries of a group
-  // that fits one tile of 16 rows (a decode step) from chunk to chunk.
-  u32 qf[kDim / 8][2];
-  float rs[2], lse[2];
-  int at[2];
-  long long held_r = -1;
-  int held_head = -1;
-  for (long long x = a_cta + warp; x < b_cta; x += kMassThreads / 32) {
-    while (x >= before + sp.total) {
-      before += sp.total;
-      ++r;
-      q = read_request(p.tab, r, p.map.block_size, false);
-      sp = mass_span(p, q);
-    }
-    const long long w = x - before;
-    const int head = static_cast<int>(w / sp.chunks);
-    const int key0 = (sp.lo + static_cast<int>(w % sp.chunks)) * kChunkKeys;
-    // this lane's two keys, j * 8 + pg
-    uint4 k[2][kWords];
-    u32 valid = 0;
-    {
+  // The CTA's run goes round its warps.  A lane copies the pieces that it will
+  // read itself, so a stage needs no more than the lane's own wait.
+  const u32 ring = ptx::smem_addr(attend_smem) + warp * S::kStages * S::kStageBytes + lane * 16;
+  int put = 0;
+  auto fetch = [&](long long x) {
+    if (x < b_cta) {
+      while (x >= before + sp.total) {
+        before += sp.total;
+        ++r;
+        q = read_request(p.tab, r, p.map.block_size, false);
+        sp = mass_span(p, q);
+      }
+      const long long w = x - before;
+      const int head = static_cast<int>(w / sp.chunks);
+      const int key0 = (sp.lo + static_cast<int>(w % sp.chunks)) * kChunkKeys;
       const int key = key0 + (lane & 15);
       // (blocks of tokens that no observed row sees are not looked at)
       bool ok = key < q.keys && key < q.at + q.n &&
@@ -120,47 +136,69 @@ __global__ void __launch_bounds__(kMassThreads)
           off = token_offset(p.map, block, key - pos * p.map.block_size, head);
         }
       }
-      valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const u32 valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       const int row_bytes = p.head_dim * kElem;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2; ++j) {   // this lane's two keys, j * 8 + pg
         const long long o = __shfl_sync(0xffffffffu, off, j * 8 + pg);
-        const bool live = valid >> (j * 8 + pg) & 1u;
-        const unsigned char *src = p.map.base + o;
+        const int there = valid >> (j * 8 + pg) & 1u ? row_bytes : 0;
 #pragma unroll
         for (int b = 0; b < kWords; ++b) {
           const int c = 4 * b + t;
-          const unsigned char *at = src + static_cast<long long>(c) * p.map.chunk_stride;
-          k[j][b] = make_uint4(0, 0, 0, 0);
-          if (live && c * 16 < row_bytes) {
-            if (!p.unit8) {
-              k[j][b] = __ldg(reinterpret_cast<const uint4 *>(at));
-            } else {
-              const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(at));
-              k[j][b].x = lo.x;
-              k[j][b].y = lo.y;
-              if (c * 16 + 8 < row_bytes) {
-                const uint2 hi = __ldg(reinterpret_cast<const uint2 *>(at + 8));
-                k[j][b].z = hi.x;
-                k[j][b].w = hi.y;
-              }
-            }
+          const unsigned char *src = p.map.base;   // (not read where nothing is there)
+          if (c * 16 < there) src += o + static_cast<long long>(c) * p.map.chunk_stride;
+          const u32 dst = ring + put * S::kStageBytes + (j * kWords + b) * 512;
+          if (!p.unit8) {
+            cp_async16(dst, src, c * 16 < there ? 16 : 0);
+          } else {
+            cp_async8z(dst, src, c * 16 < there ? 8 : 0);
+            cp_async8z(dst + 8, c * 16 + 8 < there ? src + 8 : src, c * 16 + 8 < there ? 8 : 0);
           }
         }
       }
+      if (lane == 0) s_chunk[warp][put] = MassChunk{r, head, key0, valid};
+      put = put + 1 == S::kStages ? 0 : put + 1;
+    }
+    cp_async_commit();
+  };
+  constexpr int kWarps = kMassThreads / 32;
+#pragma unroll 1
+  for (int i = 0; i < S::kStages - 1; ++i) fetch(a_cta + warp + i * kWarps);
+  // A warp keeps the queries of a group that fits one tile of 16 rows (a
+  // decode step) from chunk to chunk.
+  u32 qf[kDim / 8][2];
+  float rs[2], lse[2];
+  int at[2];
+  long long held_r = -1, now_r = -1;
+  int held_head = -1, stage = 0;
+  Request now;
+  int now_first = 0;
+  for (long long x = a_cta + warp; x < b_cta; x += kWarps) {
+    cp_async_wait<S::kStages - 2>();
+    __syncwarp();
+    const MassChunk chunk = s_chunk[warp][stage];
+    const int head = chunk.head, key0 = chunk.key0;
+    const u32 valid = chunk.valid;
+    const u32 keys = ring + stage * S::kStageBytes;
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    fetch(x + (S::kStages - 1) * kWarps);
+    if (chunk.r != now_r) {
+      now_r = chunk.r;
+      now = read_request(p.tab, now_r, p.map.block_size, false);
+      now_first = mass_span(p, now).first;
     }
     float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};   // tokens j * 8 + t + 4 i
     // observed tokens that see some key of the chunk (all of a small group)
-    const bool small = (q.n - sp.first) * p.group <= 16;
-    const int i0 = small ? sp.first : max(sp.first, key0 - q.at);
-    int i1 = q.n;
+    const bool small = (now.n - now_first) * p.group <= 16;
+    const int i0 = small ? now_first : max(now_first, key0 - now.at);
+    int i1 = now.n;
     if (p.window > 0 && !small)
       i1 = static_cast<int>(min(static_cast<long long>(i1),
-                                static_cast<long long>(key0) + kChunkKeys - 1 + p.window - q.at));
+                                static_cast<long long>(key0) + kChunkKeys - 1 + p.window - now.at));
     const int rows_end = i1 * p.group;
 #pragma unroll 1
     for (int row0 = i0 * p.group; row0 < rows_end; row0 += 16) {
-      if (!small || r != held_r || head != held_head) {
+      if (!small || now_r != held_r || head != held_head) {
         int row[2];
         bool has[2];
 #pragma unroll
@@ -169,12 +207,12 @@ __global__ void __launch_bounds__(kMassThreads)
           has[i] = rr < rows_end;
           row[i] = has[i] ? rr : row0;
           const int ti = p.by_group(row[i]);
-          at[i] = has[i] ? q.at + ti : -1;   // spare rows see nothing
-          lse[i] = kLog2e * __ldg(p.lse + (q.q0 + ti) * (p.group * p.kv_heads) + head * p.group +
+          at[i] = has[i] ? now.at + ti : -1;   // spare rows see nothing
+          lse[i] = kLog2e * __ldg(p.lse + (now.q0 + ti) * (p.group * p.kv_heads) + head * p.group +
                                   row[i] - ti * p.group);
         }
-        load_queries<kType, kDim>(p, q, head, row, has, qf, rs);
-        held_r = small ? r : -1;
+        load_queries<kType, kDim>(p, now, head, row, has, qf, rs);
+        held_r = small ? now_r : -1;
         held_head = head;
       }
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -182,8 +220,9 @@ __global__ void __launch_bounds__(kMassThreads)
       for (int b = 0; b < kWords; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          const uint4 k = lds128(keys + (j * kWords + b) * 512);
           if constexpr (kType == kKvFp8) {
-            const u32 kw[4] = {k[j][b].x, k[j][b].y, k[j][b].z, k[j][b].w};
+            const u32 kw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               u32 lo, hi;
@@ -194,9 +233,9 @@ __global__ void __launch_bounds__(kMassThreads)
             }
           } else {
             mma16816<kBf16>(s[j], qf[4 * b][0], qf[4 * b][1], qf[4 * b + 1][0], qf[4 * b + 1][1],
-                            k[j][b].x, k[j][b].y);
+                            k.x, k.y);
             mma16816<kBf16>(s[j], qf[4 * b + 2][0], qf[4 * b + 2][1], qf[4 * b + 3][0],
-                            qf[4 * b + 3][1], k[j][b].z, k[j][b].w);
+                            qf[4 * b + 3][1], k.z, k.w);
           }
         }
 #pragma unroll
@@ -220,7 +259,7 @@ __global__ void __launch_bounds__(kMassThreads)
         const int kk = j * 8 + t + 4 * i;
         if (g == 0 && (valid >> kk & 1u)) {
           const int key = key0 + kk, pos = p.map.by_block(key);
-          const long long block = p.tab.block_ids[q.pos0 + pos];
+          const long long block = p.tab.block_ids[now.pos0 + pos];
           atomicAdd(p.mass + (block * p.kv_heads + head) * p.map.block_size +
                         (key - pos * p.map.block_size), v);
         }
