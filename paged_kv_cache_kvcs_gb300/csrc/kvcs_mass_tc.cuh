@@ -32,7 +32,7 @@ namespace kvcs {
 constexpr int kMtKeys = 256;       // tokens of a unit
 constexpr int kMtQStages = 3;      // query tiles in flight
 constexpr int kMtLseStages = 3;
-constexpr int kMtControl = 3072;   // bytes ahead of the tiles
+constexpr int kMtControl = 3 * 1024;   // bytes ahead of the tiles
 // Five warpgroups: four for the sums (two per token tile, each for one half of
 // a query tile's rows: with one, a scheduler had two warps to hide each step's
 // latencies with, and 4 x 2048 queries over 8192 tokens took 435 us, not 423),
@@ -407,11 +407,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(s_empty + 16 * i + 8 * (n_s & 1));
           ++n_s;
-          if constexpr (!kPlain) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              s[c] = __float_as_uint(score_of(a, __uint_as_float(s[c]), 1.0f));
-          }
+          if constexpr (!kPlain) make_scores(a, s);
           const int row0 = t * width + hf * 64;   // this half's first row
           const bool full = width == 128 && all_lo <= row0 && all_hi >= row0 + 64;
           // weights, 0 where the row does not see the token (whatever the

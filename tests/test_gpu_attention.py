@@ -446,3 +446,15 @@ def test_requests_that_share_rows_stay_within_the_workspace(R):
     _, _, status = run(case, workspace=space, out=out)
     assert status == K.KVCS_STATUS_BAD_REQUESTS
     assert (space[n:] == 171).all() and (out[256:] == 7).all()
+
+
+@pytest.mark.parametrize("softcap", [0.5, 7.0, 40.0, 1e4])
+@pytest.mark.parametrize("kv", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_capped_scores_on_either_side_of_the_cap(softcap, kv, dim):
+    """Scores that all lie far above the cap, on both sides of it (within a
+    tile too), and far below it."""
+    case = A.Case(kv=kv, lengths=[700, 300], new=[130, 20], seed=33, dim=dim, scale=2.0)
+    check(case, softcap=softcap, scale=4.0 / dim)
+    check_mass(case, softcap=softcap, scale=4.0 / dim)
+    check(case, softcap=softcap, scale=-4.0 / dim)
