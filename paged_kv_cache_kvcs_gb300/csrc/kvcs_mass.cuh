@@ -11,10 +11,11 @@
 // what it reads, two chunks ahead.
 //
 // Measured: 64 requests of 512 to 4096 tokens (8 KV heads of 128, bf16), one
-// token each: 74 us, 4.2 TB/s of K; with the keys loaded to registers, 88 (a
-// chunk ahead 160 registers, three CTAs an SM, 104).  Four CTAs with three
-// stages; with two 74, three CTAs with four 83, five with two 81.  fp8 takes
-// 70: conversions and products, not DRAM.
+// token each: 57 us, 5.4 TB/s of K.  With the keys loaded to registers 88 (a
+// chunk ahead 160 registers, three CTAs an SM, 104); with divisions for each
+// chunk's place, a test for each piece and four additions to memory of four
+// lanes each, 74.  Four CTAs with three stages; three with four 60, five with
+// two 58.  fp8 takes 52 (59, 68): conversions and products, not DRAM.
 #pragma once
 
 #include "kvcs_attend.cuh"
@@ -106,10 +107,11 @@ __global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
   }
   Request q = read_request(p.tab, r, p.map.block_size, false);
   MassSpan sp = mass_span(p, q);
+  constexpr int kWarps = kMassThreads / 32;
   // The CTA's run goes round its warps.  A lane copies the pieces that it will
   // read itself, so a stage needs no more than the lane's own wait.
   const u32 ring = ptx::smem_addr(attend_smem) + warp * S::kStages * S::kStageBytes + lane * 16;
-  int put = 0;
+  int put = 0, f_head = 0, f_chunk = -1;   // the next chunk's, counted on
   auto fetch = [&](long long x) {
     if (x < b_cta) {
       while (x >= before + sp.total) {
@@ -117,10 +119,19 @@ __global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
         ++r;
         q = read_request(p.tab, r, p.map.block_size, false);
         sp = mass_span(p, q);
+        f_chunk = -1;
       }
-      const long long w = x - before;
-      const int head = static_cast<int>(w / sp.chunks);
-      const int key0 = (sp.lo + static_cast<int>(w % sp.chunks)) * kChunkKeys;
+      if (f_chunk < 0) {
+        f_head = static_cast<int>((x - before) / sp.chunks);
+        f_chunk = static_cast<int>((x - before) % sp.chunks);
+      } else {
+        f_chunk += kWarps;
+        while (f_chunk >= sp.chunks) {
+          f_chunk -= sp.chunks;
+          ++f_head;
+        }
+      }
+      const int key0 = (sp.lo + f_chunk) * kChunkKeys;
       const int key = key0 + (lane & 15);
       // (blocks of tokens that no observed row sees are not looked at)
       bool ok = key < q.keys && key < q.at + q.n &&
@@ -133,35 +144,42 @@ __global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
           ok = false;
           raise(p.tab, kStatusBadBlockId);
         } else {
-          off = token_offset(p.map, block, key - pos * p.map.block_size, head);
+          off = token_offset(p.map, block, key - pos * p.map.block_size, f_head);
         }
       }
       const u32 valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       const int row_bytes = p.head_dim * kElem;
+      const bool plain = !p.unit8 && row_bytes == kDim * kElem;   // whole 16-byte pieces
 #pragma unroll
       for (int j = 0; j < 2; ++j) {   // this lane's two keys, j * 8 + pg
-        const long long o = __shfl_sync(0xffffffffu, off, j * 8 + pg);
+        const long long o = __shfl_sync(0xffffffffu, off, j * 8 + pg);   // (0 where nothing is)
         const int there = valid >> (j * 8 + pg) & 1u ? row_bytes : 0;
+        const u32 dst = ring + put * S::kStageBytes + j * kWords * 512;
+        const unsigned char *src = p.map.base + o + t * static_cast<long long>(p.map.chunk_stride);
+        if (plain) {
 #pragma unroll
-        for (int b = 0; b < kWords; ++b) {
-          const int c = 4 * b + t;
-          const unsigned char *src = p.map.base;   // (not read where nothing is there)
-          if (c * 16 < there) src += o + static_cast<long long>(c) * p.map.chunk_stride;
-          const u32 dst = ring + put * S::kStageBytes + (j * kWords + b) * 512;
-          if (!p.unit8) {
-            cp_async16(dst, src, c * 16 < there ? 16 : 0);
-          } else {
-            cp_async8z(dst, src, c * 16 < there ? 8 : 0);
-            cp_async8z(dst + 8, c * 16 + 8 < there ? src + 8 : src, c * 16 + 8 < there ? 8 : 0);
+          for (int b = 0; b < kWords; ++b)
+            cp_async16(dst + b * 512, src + b * (4ll * p.map.chunk_stride), there ? 16 : 0);
+        } else {
+#pragma unroll
+          for (int b = 0; b < kWords; ++b) {
+            const int c = 4 * b + t;
+            const unsigned char *at = c * 16 < there ? src + b * (4ll * p.map.chunk_stride) : p.map.base;
+            if (!p.unit8) {
+              cp_async16(dst + b * 512, at, c * 16 < there ? 16 : 0);
+            } else {
+              cp_async8z(dst + b * 512, at, c * 16 < there ? 8 : 0);
+              cp_async8z(dst + b * 512 + 8, c * 16 + 8 < there ? at + 8 : at,
+                         c * 16 + 8 < there ? 8 : 0);
+            }
           }
         }
       }
-      if (lane == 0) s_chunk[warp][put] = MassChunk{r, head, key0, valid};
+      if (lane == 0) s_chunk[warp][put] = MassChunk{r, f_head, key0, valid};
       put = put + 1 == S::kStages ? 0 : put + 1;
     }
     cp_async_commit();
   };
-  constexpr int kWarps = kMassThreads / 32;
 #pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) fetch(a_cta + warp + i * kWarps);
   // A warp keeps the queries of a group that fits one tile of 16 rows (a
@@ -248,22 +266,22 @@ __global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
             acc[j][i & 1] += ex2(score_of(p, s[j][i], rs[i >> 1]) - lse[i >> 1]);
         }
     }
+    // over the 8 lanes of a token: each exchange halves what a lane holds, and
+    // lane kk ends up with token kk
+    const bool hi_i = lane & 4, hi_j = lane & 8;
+    float v[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v = acc[j][i];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        const int kk = j * 8 + t + 4 * i;
-        if (g == 0 && (valid >> kk & 1u)) {
-          const int key = key0 + kk, pos = p.map.by_block(key);
-          const long long block = p.tab.block_ids[now.pos0 + pos];
-          atomicAdd(p.mass + (block * p.kv_heads + head) * p.map.block_size +
-                        (key - pos * p.map.block_size), v);
-        }
-      }
+      v[j] = (hi_i ? acc[j][1] : acc[j][0]) +
+             __shfl_xor_sync(0xffffffffu, hi_i ? acc[j][0] : acc[j][1], 4);
+    float sum_kk = (hi_j ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi_j ? v[0] : v[1], 8);
+    sum_kk += __shfl_xor_sync(0xffffffffu, sum_kk, 16);
+    if (lane < 16 && (valid >> lane & 1u)) {
+      const int key = key0 + lane, pos = p.map.by_block(key);
+      const long long block = p.tab.block_ids[now.pos0 + pos];
+      atomicAdd(p.mass + (block * p.kv_heads + head) * p.map.block_size +
+                    (key - pos * p.map.block_size), sum_kk);
+    }
   }
 }
 
