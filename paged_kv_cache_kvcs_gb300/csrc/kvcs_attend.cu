@@ -241,9 +241,9 @@ bool query_map(CUtensorMap *map, const AttnParams &p, bool bf16, int tokens) {
 // 32,768 tokens 93 and 35, 197 and 38; one of 1024 tokens, 32 rows, 37 and 16.
 constexpr int kNarrowRows = 16;
 // Observed rows the small mass kernel takes, at most (it against the
-// tensor-memory one, 64 requests of 2048 tokens: 16 rows 77 and 107 us, 32
-// rows 110 and 108, 64 rows 164 and 110; 4 of 8192: 20 and 31, 28 and 31, 42
-// and 31).
+// tensor-memory one, 64 requests of 2048 tokens: 16 rows 52 and 107 us, 32
+// rows 93 and 107, 40 rows 117 and 107, 64 rows 147 and 110; 4 of 8192: 15 and
+// 31, 25 and 31, 32 and 31, 39 and 30).
 constexpr int kMassRows = 32;
 // Token tiles a part holds, at least (on average).  256 rows over 1024, 512 and
 // 2048 tokens: at least 2 tiles 23, 23 and 23 us; 4 tiles 26, 18 and 26; 8
