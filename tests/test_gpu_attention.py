@@ -458,3 +458,17 @@ def test_capped_scores_on_either_side_of_the_cap(softcap, kv, dim):
     check(case, softcap=softcap, scale=4.0 / dim)
     check_mass(case, softcap=softcap, scale=4.0 / dim)
     check(case, softcap=softcap, scale=-4.0 / dim)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=700), dict(softcap=9.0, scale=-0.1)], ids=str)
+@pytest.mark.parametrize("new,lengths", [([5, 1, 64, 130, 2], [9000, 30, 4100, 2000, 3]),
+                                         ([17], [5000]), ([40] + [1] * 40, [12000] + [500] * 40),
+                                         ([100, 20], [60, 7000])])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_split_chunks_among_others(kw, new, lengths, dim):
+    """Chunks whose token ranges are split and joined, beside decode steps,
+    rows that see nothing, and parts that a window leaves empty."""
+    case = A.Case(dim=dim, heads=2, group=4, lengths=lengths, new=new, seed=44)
+    check(case, **kw)
+    check(case, max_new="unknown", **kw)
+    check_mass(case, **kw)
