@@ -487,7 +487,8 @@ int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_
  *           its tokens are left out, as if masked.  KVCS_STATUS_BAD_REQUESTS:
  *           inconsistent tables (also more than 2^30 cached tokens in one
  *           request): the request's rows see nothing (or, where its
- *           new_offsets are at fault, are left as they were).
+ *           new_offsets are at fault, are left as they were; rows that two
+ *           requests claim, where offsets decrease, have no defined result).
  *
  * Results do not depend on timing: the same call gives the same bits.
  * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a
@@ -564,9 +565,9 @@ int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_
  * arguments as in kvcs_block_checksums.
  *
  * Blocks that the call writes must belong to one request alone (in place:
- * all its blocks), listed once.  A request with a bad block id
- * (KVCS_STATUS_BAD_BLOCK_ID), inconsistent tables or a negative keep
- * (KVCS_STATUS_BAD_REQUESTS) is left untouched.
+ * all its blocks), listed once; the caches' pools and scores must not overlap.
+ * A request with a bad block id (KVCS_STATUS_BAD_BLOCK_ID), inconsistent tables
+ * or a negative keep (KVCS_STATUS_BAD_REQUESTS) is left untouched.
  * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a
  * STATE cache, a negative count, missing or misaligned pointers or a short
  * workspace; KVCS_EUNSUPPORTED for a page of 2 GiB or more, or 2^31 or more
