@@ -472,3 +472,20 @@ def test_split_chunks_among_others(kw, new, lengths, dim):
     check(case, **kw)
     check(case, max_new="unknown", **kw)
     check_mass(case, **kw)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 0), (128, 1500)])
+def test_nonfinite_values_in_split_chunks(kv, dim, window):
+    """NaN and infinite V that only the later rows of a split chunk see, in
+    another part than most of their tokens, and NaN before the window."""
+    case = A.Case(kv=kv, dim=dim, lengths=[6000], new=[64], seed=45)
+    case.put(0, 1, 5990, torch.full((1, dim), float("nan")))
+    case.put(0, 1, 5970, torch.full((1, dim), float("inf")))
+    if window:
+        case.put(0, 1, 100, torch.full((1, dim), float("nan")))
+    out, lse, _ = run(case, window=window, max_new=64)
+    ref = A.attention(case, window=window)
+    A.close(lse, ref[1], ref[3])
+    A.close(out, ref[0], ref[2])
+    assert torch.isfinite(ref[0][:34]).all() and torch.isnan(ref[0][54:]).all()
