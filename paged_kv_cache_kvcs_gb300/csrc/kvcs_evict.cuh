@@ -33,10 +33,10 @@
 // with t the token's new position, are added while the bytes pass through.
 //
 // Measured: 8 layers of 16 requests of 512 to 4096 tokens (8 KV heads of 128,
-// bf16) down to 1024 in place: 190 us from fresh caches (885 MB, 4.7 TB/s),
-// about 45 of them the selection; 32 layers of 32 requests 1460 us, 5.9 TB/s;
+// bf16) down to 1024 in place: 203 us from fresh caches (885 MB, 4.4 TB/s),
+// about 46 of them the selection; 32 layers of 32 requests 1460 us, 5.9 TB/s;
 // three requests of 6001 to 20,011 tokens, 4 layers, into fresh HND blocks with
-// their words: 126 us; one request of 613 tokens, one layer: 14 us, of 131,072
+// their words: 131 us; one request of 613 tokens, one layer: 14 us, of 131,072
 // down to 65,536 628 us.  The first form, one kernel a row, took 277 us for the
 // first, 628 for the fresh blocks and 49 for the short request.
 #pragma once
