@@ -428,6 +428,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // step and both waiting: 863 us.  One warp for both tiles shows its waits,
     // 721 us.)  A warp stays together and one lane issues: with the waits
     // inside a one-lane branch the whole took 822 us.
+    // Every step is handed over and waited for, a unit's last one too (but for
+    // tile 0's very first): a barrier shows its phase's parity alone, so that
+    // a second turn given before the first is taken would read as none.
     constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
     constexpr u32 kDescO = tc::instr_desc(kBf16, 128, kDim, true);
     const int i = warp == 8 ? 0 : 1;
@@ -435,6 +438,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const u32 q_low = tc::desc_low(q_smem + i * S::kTileBytes, 16);
     const u32 k_low = tc::desc_low(ring, 16), v_low = tc::desc_low(ring, 1024);
     u32 stage = 0, turn = 0, n_q = 0, n_p = 0, n_t = 0;   // stage: ring position, turn: its phase
+    bool begun = i == 1;   // tile 0 begins
     auto next_stage = [&]() {
       if (++stage == S::kStages) {
         stage = 0;
@@ -463,8 +467,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (k == x.k0) ok = ok && tc::wait(q_full + 8 * i, n_q++ & 1, limit);
         }
         if (do_o) ok = ok && tc::wait(p_half + 8 * i, n_p & 1, limit);
-        if (pair && (i == 1 || k > x.k0)) ok = ok && tc::wait(turns + 8 * i, n_t++ & 1, limit);
+        if (pair && begun) ok = ok && tc::wait(turns + 8 * i, n_t++ & 1, limit);
         if (!ok) break;
+        begun |= pair;
         tc::fence_after();
         if (do_o) {
           // half of the weights at a time: the second half is made while the
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::commit(s_full + 8 * i);
             if (last) tc::commit(empty + 8 * k_stage);
           }
-          if (pair && (i == 0 || do_s)) ptx::mbar_arrive(turns + 8 * (1 - i));
+          if (pair) ptx::mbar_arrive(turns + 8 * (1 - i));
         }
         __syncwarp();
       }

@@ -1,0 +1,257 @@
+"""Model check of the barriers between the warps of the attention kernel for
+chunks, on the CPU.
+
+Two loading warps (K and V) fill a ring of shared-memory stages; a product
+warp per query tile issues S_i = Q_i K^T and O_i += P_i V, the two taking
+turns; the softmax warps of a tile turn S into the weights P, in place.  The
+model replays this under random interleavings: no step takes any particular
+time, copies land in any order, and products run after they were issued, in
+the order of their own thread alone.  Barriers only show phase parity, as on
+the card (``Bar`` of test_pipeline_protocol).
+
+Checked: nothing stalls, every product finds the tile, the queries and the
+weights that it is meant for (when it runs, not when it is issued), and no
+copy lands in a stage that a product still reads.
+"""
+
+import random
+
+import pytest
+
+from test_pipeline_protocol import Bar
+
+WARPS = 2        # softmax warps of a query tile (four on the card)
+
+
+class Wrong(AssertionError):
+    pass
+
+
+class Stall(AssertionError):
+    pass
+
+
+class Machine:
+    """Actors are generators that yield (barrier, parity) to wait, or None
+    between two steps.  Tensor-core queues and copies in flight act too."""
+
+    def __init__(self, seed):
+        self.rnd = random.Random(seed)
+        self.actors, self.waits = {}, {}
+        self.flying, self.queues = [], {}
+
+    def add(self, name, gen):
+        self.actors[name], self.waits[name] = gen, None
+
+    def run(self, most=200000):
+        rnd, idle = self.rnd, 0
+        # some interleavings hold one actor back for long
+        slow = rnd.choice([None, *self.actors, *self.queues, "copies"])
+        for _ in range(most):
+            ready = [*self.actors] + [q for q in self.queues if self.queues[q]] + \
+                    (["copies"] if self.flying else [])
+            if not ready:
+                return
+            a = rnd.choice(ready)
+            if a == slow and idle < 40 and rnd.random() < 0.97:
+                idle += 1
+                continue
+            if a == "copies":
+                self.flying.pop(rnd.randrange(len(self.flying)))()
+            elif a in self.queues:
+                self.queues[a].pop(0)()
+            else:
+                w = self.waits[a]
+                if w is not None and not w[0].try_wait(w[1] & 1):
+                    idle += 1
+                    if idle > 60 * len(ready) and not self.flying and \
+                            not any(self.queues.values()) and \
+                            not any(w is None or w[0].try_wait(w[1] & 1)
+                                    for w in self.waits.values()):
+                        raise Stall(sorted(self.actors))
+                    continue
+                try:
+                    self.waits[a] = next(self.actors[a])
+                except StopIteration:
+                    del self.actors[a], self.waits[a]
+            idle = 0
+        raise Stall("no end")
+
+
+def chunk(seed, units, stages, hand_back=True, one_queue=False):
+    """units of one CTA: (query tiles, token tiles, set of token tiles whose V
+    the loading warp mends).  one_queue: the products of both threads run in
+    the order in which they were issued."""
+    m = Machine(seed)
+    NS = stages
+    full = [Bar(1) for _ in range(NS)]
+    empty = [Bar(1) for _ in range(NS)]
+    q_full, p_half, p_ready = ([Bar(WARPS), Bar(WARPS)] for _ in range(3))
+    s_full, o_full, turns = ([Bar(1), Bar(1)] for _ in range(3))
+    fix, loaded, released = Bar(1), Bar(1), Bar(2 * WARPS)
+    ring = [None] * NS
+    queries, s_at, o_at = [None, None], [None, None], [None, None]
+    p_at = [[None, None] for _ in range(2)]
+    out = {}
+
+    def expect(got, want):
+        if got != want:
+            raise Wrong(f"{got} where {want} is meant")
+
+    def load(half):
+        it, n_fix = half, 0
+        for n, (tiles, nk, mends) in enumerate(units):
+            for k in range(nk):
+                s = it % NS
+                if it >= NS:
+                    yield empty[s], it // NS - 1
+                mend = half == 1 and k in mends
+                bar, tag = fix if mend else full[s], (n, half, k)
+                ring[s] = None
+                bar.arrive(tx=1)
+
+                def land(s=s, bar=bar, tag=tag):
+                    ring[s] = tag
+                    bar.land(1)
+                m.flying.append(land)
+                yield None
+                if mend:
+                    yield fix, n_fix
+                    n_fix += 1
+                    expect(ring[s], tag)
+                    full[s].arrive()
+                it += 2
+            if half:
+                if n > 0:
+                    yield released, n - 1
+                loaded.arrive()
+
+    def products(i):
+        q = m.queues["T0" if one_queue else f"T{i}"]
+        it = n_q = n_p = n_t = steps = 0
+
+        def product_s(s, n, k):
+            def run():
+                expect(ring[s], (n, 0, k))
+                expect(queries[i], [n] * WARPS)
+                s_at[i], p_at[i] = (n, k), [None, None]
+            return run
+
+        def product_o(s, n, k, part):
+            def run():
+                expect(ring[s], (n, 1, k))
+                expect(p_at[i][part], [(n, k)] * WARPS)
+                o_at[i] = (n, k, part)
+            return run
+        for n, (tiles, nk, _) in enumerate(units):
+            if i >= tiles:
+                it += 2 * nk
+                continue
+            last, pair = i == tiles - 1, tiles == 2
+            for k in range(nk + 1 if nk else 0):
+                do_o, do_s = k > 0, k < nk
+                vs = it % NS
+                if do_o:
+                    yield full[vs], it // NS
+                    it += 1
+                ks = it % NS
+                if do_s:
+                    yield full[ks], it // NS
+                    it += 1
+                    if k == 0:
+                        yield q_full[i], n_q
+                        n_q += 1
+                if do_o:
+                    yield p_half[i], n_p
+                if pair and (i == 1 or (steps > 0 if hand_back else k > 0)):
+                    yield turns[i], n_t
+                    n_t += 1
+                if do_o:
+                    q.append(product_o(vs, n, k - 1, 0))
+                    yield p_ready[i], n_p
+                    n_p += 1
+                    q.append(product_o(vs, n, k - 1, 1))
+                    if not do_s:
+                        q.append(o_full[i].arrive)
+                    if last:
+                        q.append(empty[vs].arrive)
+                if do_s:
+                    q.append(product_s(ks, n, k))
+                    q.append(s_full[i].arrive)
+                    if last:
+                        q.append(empty[ks].arrive)
+                if pair:
+                    if hand_back or i == 0 or do_s:
+                        turns[1 - i].arrive()
+                    steps += 1
+                yield None
+
+    def softmax(i, w):
+        n_s = n_o = 0
+        for n, (tiles, nk, _) in enumerate(units):
+            if i < tiles and nk > 0:
+                if queries[i] is None:
+                    queries[i] = [None] * WARPS
+                queries[i][w] = n
+                q_full[i].arrive()
+                for k in range(nk):
+                    yield s_full[i], n_s
+                    n_s += 1
+                    expect(s_at[i], (n, k))
+                    yield None
+                    for part, bar in ((0, p_half[i]), (1, p_ready[i])):
+                        if p_at[i][part] is None:
+                            p_at[i][part] = [None] * WARPS
+                        p_at[i][part][w] = (n, k)
+                        bar.arrive()
+                        yield None
+                yield o_full[i], n_o
+                n_o += 1
+                expect(o_at[i], (n, nk - 1, 1))
+            yield loaded, n
+            if i < tiles:
+                out[n, i, w] = True
+            released.arrive()
+
+    for half in (0, 1):
+        m.add(f"load{half}", load(half))
+    for i in (0, 1):
+        m.queues[f"T{i}"] = []
+        m.add(f"products{i}", products(i))
+        for w in range(WARPS):
+            m.add(f"softmax{i}.{w}", softmax(i, w))
+    m.run()
+    assert len(out) == sum(t for t, _, _ in units) * WARPS
+
+
+def random_units(rnd, pairs_only=False):
+    units = []
+    for _ in range(rnd.randint(1, 5)):
+        nk = rnd.choice([0, 1, 1, 2, 3, 4, 7])
+        units.append((2 if pairs_only else rnd.choice([1, 2, 2]), nk,
+                      {k for k in range(nk) if rnd.random() < 0.3}))
+    return units
+
+
+def fails(what, trials, **kw):
+    """The trials' first failure of a kind, or None."""
+    for trial in range(trials):
+        rnd = random.Random(trial)
+        try:
+            chunk(trial, random_units(rnd, kw.get("pairs_only", False)), rnd.choice([5, 10]),
+                  **{k: v for k, v in kw.items() if k != "pairs_only"})
+        except what as e:
+            return trial, e
+    return None
+
+
+def test_turns_of_the_query_tiles_never_stall():
+    """Every unit ends, whichever tile is late (the rule: each step is handed
+    over, a unit's last one too, and waited for)."""
+    assert fails((Stall, Wrong), 1500, one_queue=True, pairs_only=True) is None
+
+
+def test_model_catches_a_last_step_that_is_not_handed_over():
+    """Without it tile 0 may hand over twice before tile 1 has looked: the
+    parity then reads as if it had not, and both wait for good."""
+    assert fails(Stall, 1500, one_queue=True, pairs_only=True, hand_back=False) is not None
