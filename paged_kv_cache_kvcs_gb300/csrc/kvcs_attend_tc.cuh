@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
-      ptx::mbar_init(empty + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(q_full + 8 * i, 4);
@@ -431,6 +431,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Every step is handed over and waited for, a unit's last one too (but for
     // tile 0's very first): a barrier shows its phase's parity alone, so that
     // a second turn given before the first is taken would read as none.
+    // A commit speaks for its own thread's products, so a stage is free when
+    // both warps have let it go.  In a unit of one query tile the other warp
+    // does so too, behind its own products: the stages then become free in
+    // their order, on which the loading warps rely (each waits for every other
+    // use of a stage).
     constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
     constexpr u32 kDescO = tc::instr_desc(kBf16, 128, kDim, true);
     const int i = warp == 8 ? 0 : 1;
@@ -447,11 +452,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const TcUnit x = finder.find(p, u);
-      if (i >= x.tiles) {   // the ring goes on without this warp
-        for (int n = 0; n < 2 * (x.k1 - x.k0); ++n) next_stage();
+      if (i >= x.tiles) {   // the ring goes on: each stage is let go once it has come
+        for (int n = 0; n < 2 * (x.k1 - x.k0); ++n) {
+          ok = tc::wait(full + 8 * stage, turn, limit);
+          if (!ok) break;
+          if (tc::elect()) tc::commit(empty + 8 * stage);
+          __syncwarp();
+          next_stage();
+        }
         continue;
       }
-      const bool last = i == x.tiles - 1, pair = x.tiles == 2;
+      const bool pair = x.tiles == 2;
       // ring: K0 V0 K1 V1 ...; V of tile k - 1 comes before K of tile k.
       for (int k = x.k0; k < x.k1 + (x.k1 > x.k0 ? 1 : 0) && ok; ++k) {
         const bool do_o = k > x.k0, do_s = k < x.k1;
@@ -491,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tc::mma_ts(to, ts + s * 8, tc::desc<S::kHalves * 1024>(v + s * (S::kHalves * 2048 >> 4)),
                          kDescO, true);
             if (!do_s) tc::commit(o_full + 8 * i);
-            if (last) tc::commit(empty + 8 * v_stage);
+            tc::commit(empty + 8 * v_stage);
           }
           __syncwarp();
         }
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          tc::desc<S::kHalves * 1024>(kk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4)),
                          kDescS, s > 0);
             tc::commit(s_full + 8 * i);
-            if (last) tc::commit(empty + 8 * k_stage);
+            tc::commit(empty + 8 * k_stage);
           }
           if (pair) ptx::mbar_arrive(turns + 8 * (1 - i));
         }

@@ -78,14 +78,17 @@ class Machine:
         raise Stall("no end")
 
 
-def chunk(seed, units, stages, hand_back=True, one_queue=False):
+def chunk(seed, units, stages, hand_back=True, one_queue=False, both_release=True,
+          step_along=True, in_order=True):
     """units of one CTA: (query tiles, token tiles, set of token tiles whose V
     the loading warp mends).  one_queue: the products of both threads run in
-    the order in which they were issued."""
+    the order in which they were issued.  both_release: a stage is free once
+    both product warps have let it go, the second one in units of one query
+    tile too, after the stage's copy (step_along) or ahead of it."""
     m = Machine(seed)
     NS = stages
     full = [Bar(1) for _ in range(NS)]
-    empty = [Bar(1) for _ in range(NS)]
+    empty = [Bar(2 if both_release else 1) for _ in range(NS)]
     q_full, p_half, p_ready = ([Bar(WARPS), Bar(WARPS)] for _ in range(3))
     s_full, o_full, turns = ([Bar(1), Bar(1)] for _ in range(3))
     fix, loaded, released = Bar(1), Bar(1), Bar(2 * WARPS)
@@ -145,9 +148,17 @@ def chunk(seed, units, stages, hand_back=True, one_queue=False):
             return run
         for n, (tiles, nk, _) in enumerate(units):
             if i >= tiles:
-                it += 2 * nk
+                for it in range(it, it + 2 * nk):
+                    if both_release:
+                        if step_along:
+                            yield full[it % NS], it // NS
+                        if in_order:
+                            q.append(empty[it % NS].arrive)
+                        else:
+                            empty[it % NS].arrive()
+                it += 1 if nk else 0
                 continue
-            last, pair = i == tiles - 1, tiles == 2
+            lets_go, pair = both_release or i == tiles - 1, tiles == 2
             for k in range(nk + 1 if nk else 0):
                 do_o, do_s = k > 0, k < nk
                 vs = it % NS
@@ -173,12 +184,12 @@ def chunk(seed, units, stages, hand_back=True, one_queue=False):
                     q.append(product_o(vs, n, k - 1, 1))
                     if not do_s:
                         q.append(o_full[i].arrive)
-                    if last:
+                    if lets_go:
                         q.append(empty[vs].arrive)
                 if do_s:
                     q.append(product_s(ks, n, k))
                     q.append(s_full[i].arrive)
-                    if last:
+                    if lets_go:
                         q.append(empty[ks].arrive)
                 if pair:
                     if hand_back or i == 0 or do_s:
@@ -255,3 +266,28 @@ def test_model_catches_a_last_step_that_is_not_handed_over():
     """Without it tile 0 may hand over twice before tile 1 has looked: the
     parity then reads as if it had not, and both wait for good."""
     assert fails(Stall, 1500, one_queue=True, pairs_only=True, hand_back=False) is not None
+
+
+def test_stages_are_free_when_both_tiles_products_have_read_them():
+    """Products of the two threads run in any order among each other, and
+    units of one and two query tiles follow one another."""
+    assert fails((Stall, Wrong), 3000) is None
+
+
+def test_model_catches_a_release_by_the_last_tile_alone():
+    """A commit speaks for its own thread's products: tile 0's may still read
+    the stage.  And where a unit of one tile follows one of two, tile 0 may
+    let its stages go before tile 1 has let go of the unit before, so that a
+    loading warp takes one release for another."""
+    assert fails(Wrong, 1500, both_release=False, pairs_only=True) is not None
+    assert fails((Stall, Wrong), 1500, both_release=False, one_queue=True) is not None
+
+
+def test_model_catches_releases_out_of_order():
+    """The warp without rows lets go of a stage once its copy is there, and
+    behind its own products: ahead of the copy the release would count for the
+    stage's use before, and ahead of the products a later stage would be free
+    before an earlier one, where a loading warp looks at every other use of a
+    stage only."""
+    assert fails((Stall, Wrong), 3000, step_along=False) is not None
+    assert fails((Stall, Wrong), 3000, in_order=False) is not None
