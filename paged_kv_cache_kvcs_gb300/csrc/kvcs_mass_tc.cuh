@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(k_full + 8 * i, 1);
-      ptx::mbar_init(k_empty + 8 * i, 1);
+      ptx::mbar_init(k_empty + 8 * i, 2);
       ptx::mbar_init(s_full + 8 * i, 1);
       ptx::mbar_init(s_empty + 8 * i, 8);
     }
@@ -318,8 +318,15 @@ __global__ void __launch_bounds__(kMtThreads, 1)
       if (x.steps == 0) continue;
       const bool work = i < x.tiles;
       const u32 k_slot = (n_k + i) & 3;
-      if (work) ok = tc::wait(k_full + 8 * k_slot, ((n_k + i) / 4) & 1, limit);
-      n_k += x.tiles;
+      // A warp waits for both K tiles and lets the one go that it does not read:
+      // a barrier shows its phase's parity alone, so that a warp that skipped
+      // some would take the parity of a slot's use before for its own.
+      for (u32 j = 0; j < static_cast<u32>(x.tiles) && ok; ++j, ++n_k) {
+        ok = tc::wait(k_full + 8 * (n_k & 3), (n_k / 4) & 1, limit);
+        if (!ok) break;
+        if (j != static_cast<u32>(i) && tc::elect()) tc::commit(k_empty + 8 * (n_k & 3));
+        __syncwarp();
+      }
       const u32 kk = k_low + k_slot * (S::kTileBytes >> 4);
       for (int t = 0; t < x.steps && ok; ++t, ++n_l) {
         ok = tc::wait(q_full + 8 * slot, turn, limit);

@@ -291,3 +291,163 @@ def test_model_catches_releases_out_of_order():
     stage only."""
     assert fails((Stall, Wrong), 3000, step_along=False) is not None
     assert fails((Stall, Wrong), 3000, in_order=False) is not None
+
+
+# ---------------------------------------------------------------------------
+# Attention mass of many rows
+# ---------------------------------------------------------------------------
+
+def mass(seed, units, watch_all=True):
+    """The mass kernel: a warp loads a unit's K tiles (four slots) and the
+    query tiles that pass by (three), a warp reads the log-sum-exps of their
+    rows (three), a product warp per K tile writes S to two buffers in turn,
+    and the sums of a tile are made in two halves.  units: (K tiles, query
+    tiles).  watch_all: a product warp waits for both K tiles of a unit, and
+    lets the one that it does not read go at once."""
+    m = Machine(seed)
+    k_full, k_empty = ([Bar(1) for _ in range(4)], [Bar(2 if watch_all else 1) for _ in range(4)])
+    q_full, q_empty = [Bar(1) for _ in range(3)], [Bar(2) for _ in range(3)]
+    l_full, l_empty = [Bar(1) for _ in range(3)], [Bar(4) for _ in range(3)]
+    s_full = [[Bar(1), Bar(1)] for _ in range(2)]
+    s_empty = [[Bar(2), Bar(2)] for _ in range(2)]
+    half_done, half_free = [Bar(1), Bar(1)], [Bar(1), Bar(1)]
+    keys, queries, lses = [None] * 4, [None] * 3, [None] * 3
+    s_at, half_at, out = [[None, None], [None, None]], [None, None], {}
+
+    def expect(got, want):
+        if got != want:
+            raise Wrong(f"{got} where {want} is meant")
+
+    def copy(room, slot, tag, bar):
+        def land():
+            room[slot] = tag
+            bar.land(1)
+        room[slot] = None
+        bar.arrive(tx=1)
+        m.flying.append(land)
+
+    def loads():
+        n_k = n_q = 0
+        for n, (tiles, steps) in enumerate(units):
+            if steps == 0:
+                continue
+            for i in range(tiles):
+                if n_k >= 4:
+                    yield k_empty[n_k % 4], n_k // 4 - 1
+                copy(keys, n_k % 4, (n, i), k_full[n_k % 4])
+                n_k += 1
+                yield None
+            for t in range(steps):
+                if n_q >= 3:
+                    yield q_empty[n_q % 3], n_q // 3 - 1
+                copy(queries, n_q % 3, (n, t), q_full[n_q % 3])
+                n_q += 1
+                yield None
+
+    def rows():
+        n_l = 0
+        for n, (_, steps) in enumerate(units):
+            for t in range(steps):
+                if n_l >= 3:
+                    yield l_empty[n_l % 3], n_l // 3 - 1
+                lses[n_l % 3] = (n, t)
+                l_full[n_l % 3].arrive()
+                n_l += 1
+                yield None
+
+    def products(i):
+        q = m.queues[f"T{i}"]
+        n_k = n_s = n_l = 0
+
+        def product(k_slot, q_slot, buf, n, t):
+            def run():
+                expect(keys[k_slot], (n, i))
+                expect(queries[q_slot], (n, t))
+                s_at[i][buf] = (n, t)
+            return run
+        for n, (tiles, steps) in enumerate(units):
+            if steps == 0:
+                continue
+            work = i < tiles
+            k_slot = (n_k + i) % 4
+            for j in range(tiles):
+                if watch_all or j == i:
+                    yield k_full[(n_k + j) % 4], (n_k + j) // 4
+                if watch_all and j != i:
+                    q.append(k_empty[(n_k + j) % 4].arrive)
+            n_k += tiles
+            for t in range(steps):
+                yield q_full[n_l % 3], n_l // 3
+                if work:
+                    if n_s >= 2:
+                        yield s_empty[i][n_s % 2], n_s // 2 - 1
+                    q.append(product(k_slot, n_l % 3, n_s % 2, n, t))
+                    q.append(s_full[i][n_s % 2].arrive)
+                    n_s += 1
+                q.append(q_empty[n_l % 3].arrive)
+                if work and t == steps - 1:
+                    q.append(k_empty[k_slot].arrive)
+                n_l += 1
+                yield None
+
+    def sums(i, half):
+        n_s = n_l = n_h = 0
+        for n, (tiles, steps) in enumerate(units):
+            work = i < tiles
+            for t in range(steps):
+                if work:
+                    yield s_full[i][n_s % 2], n_s // 2
+                yield l_full[n_l % 3], n_l // 3
+                expect(lses[n_l % 3], (n, t))
+                if work:
+                    expect(s_at[i][n_s % 2], (n, t))
+                    s_empty[i][n_s % 2].arrive()
+                    n_s += 1
+                yield None
+                l_empty[n_l % 3].arrive()
+                n_l += 1
+            if not work or steps == 0:
+                continue
+            if half:
+                if n_h > 0:
+                    yield half_free[i], n_h - 1
+                half_at[i] = n
+                half_done[i].arrive()
+            else:
+                yield half_done[i], n_h
+                expect(half_at[i], n)
+                half_free[i].arrive()
+                out[n, i] = True
+            n_h += 1
+
+    m.add("loads", loads())
+    m.add("rows", rows())
+    for i in (0, 1):
+        m.queues[f"T{i}"] = []
+        m.add(f"products{i}", products(i))
+        for half in (0, 1):
+            m.add(f"sums{i}.{half}", sums(i, half))
+    m.run()
+    assert len(out) == sum(t for t, s in units if s)
+
+
+def mass_fails(trials, **kw):
+    for trial in range(trials):
+        rnd = random.Random(trial)
+        units = [(rnd.choice([1, 1, 2]), rnd.choice([0, 1, 1, 1, 2, 3, 5]))
+                 for _ in range(rnd.randint(1, 14))]
+        try:
+            mass(trial, units, **kw)
+        except (Stall, Wrong) as e:
+            return trial, e
+    return None
+
+
+def test_mass_reads_the_keys_of_its_unit():
+    assert mass_fails(1500) is None
+
+
+def test_model_catches_a_mass_warp_that_skips_a_key_tile():
+    """A warp that does not wait for the K tiles it does not read falls behind
+    the slots' phases: the parity of a use before then passes for its own."""
+    assert mass_fails(3000, watch_all=False) is not None
