@@ -266,8 +266,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     }
    } else if (warp == 19) {
     // ------------------------------------------------------ log-sum-exps
-    // read two query tiles ahead.  (The products of a step wait for its values
-    // too, so that the sums need only wait for the products.)
+    // read two query tiles ahead.
     u32 n_l = 0;
     int tok_of[4], head_of[4];
 #pragma unroll
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     constexpr u32 kDescS = tc::instr_desc(kBf16, 128, 128, false);
     const int i = warp == 16 ? 0 : 1;
     const u32 k_low = tc::desc_low(k_smem, 16), q_low = tc::desc_low(q_smem, 16);
-    u32 n_k = 0, slot = 0, turn = 0, n_s = 0, n_l = 0;
+    u32 n_k = 0, slot = 0, turn = 0, n_s = 0;
     for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const MtUnit x = finder.find(p, u);
       if (x.steps == 0) continue;
@@ -328,9 +327,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         __syncwarp();
       }
       const u32 kk = k_low + k_slot * (S::kTileBytes >> 4);
-      for (int t = 0; t < x.steps && ok; ++t, ++n_l) {
+      for (int t = 0; t < x.steps && ok; ++t) {
         ok = tc::wait(q_full + 8 * slot, turn, limit);
-        if (work) ok = ok && tc::wait(lse_full + 8 * (n_l % kMtLseStages), (n_l / kMtLseStages) & 1, limit);
         if (work && n_s >= 2)
           ok = ok && tc::wait(s_empty + 16 * i + 8 * (n_s & 1), (n_s / 2 - 1) & 1, limit);
         if (!ok) break;
@@ -398,10 +396,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
       u64 acc[4] = {0, 0, 0, 0};   // pairs of +0
       for (int t = 0; t < x.steps; ++t, ++n_l) {
         const u32 slot = n_l % kMtLseStages, ls = ptx::smem_addr(sh.lse[slot]) + hf * 256;
-        if (work)
-          ok = tc::wait(s_full + 16 * i + 8 * (n_s & 1), (n_s / 2) & 1, limit);
-        else
-          ok = tc::wait(lse_full + 8 * slot, (n_l / kMtLseStages) & 1, limit);
+        // (the step's log-sum-exps come from another warp's plain writes: only
+        // this wait orders them, the products' commit does not)
+        ok = tc::wait(lse_full + 8 * slot, (n_l / kMtLseStages) & 1, limit);
+        if (work) ok = ok && tc::wait(s_full + 16 * i + 8 * (n_s & 1), (n_s / 2) & 1, limit);
         if (!ok) break;
         if (work) {
           tc::fence_after();
