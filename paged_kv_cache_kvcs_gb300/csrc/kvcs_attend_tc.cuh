@@ -158,7 +158,8 @@ struct TcShared {
   u64 full[10], empty[10];
   u64 q_full[2], s_full[2], p_half[2], p_ready[2], o_full[2];
   u64 turns[2];                    // the products' warps hand each other the turn
-  u64 fix, loaded, released, drain;
+  u64 fix, loaded, released;
+  u64 drain[2];                    // a product warp's last products
   u32 tmem;
   int n_dirty[2];                  // noted tiles, by parity of the unit
   int dirty_tile[2][kTcDirty];
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const u32 turns = ptx::smem_addr(sh.turns);
   const u32 o_full = ptx::smem_addr(sh.o_full);
   const u32 fix = ptx::smem_addr(&sh.fix), loaded = ptx::smem_addr(&sh.loaded);
-  const u32 released = ptx::smem_addr(&sh.released), drain = ptx::smem_addr(&sh.drain);
+  const u32 released = ptx::smem_addr(&sh.released), drain = ptx::smem_addr(sh.drain);
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
@@ -260,10 +261,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ptx::mbar_init(p_ready + 8 * i, 4);
       ptx::mbar_init(o_full + 8 * i, 1);
       ptx::mbar_init(turns + 8 * i, 1);
+      ptx::mbar_init(drain + 8 * i, 1);
     }
     ptx::mbar_init(fix, 1);
     ptx::mbar_init(loaded, 1);
-    ptx::mbar_init(drain, 2);
     ptx::mbar_init(released, 8);
     ptx::fence_barrier_init();
   }
@@ -414,10 +415,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) ptx::mbar_arrive(loaded);
       }
     }
-    // after a wait that ran out: nothing may still be on its way to this CTA
-    if (!ok)
-      for (u32 i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-        tc::wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, limit);
+    // Whichever role's wait ran out, nothing may still be on its way to this
+    // CTA: the copies that nobody has waited for lie in the ring's last turn.
+    // (Where all went well they have long come.)
+    const u32 turn0 = it > S::kStages ? it - S::kStages : 0;
+    for (u32 i = turn0 + ((turn0 + half) & 1); i < it; i += 2)
+      tc::wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1, limit);
    } else {
     // -------------------------------------------------------------- products
     // A warp per query tile.  They take turns, each with O of token tile
@@ -522,10 +525,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok) {   // let the products issued so far end
-      if (lane == 0) tc::commit(drain);
-      tc::wait(drain, 0, limit);
-    }
+    // the products issued so far end before tensor memory is given back, a
+    // wait of whichever role ran out (one lane issues and commits: a commit
+    // speaks for its own thread's products)
+    if (tc::elect()) tc::commit(drain + 8 * i);
+    __syncwarp();
+    if (!tc::wait(drain + 8 * i, 0, limit)) ok = false;
    }
   } else {
     // --------------------------------------------------------------- softmax

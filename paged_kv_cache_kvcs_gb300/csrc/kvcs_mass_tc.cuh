@@ -64,11 +64,11 @@ struct MtShared {
   u64 lse_full[kMtLseStages], lse_empty[kMtLseStages];
   u64 s_full[2][2], s_empty[2][2];   // by token tile and buffer
   u64 half_done[2], half_free[2];    // by token tile: the second half's sums
-  u64 drain;
+  u64 drain[2];                      // a product warp's last products
   u32 tmem;
   float half[2][128];
   long long sum[kMtThreads / 32];
-  float lse[kMtLseStages][128];      // in units of log 2
+  alignas(16) float lse[kMtLseStages][128];   // in units of log 2; read four at once
 };
 static_assert(sizeof(MtShared) <= kMtControl, "control block");
 
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
   const u32 lse_full = ptx::smem_addr(sh.lse_full), lse_empty = ptx::smem_addr(sh.lse_empty);
   const u32 s_full = ptx::smem_addr(sh.s_full), s_empty = ptx::smem_addr(sh.s_empty);
   const u32 half_done = ptx::smem_addr(sh.half_done), half_free = ptx::smem_addr(sh.half_free);
-  const u32 drain = ptx::smem_addr(&sh.drain);
+  const u32 drain = ptx::smem_addr(sh.drain);
   const u64 limit = p.timeout_ns;
   if (k_smem & 1023u) {   // the swizzled tiles lie on 1 KiB boundaries (they always do)
     if (tid == 0) raise(a.tab, kStatusTimeout);
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kMtThreads, 1)
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(half_done + 8 * i, 4);
       ptx::mbar_init(half_free + 8 * i, 4);
+      ptx::mbar_init(drain + 8 * i, 1);
     }
-    ptx::mbar_init(drain, 2);
     ptx::fence_barrier_init();
   }
   if (warp == 16) tc::tmem_alloc(ptx::smem_addr(&sh.tmem), 512);
@@ -259,11 +259,10 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok) {   // nothing may still be on its way to this CTA
-      for (u32 i = n_k > 4 ? n_k - 4 : 0; i < n_k; ++i) tc::wait(k_full + 8 * (i & 3), (i / 4) & 1, limit);
-      for (u32 i = n_q > kMtQStages ? n_q - kMtQStages : 0; i < n_q; ++i)
-        tc::wait(q_full + 8 * (i % kMtQStages), (i / kMtQStages) & 1, limit);
-    }
+    // nothing may still be on its way to this CTA, whichever role's wait ran out
+    for (u32 i = n_k > 4 ? n_k - 4 : 0; i < n_k; ++i) tc::wait(k_full + 8 * (i & 3), (i / 4) & 1, limit);
+    for (u32 i = n_q > kMtQStages ? n_q - kMtQStages : 0; i < n_q; ++i)
+      tc::wait(q_full + 8 * (i % kMtQStages), (i / kMtQStages) & 1, limit);
    } else if (warp == 19) {
     // ------------------------------------------------------ log-sum-exps
     // read two query tiles ahead.
@@ -355,10 +354,11 @@ __global__ void __launch_bounds__(kMtThreads, 1)
         }
       }
     }
-    if (!ok) {   // let the products issued so far end
-      if (tc::elect()) tc::commit(drain);
-      tc::wait(drain, 0, limit);
-    }
+    // the products issued so far end before tensor memory is given back, a
+    // wait of whichever role ran out
+    if (tc::elect()) tc::commit(drain + 8 * i);
+    __syncwarp();
+    if (!tc::wait(drain + 8 * i, 0, limit)) ok = false;
    }
   } else {
     // ------------------------------------------------------------------ sums

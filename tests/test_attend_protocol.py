@@ -31,17 +31,39 @@ class Stall(AssertionError):
     pass
 
 
+class GaveUp(Exception):
+    pass
+
+
 class Machine:
     """Actors are generators that yield (barrier, parity) to wait, or None
-    between two steps.  Tensor-core queues and copies in flight act too."""
+    between two steps.  Tensor-core queues and copies in flight act too.
+    gives_up: an actor and which of its waits runs out at once (not one for
+    its own copies or products, which do end); every other wait then runs out
+    where nothing moves any more."""
 
-    def __init__(self, seed):
+    def __init__(self, seed, gives_up=None):
         self.rnd = random.Random(seed)
         self.actors, self.waits = {}, {}
         self.flying, self.queues = [], {}
+        self.gives_up, self.waited, self.gave_up = gives_up, {}, 0
 
     def add(self, name, gen):
         self.actors[name], self.waits[name] = gen, None
+
+    def step(self, a, gone=False):
+        self.gave_up += gone
+        try:
+            w = self.actors[a].throw(GaveUp()) if gone else next(self.actors[a])
+            if w is not None and len(w) == 2 and self.gives_up and self.gives_up[0] == a:
+                self.waited[a] = self.waited.get(a, 0) + 1
+                if self.waited[a] == self.gives_up[1]:
+                    return self.step(a, gone=True)
+            self.waits[a] = w
+        except StopIteration:
+            del self.actors[a], self.waits[a]
+            if not self.actors and (self.flying or any(self.queues.values())):
+                raise Wrong("copies or products are left behind")
 
     def run(self, most=200000):
         rnd, idle = self.rnd, 0
@@ -68,18 +90,34 @@ class Machine:
                             not any(self.queues.values()) and \
                             not any(w is None or w[0].try_wait(w[1] & 1)
                                     for w in self.waits.values()):
-                        raise Stall(sorted(self.actors))
+                        if not self.gave_up:
+                            raise Stall(sorted(self.actors))
+                        self.step(a, gone=True)
                     continue
-                try:
-                    self.waits[a] = next(self.actors[a])
-                except StopIteration:
-                    del self.actors[a], self.waits[a]
+                self.step(a)
             idle = 0
         raise Stall("no end")
 
 
+def ending(body, end, always):
+    """A role: its body until that ends or a wait runs out, then its end
+    (whose waits may run out too), always or after a wait of its own."""
+    gone = not always
+    try:
+        yield from body
+    except GaveUp:
+        gone = False
+    if gone:
+        return
+    for w in end():
+        try:
+            yield (*w, "end")
+        except GaveUp:
+            pass
+
+
 def chunk(seed, units, stages, hand_back=True, one_queue=False, both_release=True,
-          step_along=True, in_order=True):
+          step_along=True, in_order=True, gives_up=None, ends=True):
     """units of one CTA: (query tiles, token tiles, set of token tiles whose V
     the loading warp mends).  one_queue: the products of both threads run in
     the order in which they were issued.  both_release: a stage is free once
@@ -95,6 +133,7 @@ def chunk(seed, units, stages, hand_back=True, one_queue=False, both_release=Tru
     ring = [None] * NS
     queries, s_at, o_at = [None, None], [None, None], [None, None]
     p_at = [[None, None] for _ in range(2)]
+    at, drain = [0, 1], [Bar(1), Bar(1)]
     out = {}
 
     def expect(got, want):
@@ -117,6 +156,7 @@ def chunk(seed, units, stages, hand_back=True, one_queue=False, both_release=Tru
                     ring[s] = tag
                     bar.land(1)
                 m.flying.append(land)
+                at[half] = it + 2
                 yield None
                 if mend:
                     yield fix, n_fix
@@ -124,6 +164,7 @@ def chunk(seed, units, stages, hand_back=True, one_queue=False, both_release=Tru
                     expect(ring[s], tag)
                     full[s].arrive()
                 it += 2
+                at[half] = it
             if half:
                 if n > 0:
                     yield released, n - 1
@@ -224,15 +265,23 @@ def chunk(seed, units, stages, hand_back=True, one_queue=False, both_release=Tru
                 out[n, i, w] = True
             released.arrive()
 
+    def landed(half):
+        first = max(0, at[half] - NS)
+        return [(full[it % NS], it // NS) for it in range(first, at[half]) if it % 2 == half]
+
+    def drained(i):
+        m.queues["T0" if one_queue else f"T{i}"].append(drain[i].arrive)
+        return [(drain[i], 0)]
+
     for half in (0, 1):
-        m.add(f"load{half}", load(half))
+        m.add(f"load{half}", ending(load(half), lambda half=half: landed(half), ends))
     for i in (0, 1):
         m.queues[f"T{i}"] = []
-        m.add(f"products{i}", products(i))
+        m.add(f"products{i}", ending(products(i), lambda i=i: drained(i), ends))
         for w in range(WARPS):
-            m.add(f"softmax{i}.{w}", softmax(i, w))
+            m.add(f"softmax{i}.{w}", ending(softmax(i, w), list, ends))
     m.run()
-    assert len(out) == sum(t for t, _, _ in units) * WARPS
+    assert gives_up or len(out) == sum(t for t, _, _ in units) * WARPS
 
 
 def random_units(rnd, pairs_only=False):
@@ -293,18 +342,40 @@ def test_model_catches_releases_out_of_order():
     assert fails((Stall, Wrong), 3000, in_order=False) is not None
 
 
+def leavings(trials, **kw):
+    for trial in range(trials):
+        rnd = random.Random(trial)
+        units, stages = random_units(rnd), rnd.choice([5, 10])
+        name = rnd.choice(["load0", "load1", "products0", "products1", "softmax0.0", "softmax1.1"])
+        try:
+            chunk(trial, units, stages, gives_up=(name, rnd.randint(1, 12)), **kw)
+        except (Stall, Wrong) as e:
+            return trial, e
+    return None
+
+
+def test_nothing_is_left_behind_when_a_wait_runs_out():
+    """Copies and products that were issued end before the CTA does, whichever
+    role's wait ran out."""
+    assert leavings(1500) is None
+
+
+def test_model_catches_roles_that_leave_their_work_behind():
+    assert leavings(1500, ends=False) is not None
+
+
 # ---------------------------------------------------------------------------
 # Attention mass of many rows
 # ---------------------------------------------------------------------------
 
-def mass(seed, units, watch_all=True):
+def mass(seed, units, watch_all=True, gives_up=None, ends=True):
     """The mass kernel: a warp loads a unit's K tiles (four slots) and the
     query tiles that pass by (three), a warp reads the log-sum-exps of their
     rows (three), a product warp per K tile writes S to two buffers in turn,
     and the sums of a tile are made in two halves.  units: (K tiles, query
     tiles).  watch_all: a product warp waits for both K tiles of a unit, and
-    lets the one that it does not read go at once."""
-    m = Machine(seed)
+    lets the one that it does not read go at once.  ends: as in chunk."""
+    m = Machine(seed, gives_up)
     k_full, k_empty = ([Bar(1) for _ in range(4)], [Bar(2 if watch_all else 1) for _ in range(4)])
     q_full, q_empty = [Bar(1) for _ in range(3)], [Bar(2) for _ in range(3)]
     l_full, l_empty = [Bar(1) for _ in range(3)], [Bar(4) for _ in range(3)]
@@ -313,6 +384,7 @@ def mass(seed, units, watch_all=True):
     half_done, half_free = [Bar(1), Bar(1)], [Bar(1), Bar(1)]
     keys, queries, lses = [None] * 4, [None] * 3, [None] * 3
     s_at, half_at, out = [[None, None], [None, None]], [None, None], {}
+    at, drain = [0, 0], [Bar(1), Bar(1)]
 
     def expect(got, want):
         if got != want:
@@ -336,12 +408,14 @@ def mass(seed, units, watch_all=True):
                     yield k_empty[n_k % 4], n_k // 4 - 1
                 copy(keys, n_k % 4, (n, i), k_full[n_k % 4])
                 n_k += 1
+                at[0] = n_k
                 yield None
             for t in range(steps):
                 if n_q >= 3:
                     yield q_empty[n_q % 3], n_q // 3 - 1
                 copy(queries, n_q % 3, (n, t), q_full[n_q % 3])
                 n_q += 1
+                at[1] = n_q
                 yield None
 
     def rows():
@@ -420,24 +494,33 @@ def mass(seed, units, watch_all=True):
                 out[n, i] = True
             n_h += 1
 
-    m.add("loads", loads())
-    m.add("rows", rows())
+    def landed():
+        return [(k_full[n % 4], n // 4) for n in range(max(0, at[0] - 4), at[0])] + \
+               [(q_full[n % 3], n // 3) for n in range(max(0, at[1] - 3), at[1])]
+
+    def drained(i):
+        m.queues[f"T{i}"].append(drain[i].arrive)
+        return [(drain[i], 0)]
+
+    m.add("loads", ending(loads(), landed, ends))
+    m.add("rows", ending(rows(), list, ends))
     for i in (0, 1):
         m.queues[f"T{i}"] = []
-        m.add(f"products{i}", products(i))
+        m.add(f"products{i}", ending(products(i), lambda i=i: drained(i), ends))
         for half in (0, 1):
-            m.add(f"sums{i}.{half}", sums(i, half))
+            m.add(f"sums{i}.{half}", ending(sums(i, half), list, ends))
     m.run()
-    assert len(out) == sum(t for t, s in units if s)
+    assert gives_up or len(out) == sum(t for t, s in units if s)
 
 
-def mass_fails(trials, **kw):
+def mass_fails(trials, gives_up=False, **kw):
     for trial in range(trials):
         rnd = random.Random(trial)
         units = [(rnd.choice([1, 1, 2]), rnd.choice([0, 1, 1, 1, 2, 3, 5]))
                  for _ in range(rnd.randint(1, 14))]
+        who = rnd.choice(["loads", "rows", "products0", "products1", "sums0.0", "sums1.1"])
         try:
-            mass(trial, units, **kw)
+            mass(trial, units, gives_up=(who, rnd.randint(1, 20)) if gives_up else None, **kw)
         except (Stall, Wrong) as e:
             return trial, e
     return None
@@ -451,3 +534,8 @@ def test_model_catches_a_mass_warp_that_skips_a_key_tile():
     """A warp that does not wait for the K tiles it does not read falls behind
     the slots' phases: the parity of a use before then passes for its own."""
     assert mass_fails(3000, watch_all=False) is not None
+
+
+def test_mass_leaves_nothing_behind_when_a_wait_runs_out():
+    assert mass_fails(1500, gives_up=True) is None
+    assert mass_fails(1500, gives_up=True, ends=False) is not None
