@@ -60,6 +60,13 @@ __device__ __forceinline__ u64 globaltimer_ns() {
   return t;
 }
 
+// Its low word: wraps after 4.29 s.
+__device__ __forceinline__ u32 globaltimer_low() {
+  u32 t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
 // Bounded wait for phase `parity` of barrier `bar`: gives up (returns false)
 // after `limit_ns` of wall time or 2^26 probes, whichever comes first, so a
 // lost arrival can never hang the GPU.

@@ -99,21 +99,24 @@ __device__ __forceinline__ void mma_ts(u32 d, u32 a, u64 b, u32 idesc, bool add)
 // about a microsecond) before 1024 probes have failed: the waits of a
 // product pipeline are shorter than that, and on its critical path.
 // The first probe stands apart: one that succeeds costs about 15 cycles, the
-// loop's bookkeeping about 100 more.  A warp calls it converged: its lanes
-// probe with one instruction and read one clock, and so get one answer (a
-// vote on it cost 3 to 9% of a product pipeline's time).
+// loop's bookkeeping about 100 more.  A warp calls it converged and leaves it
+// with one answer, so that none of its lanes goes on alone: only the second
+// loop gives up, where what one lane sees or decides goes for all, and a phase
+// that a lane has seen before is there at the others' next probe.  (Votes on
+// every wait cost 3 to 9% of a product pipeline's time, in the first loop 5%.)
 __device__ __forceinline__ bool wait(u32 bar, u32 parity, u64 limit_ns) {
   if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
-  u64 t0 = 0;
-  for (u32 i = 0; i < (1u << 28); ++i) {
+#pragma unroll 1
+  for (u32 i = 0; i < 1024; ++i)
     if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023u) == 1023u) {
-      const u64 now = ptx::globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > limit_ns) return false;
+  const u32 late = __activemask(), t0 = ptx::globaltimer_low();
+  for (;;) {
+    if (__any_sync(late, ptx::mbar_try_wait(bar, parity))) {
+      __syncwarp(late);   // (orders what follows for the lanes that did not see it themselves)
+      return true;
     }
+    if (__any_sync(late, ptx::globaltimer_low() - t0 > static_cast<u32>(limit_ns))) return false;
   }
-  return false;
 }
 // 32 columns of this warp's 32 lanes.
 __device__ __forceinline__ void ld32(u32 addr, u32 *v) {

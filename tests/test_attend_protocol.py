@@ -539,3 +539,37 @@ def test_model_catches_a_mass_warp_that_skips_a_key_tile():
 def test_mass_leaves_nothing_behind_when_a_wait_runs_out():
     assert mass_fails(1500, gives_up=True) is None
     assert mass_fails(1500, gives_up=True, ends=False) is not None
+
+
+# ---------------------------------------------------------------------------
+# One wait of a warp whose limit runs out while the phase completes
+# ---------------------------------------------------------------------------
+
+def answers(seed, votes):
+    """What each of a warp's lanes gets from one wait.  A lane's probe sees the
+    phase if it has completed by then; lanes probe at moments of their own."""
+    rnd = random.Random(seed)
+    done_at, limit = rnd.uniform(0, 30), 20.0
+    first = [rnd.uniform(0, 1) for _ in range(32)]
+    got = [True if t >= done_at else None for t in first]
+    late = [n for n in range(32) if got[n] is None]
+    t = 1.0
+    while any(got[n] is None for n in late):
+        seen = {n: t + rnd.uniform(0, 1) >= done_at for n in late if got[n] is None}
+        over = {n: t + rnd.uniform(0, 1) - first[n] > limit for n in seen}
+        if votes:
+            seen = dict.fromkeys(seen, any(seen.values()))
+            over = dict.fromkeys(over, any(over.values()))
+        for n in seen:
+            got[n] = True if seen[n] else False if over[n] else None
+        t += 1.0
+    return got
+
+
+def test_a_warp_leaves_a_wait_with_one_answer():
+    seen = [set(answers(seed, votes=True)) for seed in range(5000)]
+    assert all(len(s) == 1 for s in seen) and {True} in seen and {False} in seen
+
+
+def test_model_catches_lanes_that_decide_alone():
+    assert any(len(set(answers(seed, votes=False))) > 1 for seed in range(5000))
