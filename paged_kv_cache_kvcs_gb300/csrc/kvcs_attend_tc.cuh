@@ -187,46 +187,51 @@ __device__ __forceinline__ bool bad_blocks(const AttnParams &a, const TcUnit &x)
 __device__ __forceinline__ float lo_of(u32 w, bool bf16) { return half_bits_to_float(w & 0xffffu, bf16); }
 __device__ __forceinline__ float hi_of(u32 w, bool bf16) { return half_bits_to_float(w >> 16, bf16); }
 
-// Raw products as scores in units of log 2, in place, by a whole warp.
+// A thread's raw products as scores in units of log 2, in place.  whole: its
+// row sees all of them (its token is seen by all of their rows).
 //
 // Capped ones: tanh from its exponential is two operations of the exponential
-// unit a score and six others.  Where no product of the warp passes the cap,
-// |x| <= 1, tanh(x) = x P(x^2) instead, P the Chebyshev interpolation of degree
-// 6 of tanh(x) / x in x^2 (computed in 64 bits; off by less than 2^-23 with its
-// roundings): ten operations on pairs.  4 requests of 2048 new tokens over 8192
-// (32 query heads to 8 KV heads of 128, bf16), capped: 1424 us with the
-// exponential, 1316 so, 664 uncapped; their mass 1049, 908 and 428; 13 requests
-// of up to 777 over 33 to 5001 (16 to 2 of 64, window of 1024) 94, 86 and 56.
-// A fourth of the scores by the exponential beside it: 1653, 1064 and 103.
+// unit a score and six others.  The polynomial is ten operations on pairs; it
+// is taken in whole tiles until one of the thread's products has passed the
+// cap (`past`).  So the form hangs on places, and on what is seen by the
+// thread's row, alone: the two differ in the last bits, and nothing else may
+// show in a row.  (A vote of the warp over all products let the slots behind
+// the last token and the tiles' leftovers choose.)
+// 4 requests of 2048 new tokens over 8192 (32 query heads to 8 KV heads of 128,
+// bf16): 628 us without a cap, 1260 with one of 30 (none passes it), 1510 with
+// one of 2 (one in twenty does); their mass 420, 991 and 1092.  By the vote
+// 1242, 1500; 990, 1094.  Both forms for each score where any passes: 4518.
+// Zeros put in the place of what is not seen, so that partly seen tiles can
+// choose too: 1315 and 1568, and 138 instead of 115 for the mass of a windowed
+// chunk.
 template <int kN>
-__device__ __forceinline__ void make_scores(const AttnParams &a, u32 (&s)[kN]) {
-  float big = 0.0f;
-  if (a.cap != 0.0f) {
+__device__ __forceinline__ void make_scores(const AttnParams &a, u32 (&s)[kN], bool whole, bool &past) {
+  if (a.cap != 0.0f && whole) {
+    float big = 0.0f;
 #pragma unroll
     for (int c = 0; c < kN; c += 2)
       big = tc::max3(big, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-    big *= fabsf(a.inv_cap);
+    past |= big * fabsf(a.inv_cap) > 1.0f;
   }
-  if (a.cap == 0.0f || !__all_sync(0xffffffffu, big <= 1.0f)) {
+  if (a.cap == 0.0f || !whole || past) {
 #pragma unroll
     for (int c = 0; c < kN; ++c) s[c] = __float_as_uint(score_of(a, __uint_as_float(s[c]), 1.0f));
-    return;
-  }
-  constexpr float kP[7] = {9.999999404e-01f,  -3.333282769e-01f, 1.332507581e-01f, -5.345164612e-02f,
-                           2.027970739e-02f, -6.194324698e-03f, 1.038025133e-03f};
-  const u64 inv2 = tc::pair(a.inv_cap, a.inv_cap), cap2 = tc::pair(a.cap, a.cap);
+  } else {
+    const u64 inv2 = tc::pair(a.inv_cap, a.inv_cap), cap2 = tc::pair(a.cap, a.cap);
 #pragma unroll
-  for (int c = 0; c < kN; c += 2) {
-    const u64 x = tc::mul2(tc::pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), inv2);
-    const u64 u = tc::mul2(x, x);
-    u64 y = tc::pair(kP[6], kP[6]);
+    for (int c = 0; c < kN; c += 2) {
+      const u64 x = tc::mul2(tc::pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), inv2);
+      const u64 u = tc::mul2(x, x);
+      u64 y = tc::pair(tanh_p(6), tanh_p(6));
 #pragma unroll
-    for (int k = 5; k >= 0; --k) y = tc::fma2(y, u, tc::pair(kP[k], kP[k]));
-    float y0, y1;
-    tc::unpair(tc::mul2(tc::mul2(x, cap2), y), y0, y1);
-    s[c] = __float_as_uint(y0);
-    s[c + 1] = __float_as_uint(y1);
+      for (int k = 5; k >= 0; --k) y = tc::fma2(y, u, tc::pair(tanh_p(k), tanh_p(k)));
+      float y0, y1;
+      tc::unpair(tc::mul2(tc::mul2(x, cap2), y), y0, y1);
+      s[c] = __float_as_uint(y0);
+      s[c + 1] = __float_as_uint(y1);
+    }
   }
+  __syncwarp();
 }
 
 template <bool kBf16, int kDim, bool kPlain>
@@ -551,6 +556,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int tok_i = a.by_group(row_c), hq = x.head * a.group + row_c - tok_i * a.group;
       const int at = x.q.at + tok_i;
       float m = kNegInf, l = 0.0f;
+      bool past = false;   // a capped score of the row has passed the cap
       const int nk = x.k1 - x.k0;
       const unsigned char *q_row =
           static_cast<const unsigned char *>(a.q) +
@@ -593,14 +599,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc::wait_ld();
           // scores = sc * s; capped ones, and those of a scale that would turn
           // the maximum round or make 0 of a masked score, are made first
+          const bool part = key0 + kTcKeys - 1 > min(at_min, x.q.keys - 1) ||
+                            (a.window > 0 && key0 <= at_max - a.window) || bad;
           float sc = a.scale;
           if constexpr (!kPlain) {
             sc = 1.0f;
-            make_scores(a, s);
+            make_scores(a, s, !part, past);
           }
-          if (__builtin_expect(key0 + kTcKeys - 1 > min(at_min, x.q.keys - 1) ||
-                                   (a.window > 0 && key0 <= at_max - a.window) || bad,
-                               0)) {
+          if (__builtin_expect(part, 0)) {
             const int hi = upto - key0, lo = a.window > 0 ? at - a.window + 1 - key0 : 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {

@@ -202,6 +202,14 @@ __device__ __forceinline__ float tanh_of(float x) {
   return 1.0f - __fdividef(2.0f, ex2(x * (2.0f * kLog2e)) + 1.0f);
 }
 
+// tanh(x) = x P(x^2) for |x| <= 1, P the Chebyshev interpolation of degree 6
+// of tanh(x) / x in x^2 (computed in 64 bits), its coefficients from the lowest.
+__device__ __forceinline__ constexpr float tanh_p(int k) {
+  constexpr float kP[7] = {9.999999404e-01f,  -3.333282769e-01f, 1.332507581e-01f, -5.345164612e-02f,
+                           2.027970739e-02f, -6.194324698e-03f, 1.038025133e-03f};
+  return kP[k];
+}
+
 // A raw product as a score in units of log 2.
 __device__ __forceinline__ float score_of(const AttnParams &p, float raw, float row_scale) {
   if (p.cap != 0.0f) return p.cap * tanh_of(raw * row_scale * p.inv_cap);

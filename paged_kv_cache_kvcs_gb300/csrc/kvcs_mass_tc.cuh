@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
       const float sc = kPlain ? a.scale : 1.0f;
       const u64 sc2 = tc::pair(sc, sc);
       u64 acc[4] = {0, 0, 0, 0};   // pairs of +0
+      bool past = false;           // a capped score of the token has passed the cap
       for (int t = 0; t < x.steps; ++t, ++n_l) {
         const u32 slot = n_l % kMtLseStages, ls = ptx::smem_addr(sh.lse[slot]) + hf * 256;
         // (the step's log-sum-exps come from another warp's plain writes: only
@@ -412,9 +413,9 @@ __global__ void __launch_bounds__(kMtThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(s_empty + 16 * i + 8 * (n_s & 1));
           ++n_s;
-          if constexpr (!kPlain) make_scores(a, s);
           const int row0 = t * width + hf * 64;   // this half's first row
           const bool full = width == 128 && all_lo <= row0 && all_hi >= row0 + 64;
+          if constexpr (!kPlain) make_scores(a, s, full, past);
           // weights, 0 where the row does not see the token (whatever the
           // row's scores and its log-sum-exp are)
           auto add = [&](auto masked) {

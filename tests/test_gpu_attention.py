@@ -489,3 +489,62 @@ def test_nonfinite_values_in_split_chunks(kv, dim, window):
     A.close(lse, ref[1], ref[3])
     A.close(out, ref[0], ref[2])
     assert torch.isfinite(ref[0][:34]).all() and torch.isnan(ref[0][54:]).all()
+
+
+def bits(case, poison=None, **kw):
+    """Attention and mass of a case, after another call has left shared memory
+    full of `poison`'s numbers."""
+    m = max(case.new)
+    if poison is not None:
+        run(poison, max_new=max(poison.new))
+    out, lse, _ = run(case, max_new=m, **kw)
+    mass = torch.zeros((case.nb, case.heads, case.bs), device="cuda")
+    if poison is not None:
+        run(poison, max_new=max(poison.new))
+    K.attention_mass(case.cache, case.bs, *case.table, case.q, case.new_offsets, lse, mass,
+                     max_new=m, kv_dtype=case.kv, **kw)
+    torch.cuda.synchronize()
+    return out, lse, mass
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[1, 1], [40, 70]], ids=["one", "many"])
+def test_capped_scores_hang_on_nothing_unseen(kv, dim, new):
+    """What a row does not see never changes its bits: large finite values in
+    slots past the last token, in later tokens and before the window, other
+    requests' queries, and what another call has left in shared memory."""
+    kw = dict(kv=kv, dim=dim, lengths=[300, 190], new=new, seed=50, bs=16)
+    cap = dict(softcap=12.0, scale=dim ** -0.5, window=150)
+    plain = A.Case(tail=0.0, **kw)
+    out, lse, mass = bits(plain, **cap)
+    ref = A.attention(plain, **cap)
+    A.close(lse, ref[1], ref[3])
+    big = 448.0 if kv == "fp8" else 6e4
+    poison = A.Case(kv=kv, dim=dim, lengths=[2000] * 8, new=[64] * 8, seed=51,
+                    scale=100.0 if kv == "fp8" else 3000.0)
+    other = A.Case(tail=big, **kw)
+    for r, n in enumerate(new):
+        first = other.lengths[r] - n
+        for t in range(max(0, first - 160), max(0, first - 150)):      # before every window
+            other.put(r, 0, t, torch.full((1, dim), big))
+        if n > 1:                                                      # seen by the last row alone
+            other.put(r, 0, other.lengths[r] - 1, torch.full((1, dim), big))
+    got = bits(other, poison=poison, **cap)
+    same = torch.ones(plain.starts[-1], dtype=torch.bool)
+    for r, n in enumerate(new):
+        if n > 1:
+            same[plain.starts[r + 1] - 1] = False
+    assert torch.equal(out[same.cuda()], got[0][same.cuda()])
+    assert torch.equal(lse[same.cuda()], got[1][same.cuda()])
+    if max(new) == 1:
+        for h in range(plain.heads):
+            assert torch.equal(mass[:, h], got[2][:, h])
+    # the second request's queries do not change the first one's mass
+    other = A.Case(tail=big, **kw)
+    other.q[other.starts[1]:] *= 100.0
+    got = bits(other, poison=poison, **cap)
+    ids = plain.ids[:plain.offsets[1]].long()
+    assert torch.equal(mass[ids], got[2][ids])
+    n = plain.starts[1]
+    assert torch.equal(out[:n], got[0][:n]) and torch.equal(lse[:n], got[1][:n])
