@@ -189,10 +189,7 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
   // maximum round or make 0 of a masked score, are made first
   float sc[2] = {rs[0] * p.scale, rs[1] * p.scale};
   if (p.cap != 0.0f || p.scale <= 0.0f) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[j][i] = score_of(p, s[j][i], rs[i >> 1]);
+    scores_of(p, s, rs);
     sc[0] = sc[1] = 1.0f;
   }
   // s[j][2 r + i]: row g + 8 r, token j * 8 + t + 4 i

@@ -187,6 +187,15 @@ __device__ __forceinline__ bool bad_blocks(const AttnParams &a, const TcUnit &x)
 __device__ __forceinline__ float lo_of(u32 w, bool bf16) { return half_bits_to_float(w & 0xffffu, bf16); }
 __device__ __forceinline__ float hi_of(u32 w, bool bf16) { return half_bits_to_float(w >> 16, bf16); }
 
+// How a kernel makes scores of products: kPlain by a positive scale alone (on
+// the way to the weights), kCapped with a cap, or by any scale, and kFarCapped
+// with a cap past kNearCap.  (Both kinds of caps in one kernel: 1398 us, not
+// 1260, for the chunk below.)
+constexpr int kPlain = 0, kCapped = 1, kFarCapped = 2;
+inline int scores_kind(const AttnParams &a) {
+  return a.cap > kNearCap ? kFarCapped : a.cap != 0.0f || !(a.scale > 0.0f) ? kCapped : kPlain;
+}
+
 // A thread's raw products as scores in units of log 2, in place.  whole: its
 // row sees all of them (its token is seen by all of their rows).
 //
@@ -204,7 +213,7 @@ __device__ __forceinline__ float hi_of(u32 w, bool bf16) { return half_bits_to_f
 // Zeros put in the place of what is not seen, so that partly seen tiles can
 // choose too: 1315 and 1568, and 138 instead of 115 for the mass of a windowed
 // chunk.
-template <int kN>
+template <int kScores, int kN>
 __device__ __forceinline__ void make_scores(const AttnParams &a, u32 (&s)[kN], bool whole, bool &past) {
   if (a.cap != 0.0f && whole) {
     float big = 0.0f;
@@ -215,7 +224,13 @@ __device__ __forceinline__ void make_scores(const AttnParams &a, u32 (&s)[kN], b
   }
   if (a.cap == 0.0f || !whole || past) {
 #pragma unroll
-    for (int c = 0; c < kN; ++c) s[c] = __float_as_uint(score_of(a, __uint_as_float(s[c]), 1.0f));
+    for (int c = 0; c < kN; ++c) {
+      const float v = __uint_as_float(s[c]);
+      if constexpr (kScores == kFarCapped)
+        s[c] = __float_as_uint(capped(a.cap, v * a.inv_cap));
+      else
+        s[c] = __float_as_uint(a.cap != 0.0f ? near_capped(a.cap, v * a.inv_cap) : v * a.scale);
+    }
   } else {
     const u64 inv2 = tc::pair(a.inv_cap, a.inv_cap), cap2 = tc::pair(a.cap, a.cap);
 #pragma unroll
@@ -234,7 +249,7 @@ __device__ __forceinline__ void make_scores(const AttnParams &a, u32 (&s)[kN], b
   __syncwarp();
 }
 
-template <bool kBf16, int kDim, bool kPlain>
+template <bool kBf16, int kDim, int kScores>
 __global__ void __launch_bounds__(kTcThreads, 1)
     kvcs_attend_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v) {
@@ -602,9 +617,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool part = key0 + kTcKeys - 1 > min(at_min, x.q.keys - 1) ||
                             (a.window > 0 && key0 <= at_max - a.window) || bad;
           float sc = a.scale;
-          if constexpr (!kPlain) {
+          if constexpr (kScores != kPlain) {
             sc = 1.0f;
-            make_scores(a, s, !part, past);
+            make_scores<kScores>(a, s, !part, past);
           }
           if (__builtin_expect(part, 0)) {
             const int hi = upto - key0, lo = a.window > 0 ? at - a.window + 1 - key0 : 0;

@@ -56,13 +56,13 @@ struct TypeLaunch {
     return cudaLaunchKernelEx(&cfg, kvcs_attend_kernel<kType, kDim, kWide>, p);
   }
 
-  template <int kDim, bool kPlain>
+  template <int kDim, int kScores>
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
                                int grid, cudaStream_t st) {
     if constexpr (kType == kKvFp8) {
       return cudaErrorNotSupported;
     } else {
-      auto kernel = kvcs_attend_tc_kernel<kType == kKvBf16, kDim, kPlain>;
+      auto kernel = kvcs_attend_tc_kernel<kType == kKvBf16, kDim, kScores>;
       constexpr int smem = TcShape<kDim>::kSmemBytes;
       static std::atomic<u64> done{0};
       const cudaError_t e = allow_smem(kernel, smem, &done);
@@ -93,13 +93,13 @@ struct TypeLaunch {
     return cudaGetLastError();
   }
 
-  template <int kDim, bool kPlain>
+  template <int kDim, int kScores>
   static cudaError_t mass_tc(const MtParams &p, const CUtensorMap &k, const CUtensorMap &q, int grid,
                              cudaStream_t st) {
     if constexpr (kType == kKvFp8) {
       return cudaErrorNotSupported;
     } else {
-      auto kernel = kvcs_mass_tc_kernel<kType == kKvBf16, kDim, kPlain>;
+      auto kernel = kvcs_mass_tc_kernel<kType == kKvBf16, kDim, kScores>;
       constexpr int smem = MtShape<kDim>::kSmemBytes;
       static std::atomic<u64> done{0};
       const cudaError_t e = allow_smem(kernel, smem, &done);
@@ -139,19 +139,19 @@ cudaError_t AttendLaunch<kThisType>::attend(const AttnParams &p, bool wide, int 
 template <>
 cudaError_t AttendLaunch<kThisType>::attend_tc(const TcParams &p, const CUtensorMap &k,
                                                const CUtensorMap &v, int grid, cudaStream_t st) {
-  const bool plain = p.a.cap == 0.0f && p.a.scale > 0.0f;
-  auto run = p.a.head_dim == 64 ? (plain ? &This::attend_tc<64, true> : &This::attend_tc<64, false>)
-                                : (plain ? &This::attend_tc<128, true> : &This::attend_tc<128, false>);
-  return run(p, k, v, grid, st);
+  static constexpr decltype(&This::attend_tc<64, kPlain>) run[2][3] = {
+      {&This::attend_tc<64, kPlain>, &This::attend_tc<64, kCapped>, &This::attend_tc<64, kFarCapped>},
+      {&This::attend_tc<128, kPlain>, &This::attend_tc<128, kCapped>, &This::attend_tc<128, kFarCapped>}};
+  return run[p.a.head_dim == 128][scores_kind(p.a)](p, k, v, grid, st);
 }
 
 template <>
 cudaError_t AttendLaunch<kThisType>::mass_tc(const MtParams &p, const CUtensorMap &k,
                                              const CUtensorMap &q, int grid, cudaStream_t st) {
-  const bool plain = p.a.cap == 0.0f && p.a.scale > 0.0f;
-  auto run = p.a.head_dim == 64 ? (plain ? &This::mass_tc<64, true> : &This::mass_tc<64, false>)
-                                : (plain ? &This::mass_tc<128, true> : &This::mass_tc<128, false>);
-  return run(p, k, q, grid, st);
+  static constexpr decltype(&This::mass_tc<64, kPlain>) run[2][3] = {
+      {&This::mass_tc<64, kPlain>, &This::mass_tc<64, kCapped>, &This::mass_tc<64, kFarCapped>},
+      {&This::mass_tc<128, kPlain>, &This::mass_tc<128, kCapped>, &This::mass_tc<128, kFarCapped>}};
+  return run[p.a.head_dim == 128][scores_kind(p.a)](p, k, q, grid, st);
 }
 
 template <>

@@ -195,25 +195,69 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh from its definition, 1 - 2 / (e^2x + 1): the absolute error stays near
-// 2^-23, which a cap of tens turns into a few 1e-6 of a score (the hardware's
-// tanh approximation would be off by 2^-11 of the cap).
-__device__ __forceinline__ float tanh_of(float x) {
-  return 1.0f - __fdividef(2.0f, ex2(x * (2.0f * kLog2e)) + 1.0f);
-}
-
-// tanh(x) = x P(x^2) for |x| <= 1, P the Chebyshev interpolation of degree 6
-// of tanh(x) / x in x^2 (computed in 64 bits), its coefficients from the lowest.
+// Coefficients, from the lowest, of P with tanh(x) = x P(x^2) for |x| <= 1: the
+// Chebyshev interpolation of degree 6 of tanh(x) / x in x^2, computed in 64 bits.
 __device__ __forceinline__ constexpr float tanh_p(int k) {
   constexpr float kP[7] = {9.999999404e-01f,  -3.333282769e-01f, 1.332507581e-01f, -5.345164612e-02f,
                            2.027970739e-02f, -6.194324698e-03f, 1.038025133e-03f};
   return kP[k];
 }
 
+// Caps, in units of log 2, up to which the error of tanh's definition below,
+// about 2^-22 of the cap, stays under 2^-15 of a score's unit (a cap of 128),
+// far below the weights' rounding. (Scores past it through `capped` too: 4
+// requests of 2048 new tokens over 8192, a cap of 2, 2107 us, not 1510; their
+// mass 1725, not 1092; decode over fp8, a cap of 30, 95, not 92.)
+constexpr float kNearCap = 128.0f * kLog2e;
+
+// cap * tanh(x) by the definition, 1 - 2 / (e^2x + 1).  (The hardware's tanh is
+// off by 2^-11 of the cap.)
+__device__ __forceinline__ float near_capped(float cap, float x) {
+  return cap * (1.0f - __fdividef(2.0f, ex2(x * (2.0f * kLog2e)) + 1.0f));
+}
+
+// cap * tanh(x) for any cap, within 2^-21 of itself: below |x| = 1/2, where the
+// definition's error would be many times the score (a cap of 10^6 over scores
+// of 10: a quarter of a unit), x P(x^2), P the Chebyshev interpolation of
+// degree 4 of tanh(x) / x.  Both are made and one is taken: a branch for each
+// score costs more.
+__device__ __forceinline__ float capped(float cap, float x) {
+  const float u = x * x;
+  float y = 0.017131345346570015f;
+  y = fmaf(y, u, -0.05298423767089844f);
+  y = fmaf(y, u, 0.133247509598732f);
+  y = fmaf(y, u, -0.3333306908607483f);
+  y = fmaf(y, u, 1.0f);
+  const float small = x * cap * y;
+  const float large = near_capped(cap, x);
+  float r;
+  asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %1, 0f3F000000;\n\tselp.f32 %0, %2, %3, p;\n\t}"
+      : "=f"(r)
+      : "f"(fabsf(x)), "f"(small), "f"(large));
+  return r;
+}
+
 // A raw product as a score in units of log 2.
 __device__ __forceinline__ float score_of(const AttnParams &p, float raw, float row_scale) {
-  if (p.cap != 0.0f) return p.cap * tanh_of(raw * row_scale * p.inv_cap);
+  if (p.cap > kNearCap) return capped(p.cap, raw * row_scale * p.inv_cap);
+  if (p.cap != 0.0f) return near_capped(p.cap, raw * row_scale * p.inv_cap);
   return raw * row_scale * p.scale;
+}
+
+// A thread's products of two rows by two tokens by two, as scores.
+__device__ __forceinline__ void scores_of(const AttnParams &p, float (&s)[2][4], const float (&rs)[2]) {
+  if (p.cap > kNearCap) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      s[i >> 2][i & 3] = capped(p.cap, s[i >> 2][i & 3] * rs[i >> 1 & 1] * p.inv_cap);
+  } else if (p.cap != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      s[i >> 2][i & 3] = near_capped(p.cap, s[i >> 2][i & 3] * rs[i >> 1 & 1] * p.inv_cap);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i >> 2][i & 3] *= rs[i >> 1 & 1] * p.scale;
+  }
 }
 
 // D += A B, m16n8k16.

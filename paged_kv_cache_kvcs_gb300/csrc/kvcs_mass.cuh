@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
                             qf[4 * b + 3][1], k.z, k.w);
           }
         }
+      scores_of(p, s, rs);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kMassThreads, MassShape<kType, kDim>::kCtas)
           const int key = key0 + j * 8 + t + 4 * (i & 1);
           const int a = at[i >> 1];
           if (key <= a && (p.window == 0 || key > a - p.window))
-            acc[j][i & 1] += ex2(score_of(p, s[j][i], rs[i >> 1]) - lse[i >> 1]);
+            acc[j][i & 1] += ex2(s[j][i] - lse[i >> 1]);
         }
     }
     // over the 8 lanes of a token: each exchange halves what a lane holds, and

@@ -147,7 +147,7 @@ struct MtFinder {
   }
 };
 
-template <bool kBf16, int kDim, bool kPlain>
+template <bool kBf16, int kDim, int kScores>
 __global__ void __launch_bounds__(kMtThreads, 1)
     kvcs_mass_tc_kernel(const __grid_constant__ MtParams p, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_q) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
       // rows that every token of the warp sees
       const int all_lo = __shfl_sync(0xffffffffu, r_lo, 31), all_hi = __shfl_sync(0xffffffffu, r_hi, 0);
       const int width = p.tile_tokens * a.group;
-      const float sc = kPlain ? a.scale : 1.0f;
+      const float sc = kScores == kPlain ? a.scale : 1.0f;
       const u64 sc2 = tc::pair(sc, sc);
       u64 acc[4] = {0, 0, 0, 0};   // pairs of +0
       bool past = false;           // a capped score of the token has passed the cap
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kMtThreads, 1)
           ++n_s;
           const int row0 = t * width + hf * 64;   // this half's first row
           const bool full = width == 128 && all_lo <= row0 && all_hi >= row0 + 64;
-          if constexpr (!kPlain) make_scores(a, s, full, past);
+          if constexpr (kScores != kPlain) make_scores<kScores>(a, s, full, past);
           // weights, 0 where the row does not see the token (whatever the
           // row's scores and its log-sum-exp are)
           auto add = [&](auto masked) {

@@ -548,3 +548,32 @@ def test_capped_scores_hang_on_nothing_unseen(kv, dim, new):
     assert torch.equal(mass[ids], got[2][ids])
     n = plain.starts[1]
     assert torch.equal(out[:n], got[0][:n]) and torch.equal(lse[:n], got[1][:n])
+
+
+@pytest.mark.parametrize("softcap", [1e4, 1e6, 1e9])
+@pytest.mark.parametrize("kv,new", [("bf16", [1, 1]), ("fp16", [130, 20]), ("fp8", [1, 1]),
+                                    ("fp8", [130, 20])])
+def test_caps_far_above_the_scores(softcap, kv, new):
+    """A cap that scores never come near changes them by no more than their
+    own rounding: tanh is right relative to the score, not to the cap.
+
+    Bound: that of uncapped scores, and 2^-20 of a score for the capping: 2^-21
+    for tanh and five roundings of 2^-24 (the two constants, the product with
+    one, and the two products that join cap, x and tanh(x) / x)."""
+    case = A.Case(kv=kv, lengths=[700, 300], new=new, seed=55, dim=128)
+    want, bound = A.attention(case, softcap=softcap), A.attention(case)
+    out, lse, _ = run(case, softcap=softcap, max_new=max(new))
+    top = max(float(A.scores(case, r, h, 128 ** -0.5, 1.0, 0.0)[0].abs().max())
+              for r in (0, 1) for h in range(case.heads * case.group))
+    more = top * 2.0 ** -20
+    widest = max(float(v[1].double().abs().max()) for v in case.values)
+    A.close(out, want[0], bound[2] + 2 * more * widest)
+    A.close(lse, want[1], bound[3] + more)
+    before = torch.zeros((case.nb, case.heads, case.bs))
+    exact = want[1].float().cuda()
+    mass = before.cuda()
+    K.attention_mass(case.cache, case.bs, *case.table, case.q, case.new_offsets, exact, mass,
+                     max_new=max(new), kv_dtype=case.kv, softcap=softcap)
+    A.close(mass, A.mass(case, exact, before, softcap=softcap)[0],
+            A.mass(case, exact, before)[1] * (1 + 2 * more) + 2 * more *
+            A.mass(case, exact, before, softcap=softcap)[0])
