@@ -122,6 +122,16 @@ __device__ __forceinline__ long long block_scan(long long v, long long *total, l
   return before + inc - v;
 }
 
+// What is taken off a running maximum, in units of log 2.  Weights 2^(z - m)
+// are multiplied in 16 bits.  In fp16 they lose bits below 2^-14 and vanish
+// below 2^-25, while l counts them whole: with one token far above a long tail,
+// the tail's share of the output would be lost.  Made 2^14 times larger (the
+// largest weight is 2^14 then, of 65504) they vanish below 2^-39 of the largest
+// only; l grows alike, so the quotient and the log-sum-exp stay.  bf16 has
+// 32-bit floats' exponents.
+template <int kType>
+constexpr float kLift = kType == kKvBf16 ? 0.0f : 14.0f;
+
 // Running state of the 16 rows of a warp: lane 4 g + t holds rows g and g + 8.
 template <int kDim>
 struct RowState {
@@ -212,7 +222,7 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
     float v = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    mx[r] = fmaxf(st.m[r], v * sc[r]);
+    mx[r] = fmaxf(st.m[r], v * sc[r] - kLift<kType>);
     base[r] = mx[r] == kNegInf ? 0.0f : mx[r];
   }
   if (__any_sync(0xffffffffu, mx[0] != st.m[0] || mx[1] != st.m[1])) {
@@ -237,9 +247,10 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
       s[j][i] = ex2(fmaf(s[j][i], sc[i >> 1], -base[i >> 1]));
       st.l[i >> 1] += s[j][i];
     }
-  // the weights as the A operand, rounded to the cache's 16-bit type (fp16
-  // for fp8 caches): a relative 2^-9 (2^-12) of each, below the output's
-  // own rounding
+  // the weights as the A operand, rounded to the cache's 16-bit type (fp16 for
+  // fp8 caches), which the products take: each by 2^-8 (2^-11) of itself at
+  // most, as an output's own rounding; fp16 ones below 2^-28 of the largest by
+  // up to 2^-39 of that
   const u32 a0 = pack2<kBf16>(s[0][0], s[0][1]), a1 = pack2<kBf16>(s[0][2], s[0][3]);
   const u32 a2 = pack2<kBf16>(s[1][0], s[1][1]), a3 = pack2<kBf16>(s[1][2], s[1][3]);
   u32 seen_bad = 0;   // a non-finite V value, in chunks that some row sees only partly

@@ -20,9 +20,10 @@
 // ready also says that O_i's last addition is done.
 //
 // The running maximum is only raised when a row's scores pass it by more than
-// 2^8: weights then stay below 2^8 and nothing has to be rescaled for most
-// tiles; when a row does pass, its thread rescales its row of O in tensor
-// memory itself (the additions to it are done by then).
+// 2^8: weights then stay below 2^8 (2^15 in fp16, which starts 2^7 higher) and
+// nothing has to be rescaled for most tiles; when a row does pass, its thread
+// rescales its row of O in tensor memory itself (the additions to it are done
+// by then).
 //
 // A weight of 0 times a NaN or infinite V value would be NaN.  V rows of slots
 // that hold no token are therefore zeroed in shared memory, and in tiles that
@@ -54,7 +55,11 @@ constexpr int kTcRegsOther = 88;
 constexpr int kTcRows = 256;      // query rows of a unit
 constexpr int kTcKeys = 128;      // tokens of a tile
 constexpr int kTcMaxSplits = 16;  // parts of a unit's token range, at most
-constexpr float kTcSlack = 8.0f;  // log2 of the largest weight left unscaled
+constexpr float kTcSlack = 8.0f;  // log2 of what scores pass the running maximum by, unscaled
+// As kLift: with the slack the largest weight is 2^15, and weights vanish below
+// 2^-32 of the row's largest.
+template <bool kBf16>
+constexpr float kTcLift = kBf16 ? 0.0f : 7.0f;
 constexpr int kTcDirty = 8;       // partly seen tiles of a unit, at most
 
 template <int kDim>
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               m2 = tc::max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
               m3 = tc::max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
             }
-            const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
+            const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc - kTcLift<kBf16>;
             const bool raise_m = mx > m + kTcSlack || (m == kNegInf && mx != kNegInf);
             if (!__any_sync(0xffffffffu, raise_m)) break;
             const float f = raise_m ? (m == kNegInf ? 0.0f : ex2(m - mx)) : 1.0f;

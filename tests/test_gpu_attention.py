@@ -577,3 +577,41 @@ def test_caps_far_above_the_scores(softcap, kv, new):
     A.close(mass, A.mass(case, exact, before, softcap=softcap)[0],
             A.mass(case, exact, before)[1] * (1 + 2 * more) + 2 * more *
             A.mass(case, exact, before, softcap=softcap)[0])
+
+
+@pytest.mark.parametrize("spread", [0.1, 1.0])
+@pytest.mark.parametrize("length", [1000, 65536])
+@pytest.mark.parametrize("kv,dim,new", [("fp16", 64, 1), ("fp16", 128, 33), ("fp16", 64, 300),
+                                        ("fp16", 80, 20), ("fp8", 128, 1), ("fp8", 64, 20),
+                                        ("bf16", 128, 33)])
+def test_small_weights_beside_a_large_one(kv, dim, new, length, spread):
+    """One token takes nearly all weight and has a V of 0, as sinks have: the
+    output is made of the many others' weights, about 2^-24 each.
+
+    Bound: beyond attention_ref's, what a weight is off by where it is too
+    small for fp16's full precision, half its smallest step: 2^-25 of 2^-14
+    (chunk kernel: 2^-7) of the row's largest weight."""
+    if length > 1000 and new > 100:
+        pytest.skip("a long reference")
+    case = A.Case(kv=kv, heads=1, group=2, dim=dim, lengths=[length], new=[new], seed=60,
+                  scale=spread, tail=0.0)
+    v = (case.values[0][1].float() + 1).to(case.kv)
+    case.values[0][1] = v
+    whole, raw = length // case.bs, v.view(torch.uint8).cuda()
+    pool = case.pool.view(2, case.nb, case.bs, -1)
+    ids = case.ids.long().cuda()
+    pool[1, ids[:whole]] = raw[:whole * case.bs].view(whole, case.bs, -1)
+    if length % case.bs:
+        pool[1, ids[whole], :length % case.bs] = raw[whole * case.bs:].view(length % case.bs, -1)
+    case.q[:, :, 0] = 8.0
+    sink = torch.zeros((1, dim))
+    sink[0, 0] = 17.0 * dim ** 0.5 / 8
+    case.put(0, 0, 0, sink)
+    case.put(0, 1, 0, torch.zeros((1, dim)))
+    out, lse, status = run(case, v_scale=1024.0, max_new=new)
+    ref = A.attention(case, v_scale=1024.0)
+    assert status == 0 and float(ref[0].abs().max()) > 1e-3
+    step = 2.0 ** -32 if kv == "fp16" and dim in (64, 128) and new * 2 > 16 else 2.0 ** -39
+    lost = case.values[0][1].double().abs().sum(0)[0] * (step if kv != "bf16" else 0.0) * 1024.0
+    A.close(out, ref[0], ref[2] + lost)
+    A.close(lse, ref[1], ref[3])
