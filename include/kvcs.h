@@ -551,7 +551,8 @@ typedef struct kvcs_eviction {
  * kvcs_eviction_workspace -- bytes of workspace a kvcs_evict call with these
  * caches and sizes needs: 4 bytes per listed token and KV head of the caches
  * that one launch takes (up to 32), as the scores take.
- * Returns the error codes of kvcs_evict for bad caches and sizes.
+ * Returns the error codes of kvcs_evict for bad caches and sizes, those too
+ * large among them.
  */
 int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                             int64_t num_requests, int64_t total_positions, int64_t *bytes);
@@ -570,8 +571,9 @@ int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_
  * or a negative keep (KVCS_STATUS_BAD_REQUESTS) is left untouched.
  * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a
  * STATE cache, a negative count, missing or misaligned pointers or a short
- * workspace; KVCS_EUNSUPPORTED for a page of 2 GiB or more, or 2^31 or more
- * tokens in the listed blocks.
+ * workspace; KVCS_EUNSUPPORTED for a page of 2 GiB or more, 2^31 or more
+ * tokens in the listed blocks, or 2^27 or more (request, KV head) pairs of one
+ * cache.  A refused call has done nothing.
  */
 int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                const kvcs_requests *reqs, int64_t total_positions, const kvcs_eviction *ev,

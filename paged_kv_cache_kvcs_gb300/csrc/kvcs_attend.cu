@@ -335,13 +335,25 @@ int check_evict_caches(const kvcs_cache *caches, int32_t num_caches, int32_t blo
   return KVCS_OK;
 }
 
+// What an eviction's sizes must stay below, whatever its launches: 31-bit token
+// and row numbers.
+int check_evict_sizes(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
+                      int64_t num_requests, int64_t total_positions) {
+  if (static_cast<double>(total_positions) * block_size >= 2147483648.0) return KVCS_EUNSUPPORTED;
+  for (int32_t lo = 0; lo < num_caches;) {
+    const EvictLaunch l = evict_launch(caches, lo, num_caches, num_requests);
+    if (l.caches == 0) return KVCS_EUNSUPPORTED;
+    lo += l.caches;
+  }
+  return KVCS_OK;
+}
+
 // Launches follow one another on the stream and share the space.
 int64_t evict_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                         int64_t num_requests, int64_t total_positions) {
   long long rows = 0;
   for (int32_t lo = 0; lo < num_caches;) {
     const EvictLaunch l = evict_launch(caches, lo, num_caches, num_requests);
-    if (l.caches == 0) break;
     rows = std::max(rows, l.rows);
     lo += l.caches;
   }
@@ -577,7 +589,9 @@ int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_
 int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                             int64_t num_requests, int64_t total_positions, int64_t *bytes) {
   if (!bytes || num_requests < 0 || total_positions < 0) return KVCS_EINVAL;
-  const int rc = check_evict_caches(caches, num_caches, block_size);
+  int rc = check_evict_caches(caches, num_caches, block_size);
+  if (rc == KVCS_OK)
+    rc = check_evict_sizes(caches, num_caches, block_size, num_requests, total_positions);
   if (rc != KVCS_OK) return rc;
   *bytes = evict_workspace(caches, num_caches, block_size, num_requests, total_positions);
   return KVCS_OK;
@@ -597,7 +611,8 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   if (!aligned(ev->new_block_ids, 4) || !aligned(ev->block_sums, 8)) return KVCS_EINVAL;
   if (reqs->num_requests == 0 || total_positions == 0) return KVCS_OK;
   if (!ev->keep || !aligned(ev->keep, 8)) return KVCS_EINVAL;
-  if (static_cast<double>(total_positions) * block_size >= 2147483648.0) return KVCS_EUNSUPPORTED;
+  rc = check_evict_sizes(caches, num_caches, block_size, reqs->num_requests, total_positions);
+  if (rc != KVCS_OK) return rc;
   if (!ev->workspace || !aligned(ev->workspace, 16) ||
       ev->workspace_bytes <
           evict_workspace(caches, num_caches, block_size, reqs->num_requests, total_positions))
@@ -640,7 +655,6 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   }
   for (int32_t lo = 0; lo < num_caches;) {
     const EvictLaunch l = evict_launch(caches, lo, num_caches, reqs->num_requests);
-    if (l.caches == 0) return KVCS_EUNSUPPORTED;
     // few rows: each is split by halves and columns of at least 32 bytes.  (One
     // request, 8 rows, in place: 20,011 tokens to 4096 146 us unsplit, 102 with
     // columns of 128 bytes, 74 of 64, 68 of 32; 131,072 to 65,536 1137, 706, 628

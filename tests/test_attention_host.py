@@ -228,3 +228,26 @@ def test_binding_refusals(monkeypatch):
                       (dict(status=FakeTensor(1, torch.float32)), "status")):
         with pytest.raises(ValueError, match=what):
             call(fn=ev, **bad)
+
+
+def test_evictions_too_large_are_refused_before_any_work():
+    """More rows than a launch can number, or more tokens, in the call and in
+    its workspace's size alike; a refusal leaves words and caches as they
+    were (here, without a GPU, any work at all would be KVCS_ECUDA)."""
+    def size(caches, requests, positions):
+        n = ctypes.c_int64(-1)
+        rc = K.load_library().kvcs_eviction_workspace(
+            K.cache_array(caches), len(caches), 16, requests, positions, ctypes.byref(n))
+        return n.value if rc == K.KVCS_OK else rc
+    small, large = FakeCache(layer=0, num_heads=1), FakeCache(layer=1, num_heads=8)
+    many = dict(num_requests=1 << 24)                  # 2^27 rows of the large cache
+    for caches in ([large], [small, large]):
+        assert evict(caches, reqs=many, block_sums=1 << 26, workspace_bytes=1 << 62) == \
+            K.KVCS_EUNSUPPORTED
+        assert size(caches, 1 << 24, 10) == K.KVCS_EUNSUPPORTED
+    fewer = dict(num_requests=(1 << 24) - 1)
+    assert evict([small, large], reqs=fewer, workspace_bytes=1 << 62) == K.KVCS_ECUDA
+    assert size([small, large], (1 << 24) - 1, 10) > 0
+    assert size([large], 2, 1 << 27) == K.KVCS_EUNSUPPORTED         # 2^31 tokens
+    assert size([large], 2, (1 << 27) - 1) > 0
+    assert size([large], 2, 1 << 60) == K.KVCS_EUNSUPPORTED
