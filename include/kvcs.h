@@ -493,7 +493,8 @@ int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_
  * Results do not depend on timing: the same call gives the same bits.
  * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a
  * STATE cache, types that do not go together, q_heads not a multiple of
- * num_heads, a negative or non-finite size or scale, missing or misaligned
+ * num_heads, a negative or non-finite size or scale (scale * k_scale and its
+ * quotient by softcap among them, as 32-bit floats), missing or misaligned
  * pointers, or a short workspace; KVCS_EUNSUPPORTED for a LATENT cache, a
  * head that is not 8 to 256 elements (a multiple of 8), a page of 2 GiB or
  * more, or 2^31 or more query rows.

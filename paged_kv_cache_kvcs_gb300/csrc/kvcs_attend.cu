@@ -90,6 +90,13 @@ int check_attention(const kvcs_cache *cache, int32_t block_size, const kvcs_atte
   if (!std::isfinite(a->scale) || !std::isfinite(a->k_scale) || !std::isfinite(a->v_scale) ||
       !std::isfinite(a->softcap) || a->softcap < 0.0f)
     return KVCS_EINVAL;
+  // (and what is made of them: an infinite factor turns a product of 0 into
+  // NaN, and a quotient below the normal numbers has lost bits that a cap this
+  // large brings back)
+  const float factor = a->scale * a->k_scale, quotient = a->softcap > 0.0f ? factor / a->softcap : 0.0f;
+  if (!std::isfinite(factor * kLog2e) || !std::isfinite(a->softcap * kLog2e) ||
+      !std::isfinite(quotient) || (a->softcap > 1e18f && factor != 0.0f && !std::isnormal(quotient)))
+    return KVCS_EINVAL;
   if (cache->layout == KVCS_LAYOUT_LATENT) return KVCS_EUNSUPPORTED;
   const int es = element_bytes(a->kv_dtype);
   if (cache->head_bytes % (8 * es) || cache->head_bytes / es > 256) return KVCS_EUNSUPPORTED;

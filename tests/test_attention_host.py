@@ -251,3 +251,17 @@ def test_evictions_too_large_are_refused_before_any_work():
     assert size([large], 2, 1 << 27) == K.KVCS_EUNSUPPORTED         # 2^31 tokens
     assert size([large], 2, (1 << 27) - 1) > 0
     assert size([large], 2, 1 << 60) == K.KVCS_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("mass", [False, True])
+def test_scales_that_32_bits_do_not_hold_are_refused(mass):
+    """Each number may be finite and what the kernels make of them not: an
+    infinite scale turns a product of 0 into NaN."""
+    for bad in (dict(scale=1e30, k_scale=1e30), dict(scale=3e38), dict(softcap=3e38),
+                dict(softcap=1e-30, scale=1e30), dict(softcap=1e38, scale=0.1),
+                dict(scale=-1e30, k_scale=1e30)):
+        assert attend(mass=mass, **bad) == K.KVCS_EINVAL, bad
+    for good in (dict(scale=1e-30, k_scale=1e-30), dict(softcap=50.0, scale=1e-37),
+                 dict(softcap=1e30), dict(scale=0.0, softcap=50.0),
+                 dict(scale=-1.0, softcap=1e-3), dict(scale=1e38)):
+        assert attend(mass=mass, **good) == K.KVCS_ECUDA, good
