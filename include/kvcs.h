@@ -497,7 +497,8 @@ int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_
  * quotient by softcap among them, as 32-bit floats), missing or misaligned
  * pointers, or a short workspace; KVCS_EUNSUPPORTED for a LATENT cache, a
  * head that is not 8 to 256 elements (a multiple of 8), a page of 2 GiB or
- * more, or 2^31 or more query rows.
+ * more, 2^31 or more query rows, or a max_new (where it is 0, a total_new) of
+ * 2^30 or more.
  */
 int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs_requests *reqs,
                          int64_t total_positions, const kvcs_attention *att, uint32_t *status,

@@ -103,6 +103,8 @@ int check_attention(const kvcs_cache *cache, int32_t block_size, const kvcs_atte
   const int64_t dim = cache->head_bytes / es;
   if (a->q_stride && (a->q_stride % 8 || a->q_stride < a->q_heads * dim)) return KVCS_EINVAL;
   if (static_cast<double>(a->total_new) * a->q_heads >= 2147483648.0) return KVCS_EUNSUPPORTED;
+  // (a request's positions stay below 2^31: 2^30 cached tokens and fewer new ones)
+  if ((a->max_new > 0 ? a->max_new : a->total_new) >= kMaxRequestTokens) return KVCS_EUNSUPPORTED;
   if (static_cast<double>(block_size) * cache->num_heads * cache->head_bytes >= 2147483648.0)
     return KVCS_EUNSUPPORTED;
   return KVCS_OK;

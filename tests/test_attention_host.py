@@ -265,3 +265,15 @@ def test_scales_that_32_bits_do_not_hold_are_refused(mass):
                  dict(softcap=1e30), dict(scale=0.0, softcap=50.0),
                  dict(scale=-1.0, softcap=1e-3), dict(scale=1e38)):
         assert attend(mass=mass, **good) == K.KVCS_ECUDA, good
+
+
+@pytest.mark.parametrize("mass", [False, True])
+def test_requests_of_2_30_new_tokens_are_refused(mass):
+    """Positions of new tokens are 31-bit numbers too."""
+    one = FakeCache(num_heads=1, head_bytes=16)
+    n = 1 << 30
+    assert attend(one, mass=mass, q_heads=1, total_new=n) == K.KVCS_EUNSUPPORTED
+    assert attend(one, mass=mass, q_heads=1, total_new=n + 5, max_new=n) == K.KVCS_EUNSUPPORTED
+    space = dict(workspace_bytes=1 << 50)
+    assert attend(one, mass=mass, q_heads=1, total_new=n - 1, **space) == K.KVCS_ECUDA
+    assert attend(one, mass=mass, q_heads=1, total_new=n + 5, max_new=n - 1, **space) == K.KVCS_ECUDA
