@@ -196,8 +196,13 @@ __device__ __forceinline__ void attend_chunk(const AttnParams &p, const u32 (&qf
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[j][i] += s2[j][i];
   // scores = sc * s; capped ones, and those of a scale that would turn the
-  // maximum round or make 0 of a masked score, are made first
+  // maximum round or make NaN of a masked score, are made first
   float sc[2] = {rs[0] * p.scale, rs[1] * p.scale};
+  if constexpr (kType == kKvFp8) {
+    // (a row's factor may underflow: 0 would make NaN of a masked score too)
+    sc[0] = fmaxf(sc[0], __int_as_float(1));
+    sc[1] = fmaxf(sc[1], __int_as_float(1));
+  }
   if (p.cap != 0.0f || p.scale <= 0.0f) {
     scores_of(p, s, rs);
     sc[0] = sc[1] = 1.0f;

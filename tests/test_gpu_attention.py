@@ -615,3 +615,13 @@ def test_small_weights_beside_a_large_one(kv, dim, new, length, spread):
     lost = case.values[0][1].double().abs().sum(0)[0] * (step if kv != "bf16" else 0.0) * 1024.0
     A.close(out, ref[0], ref[2] + lost)
     A.close(lse, ref[1], ref[3])
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 40]], ids=["one", "many"])
+def test_queries_and_scales_that_underflow_together(new):
+    """Queries so small that a row's factor is 0 in 32 bits: all scores are 0,
+    and masked ones stay masked."""
+    case = A.Case(kv="fp8", lengths=[37, 100], new=new, seed=61, dim=64)
+    case.q.fill_(1e-38)
+    check(case, k_scale=1e-8)
+    check_mass(case, k_scale=1e-8)
