@@ -64,8 +64,11 @@ bool needs_8(const kvcs_cache &c) {
   return !aligned(c.base, 16) || c.half_stride % 16 || c.block_stride % 16 || c.head_bytes % 16;
 }
 
-int check_tables(const kvcs_requests *reqs, int64_t total_positions) {
+int check_tables(const kvcs_requests *reqs, int64_t total_positions, const uint32_t *status) {
   if (!reqs || total_positions < 0 || reqs->num_requests < 0) return KVCS_EINVAL;
+  if (!aligned(reqs->pos_offsets, 8) || !aligned(reqs->first_position, 8) ||
+      !aligned(reqs->num_tokens, 8) || !aligned(reqs->block_ids, 4) || !aligned(status, 4))
+    return KVCS_EINVAL;
   if (reqs->num_requests == 0) return KVCS_OK;
   if (!reqs->pos_offsets || !reqs->first_position || !reqs->num_tokens) return KVCS_EINVAL;
   if (total_positions > 0 && !reqs->block_ids) return KVCS_EINVAL;
@@ -468,11 +471,11 @@ int kvcs_paged_attention(const kvcs_cache *cache, int32_t block_size, const kvcs
                          void *stream) {
   int rc = check_attention(cache, block_size, att);
   if (rc != KVCS_OK) return rc;
-  rc = check_tables(reqs, total_positions);
+  rc = check_tables(reqs, total_positions, status);
   if (rc != KVCS_OK) return rc;
   if (att->total_new == 0 || reqs->num_requests == 0) return KVCS_OK;
-  if (!att->q || !att->out || !att->new_offsets || !aligned(att->q, 16) ||
-      !aligned(att->out, 16) || !aligned(att->lse, 4) || !att->workspace ||
+  if (!att->q || !att->out || !att->new_offsets || !aligned(att->new_offsets, 8) ||
+      !aligned(att->q, 16) || !aligned(att->out, 16) || !aligned(att->lse, 4) || !att->workspace ||
       !aligned(att->workspace, 16))
     return KVCS_EINVAL;
   int sms = 0;
@@ -546,11 +549,11 @@ int kvcs_attention_mass(const kvcs_cache *cache, int32_t block_size, const kvcs_
                         uint32_t *status, void *stream) {
   int rc = check_attention(cache, block_size, att);
   if (rc != KVCS_OK) return rc;
-  rc = check_tables(reqs, total_positions);
+  rc = check_tables(reqs, total_positions, status);
   if (rc != KVCS_OK) return rc;
   if (att->total_new == 0 || reqs->num_requests == 0) return KVCS_OK;
   if (!att->q || !att->lse || !att->new_offsets || !mass || !aligned(att->q, 16) ||
-      !aligned(att->lse, 4) || !aligned(mass, 4))
+      !aligned(att->new_offsets, 8) || !aligned(att->lse, 4) || !aligned(mass, 4))
     return KVCS_EINVAL;
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return KVCS_ECUDA;
@@ -612,7 +615,7 @@ int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
   if (!ev) return KVCS_EINVAL;
   int rc = check_evict_caches(caches, num_caches, block_size);
   if (rc != KVCS_OK) return rc;
-  rc = check_tables(reqs, total_positions);
+  rc = check_tables(reqs, total_positions, status);
   if (rc != KVCS_OK) return rc;
   if (ev->sinks < 0 || ev->recent < 0 || !ev->scores) return KVCS_EINVAL;
   for (int32_t i = 0; i < num_caches; ++i)

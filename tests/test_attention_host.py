@@ -277,3 +277,22 @@ def test_requests_of_2_30_new_tokens_are_refused(mass):
     space = dict(workspace_bytes=1 << 50)
     assert attend(one, mass=mass, q_heads=1, total_new=n - 1, **space) == K.KVCS_ECUDA
     assert attend(one, mass=mass, q_heads=1, total_new=n + 5, max_new=n - 1, **space) == K.KVCS_ECUDA
+
+
+def test_misaligned_tables_are_refused():
+    """Tables that the kernels could not read without a fault."""
+    for name, at in REQS.items():
+        if name == "num_requests":
+            continue
+        off = {name: at + (2 if name == "block_ids" else 4)}
+        for code in (attend(reqs=off), attend(reqs=off, mass=True), evict(reqs=off)):
+            assert code == K.KVCS_EINVAL, name
+    for mass in (False, True):
+        assert attend(new_offsets=(1 << 21) + 4, mass=mass) == K.KVCS_EINVAL
+    lib, arr, r, a = K.load_library(), K.cache_array([FakeCache()]), B.kvcs_requests(**REQS), attention()
+    ev = B.kvcs_eviction((ctypes.c_void_p * 1)(1 << 20), 1 << 16, 0, 0, None, None, 1 << 17, 1 << 30)
+    head = (arr, 16, ctypes.byref(r), 10)
+    for status, code in (((1 << 26) + 2, K.KVCS_EINVAL), (1 << 26, K.KVCS_ECUDA)):
+        assert lib.kvcs_paged_attention(*head, ctypes.byref(a), status, None) == code
+        assert lib.kvcs_attention_mass(*head, ctypes.byref(a), 1 << 25, status, None) == code
+        assert lib.kvcs_evict(arr, 1, *head[1:], ctypes.byref(ev), status, None) == code
