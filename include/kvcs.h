@@ -575,7 +575,8 @@ int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_
  * STATE cache, a negative count, missing or misaligned pointers or a short
  * workspace; KVCS_EUNSUPPORTED for a page of 2 GiB or more, 2^31 or more
  * tokens in the listed blocks, or 2^27 or more (request, KV head) pairs of one
- * cache.  A refused call has done nothing.
+ * cache (fewer where a head's row is past 32 KiB).  A refused call has done
+ * nothing.
  */
 int kvcs_evict(const kvcs_cache *caches, int32_t num_caches, int32_t block_size,
                const kvcs_requests *reqs, int64_t total_positions, const kvcs_eviction *ev,

@@ -313,8 +313,9 @@ int64_t attend_workspace(const AttendPlan &pl) {
 
 constexpr int kEvictSmemTokens = 49152;   // 192 KiB of scores
 
-// As many caches from `lo` on as one launch holds and its grid can number
-// (up to 64 column groups and spans a row).
+// As many caches from `lo` on as one launch holds and its grids can number
+// (column groups a row: eight of its halves at most, or as many as its pieces
+// need with a thread each; spans only where the rows are few).
 struct EvictLaunch {
   int caches;
   long long rows;
@@ -322,9 +323,13 @@ struct EvictLaunch {
 EvictLaunch evict_launch(const kvcs_cache *caches, int32_t lo, int32_t num_caches,
                          int64_t num_requests) {
   EvictLaunch l = {0, 0};
+  double groups = 0.0;
   while (lo + l.caches < num_caches && l.caches < kEvictCaches) {
-    const long long rows = l.rows + caches[lo + l.caches].num_heads;
-    if (static_cast<double>(rows) * num_requests * 16.0 >= 2147483648.0) break;
+    const kvcs_cache &c = caches[lo + l.caches];
+    const long long rows = l.rows + c.num_heads;
+    const int pieces = c.head_bytes / (needs_8(c) ? 8 : 16);
+    groups = std::max(groups, 2.0 * std::max(8, (pieces + kEvictThreads - 1) / kEvictThreads));
+    if (static_cast<double>(rows) * num_requests * groups >= 2147483648.0) break;
     l.rows = rows;
     ++l.caches;
   }
@@ -407,7 +412,6 @@ int launch_evict(const EvictCall &call, const kvcs_cache *caches, float *const *
   if (p.new_block_ids)
     p.spans = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>({average / kEvictChunk, 8ll * sms / units, 64})));
-  if (static_cast<double>(units) * p.spans >= 2147483648.0) return KVCS_EUNSUPPORTED;
   // (short rows need no leave for more than the standard 48 KiB)
   if (p.smem_tokens * 4 > 32768 &&
       cudaFuncSetAttribute(reinterpret_cast<const void *>(kvcs_evict_select_kernel<kCaches>),

@@ -296,3 +296,18 @@ def test_misaligned_tables_are_refused():
         assert lib.kvcs_paged_attention(*head, ctypes.byref(a), status, None) == code
         assert lib.kvcs_attention_mass(*head, ctypes.byref(a), 1 << 25, status, None) == code
         assert lib.kvcs_evict(arr, 1, *head[1:], ctypes.byref(ev), status, None) == code
+
+
+def test_evictions_of_very_long_rows_are_refused_before_any_work():
+    """The move takes more CTAs a row where a head's row is past 32 KiB; that
+    many have to fit a grid too, which was only seen between the launches."""
+    wide = FakeCache(num_heads=1, head_bytes=1 << 20)      # 256 column groups, in 2 halves
+    def code(requests):
+        return evict([wide], reqs=dict(num_requests=requests), block_sums=1 << 26,
+                     workspace_bytes=1 << 62)
+    def size(requests):
+        n = ctypes.c_int64()
+        return K.load_library().kvcs_eviction_workspace(K.cache_array([wide]), 1, 16, requests, 10,
+                                                        ctypes.byref(n))
+    assert code(1 << 22) == size(1 << 22) == K.KVCS_EUNSUPPORTED
+    assert code((1 << 22) - 1) == K.KVCS_ECUDA and size((1 << 22) - 1) == K.KVCS_OK
