@@ -68,7 +68,9 @@ def _empty(shape, dtype, stream, handle: int, dev):
     """A tensor that belongs to the stream the call writes it on."""
     if stream is None or handle == torch.cuda.current_stream(dev).cuda_stream:
         return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+    # (a handle of 0 is no external stream to torch: it would make one of its own)
+    owner = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(owner):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 

@@ -625,3 +625,20 @@ def test_queries_and_scales_that_underflow_together(new):
     case.q.fill_(1e-38)
     check(case, k_scale=1e-8)
     check_mass(case, k_scale=1e-8)
+
+
+def test_outputs_belong_to_the_default_stream_given_by_its_handle():
+    """A call on stream 0, by number, from within another stream: what it
+    allocates belongs to stream 0, and to no other that the allocator would
+    let it be used again on."""
+    case = A.Case(dim=64, lengths=[400, 90], new=[1, 30], seed=62)
+    want = run(case, max_new=30)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out, lse = K.paged_attention(case.cache, case.bs, *case.table, case.q, case.new_offsets,
+                                     max_new=30, stream=0, total_positions=case.total)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for t in (out, lse):
+        owner = [s["stream"] for s in torch.cuda.memory_snapshot()
+                 if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+        assert owner == [0]
