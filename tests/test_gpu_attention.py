@@ -642,3 +642,24 @@ def test_outputs_belong_to_the_default_stream_given_by_its_handle():
         owner = [s["stream"] for s in torch.cuda.memory_snapshot()
                  if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
         assert owner == [0]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_bad_blocks_among_many_units(dim):
+    """Units of one and of two query tiles that follow one another on a CTA,
+    some slowed down by the look-up of bad blocks in their last tokens."""
+    g = torch.Generator().manual_seed(63)
+    lengths = torch.randint(40, 500, (40,), generator=g).tolist()
+    new = [min(n, 5 + (37 * i) % 120) for i, n in enumerate(lengths)]
+    case = A.Case(dim=dim, heads=8, group=4, lengths=lengths, new=new, seed=63, tail=0.0)
+    blocked = {}
+    for r in range(0, 40, 3):
+        last = case.counts[r] - 1
+        blocked[r] = (last, max(0, last - 4))
+        for b in blocked[r]:
+            case.table[3][case.offsets[r] + b] = -1 if r % 2 else case.nb + r
+    out, lse = check(case, blocked=blocked, want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
+    for _ in range(3):
+        again = run(case, max_new=max(new))
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    check_mass(case, blocked=blocked, want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
