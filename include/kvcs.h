@@ -489,6 +489,8 @@ int kvcs_attention_workspace(const kvcs_cache *cache, int32_t block_size, int64_
  *           request): the request's rows see nothing (or, where its
  *           new_offsets are at fault, are left as they were; rows that two
  *           requests claim, where offsets decrease, have no defined result).
+ *           KVCS_STATUS_TIMEOUT: a wait inside a kernel ran out (2 s); rows may
+ *           be left unwritten.
  *
  * Results do not depend on timing: the same call gives the same bits.
  * Returns KVCS_EINVAL for the argument errors of kvcs_block_checksums, a

@@ -31,7 +31,7 @@
 // noted; the rows that do see them add them at the end.
 //
 // Measured (4 requests of 2048 new tokens over 8192, 32 query heads to 8 KV
-// heads of 128, bf16): 664 us, 1445 TFLOP/s, 77% of the measured burst rate of
+// heads of 128, bf16): 669 us, 1437 TFLOP/s, 77% of the measured burst rate of
 // a library product and 86% of its sustained rate.  With the weights left out
 // the products and loads alone take 510 us.  What it grew from and what was
 // left again, for the same call: mma.sync 6300; one issuing thread for both
@@ -205,12 +205,13 @@ inline int scores_kind(const AttnParams &a) {
 // row sees all of them (its token is seen by all of their rows).
 //
 // Capped ones: tanh from its exponential is two operations of the exponential
-// unit a score and six others.  The polynomial is ten operations on pairs; it
-// is taken in whole tiles until one of the thread's products has passed the
-// cap (`past`).  So the form hangs on places, and on what is seen by the
-// thread's row, alone: the two differ in the last bits, and nothing else may
-// show in a row.  (A vote of the warp over all products let the slots behind
-// the last token and the tiles' leftovers choose.)
+// unit a score and six others.  The polynomial is ten operations on pairs (off
+// by 1.3 * 2^-23 of the cap at most, with its roundings); it is taken in whole
+// tiles until one of the thread's products has passed the cap (`past`).  So the
+// form hangs on places, and on what is seen by the thread's row, alone: the two
+// differ in the last bits, and nothing else may show in a row.  (A vote of the
+// warp over all products let the slots behind the last token and the tiles'
+// leftovers choose.)
 // 4 requests of 2048 new tokens over 8192 (32 query heads to 8 KV heads of 128,
 // bf16): 628 us without a cap, 1260 with one of 30 (none passes it), 1510 with
 // one of 2 (one in twenty does); their mass 420, 991 and 1092.  By the vote

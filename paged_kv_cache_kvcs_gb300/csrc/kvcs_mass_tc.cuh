@@ -18,7 +18,7 @@
 // with TMA; warp 19 the rows' log-sum-exps.
 //
 // Measured (4 requests of 2048 new tokens over 8192, 32 query heads to 8 KV
-// heads of 128, bf16): 425 us, 1130 TFLOP/s; 315 with the exponentials and
+// heads of 128, bf16): 427 us, 1127 TFLOP/s; 315 with the exponentials and
 // sums left out, 381 with the products left out.  The small kernel takes 4310.
 #pragma once
 
