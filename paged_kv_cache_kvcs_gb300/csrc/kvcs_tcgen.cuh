@@ -104,6 +104,7 @@ __device__ __forceinline__ void mma_ts(u32 d, u32 a, u64 b, u32 idesc, bool add)
 // loop gives up, where what one lane sees or decides goes for all, and a phase
 // that a lane has seen before is there at the others' next probe.  (Votes on
 // every wait cost 3 to 9% of a product pipeline's time, in the first loop 5%.)
+// The limit lies below 2^32 ns: the timer's low word is enough.
 __device__ __forceinline__ bool wait(u32 bar, u32 parity, u64 limit_ns) {
   if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
 #pragma unroll 1
