@@ -95,29 +95,34 @@ __device__ __forceinline__ void mma_ts(u32 d, u32 a, u64 b, u32 idesc, bool add)
 #define KVCS_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), \
                       "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 
-// As ptx::mbar_wait_bounded, without a look at the global timer (a read of
-// about a microsecond) before 1024 probes have failed: the waits of a
-// product pipeline are shorter than that, and on its critical path.
+// As ptx::mbar_wait_bounded, with a look at the global timer (a read of about a
+// microsecond) after every 1024 probes only: the waits of a product pipeline
+// are shorter than that, and on its critical path.
 // The first probe stands apart: one that succeeds costs about 15 cycles, the
 // loop's bookkeeping about 100 more.  A warp calls it converged and leaves it
-// with one answer, so that none of its lanes goes on alone: only the second
-// loop gives up, where what one lane sees or decides goes for all, and a phase
-// that a lane has seen before is there at the others' next probe.  (Votes on
-// every wait cost 3 to 9% of a product pipeline's time, in the first loop 5%.)
+// with one answer, so that none of its lanes goes on alone: lanes give up by a
+// vote of those that are still there, after a last probe that goes for all of
+// them, and a phase that a lane has seen before is there at that probe.  (Votes
+// on every wait cost 3 to 9% of a product pipeline's time, in the loop 5%.)
 // The limit lies below 2^32 ns: the timer's low word is enough.
 __device__ __forceinline__ bool wait(u32 bar, u32 parity, u64 limit_ns) {
   if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
+  u32 t0 = 0;
 #pragma unroll 1
-  for (u32 i = 0; i < 1024; ++i)
+  for (u32 i = 1; i < (1u << 28); ++i) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
-  const u32 late = __activemask(), t0 = ptx::globaltimer_low();
-  for (;;) {
-    if (__any_sync(late, ptx::mbar_try_wait(bar, parity))) {
-      __syncwarp(late);   // (orders what follows for the lanes that did not see it themselves)
-      return true;
+    if ((i & 1023u) == 0) {
+      const u32 now = ptx::globaltimer_low();
+      if (i == 1024) t0 = now;
+      const u32 late = __activemask();
+      if (__any_sync(late, now - t0 > static_cast<u32>(limit_ns))) {
+        const bool there = __any_sync(late, ptx::mbar_try_wait(bar, parity));
+        __syncwarp(late);   // (orders what follows for the lanes that did not see it themselves)
+        return there;
+      }
     }
-    if (__any_sync(late, ptx::globaltimer_low() - t0 > static_cast<u32>(limit_ns))) return false;
   }
+  return false;
 }
 // 32 columns of this warp's 32 lanes.
 __device__ __forceinline__ void ld32(u32 addr, u32 *v) {

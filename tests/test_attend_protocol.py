@@ -547,22 +547,29 @@ def test_mass_leaves_nothing_behind_when_a_wait_runs_out():
 
 def answers(seed, votes):
     """What each of a warp's lanes gets from one wait.  A lane's probe sees the
-    phase if it has completed by then; lanes probe at moments of their own."""
+    phase if it has completed by then; lanes probe, and read the time, at moments
+    of their own."""
     rnd = random.Random(seed)
     done_at, limit = rnd.uniform(0, 30), 20.0
     first = [rnd.uniform(0, 1) for _ in range(32)]
     got = [True if t >= done_at else None for t in first]
-    late = [n for n in range(32) if got[n] is None]
     t = 1.0
-    while any(got[n] is None for n in late):
-        seen = {n: t + rnd.uniform(0, 1) >= done_at for n in late if got[n] is None}
-        over = {n: t + rnd.uniform(0, 1) - first[n] > limit for n in seen}
-        if votes:
-            seen = dict.fromkeys(seen, any(seen.values()))
-            over = dict.fromkeys(over, any(over.values()))
-        for n in seen:
-            got[n] = True if seen[n] else False if over[n] else None
+    while any(g is None for g in got):
+        left = [n for n in range(32) if got[n] is None]
+        for n in left:
+            if t + rnd.uniform(0, 1) >= done_at:
+                got[n] = True
         t += 1.0
+        left = [n for n in left if got[n] is None]
+        over = [n for n in left if t + rnd.uniform(0, 1) - first[n] > limit]
+        t += 1.0
+        if votes and over:       # one last probe, which goes for all that are left
+            there = any(t + rnd.uniform(0, 1) >= done_at for _ in left)
+            for n in left:
+                got[n] = there
+        elif not votes:
+            for n in over:
+                got[n] = False
     return got
 
 
