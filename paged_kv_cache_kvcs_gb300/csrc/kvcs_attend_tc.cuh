@@ -271,8 +271,8 @@ __device__ __forceinline__ bool bad_blocks(const AttnParams &a, const TcUnit &x)
     const int id = a.tab.block_ids[x.q.pos0 + b];
     bad |= id < 0 || id >= a.map.num_blocks;
   }
-  if (kExt && x.k0 < x.sinks) {
-    hi = min(x.k1 * kTcKeys, x.sink_keys);
+  if constexpr (kExt) {   // (the sinks may reach into the window's first tile)
+    hi = min(x.k1 * kTcKeys, min(x.sink_keys, x.lo));
     for (int b = x.k0 * kTcKeys / bs + (threadIdx.x & 31); b * static_cast<long long>(bs) < hi; b += 32) {
       const int id = a.tab.block_ids[x.q.pos0 + b];
       bad |= id < 0 || id >= a.map.num_blocks;

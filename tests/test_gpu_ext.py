@@ -129,6 +129,32 @@ def test_bad_blocks_of_sinks_and_windows_are_left_out(new):
           want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
 
 
+@pytest.mark.parametrize("kv,dim", [("bf16", 128), ("fp16", 64), ("fp8", 64), ("fp8", 128), ("int8s", 128),
+                                    ("fp8s", 64)])
+@pytest.mark.parametrize("new", [[2, 1, 3], [20, 33, 70]], ids=["few", "many"])
+def test_bad_blocks_of_sinks_beside_the_window(new, kv, dim):
+    """A bad block of the sinks is left out and flagged where the window starts
+    in the sinks' last tile of 128 tokens: the first one, or a later one."""
+    case = make(kv, dim=dim, lengths=[300, 420, 330], new=new, seed=34)
+    case.table[3][case.offsets[0]] = -1
+    case.table[3][case.offsets[1] + 8] = case.nb
+    case.table[3][case.offsets[2] + 1] = -7
+    # windows that start at 81 to 99, 188 to 220 and 61 to 128; the bad blocks are
+    # tokens 0 to 15, 128 to 143 and 16 to 31
+    check(case, window=200, sinks=140, blocked={0: (0,), 1: (8,), 2: (1,)},
+          want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8s"])
+@pytest.mark.parametrize("bad", [0, 119, 120, 122], ids=str)
+def test_bad_blocks_of_sinks_in_split_calls(bad, kv):
+    """One request, its tokens split into parts of some tiles: a part may begin
+    where the sinks end and the window starts."""
+    case = make(kv, dim=128, heads=1, lengths=[4000], new=[20], seed=35)
+    case.table[3][case.offsets[0] + bad] = -1
+    check(case, window=2000, sinks=1960, blocked={0: (bad,)}, want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
+
+
 # ---------------------------------------------------------------------------
 # drafted trees
 # ---------------------------------------------------------------------------
