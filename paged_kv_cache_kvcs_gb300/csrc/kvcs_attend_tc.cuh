@@ -212,9 +212,12 @@ struct TcFinder {
       x.sink_keys = min(sink_keys_of(a, x.q), x.hi);
     }
     const int t0 = x.lo / kTcKeys;
-    const int t1 = x.hi > x.lo ? (x.hi + kTcKeys - 1) / kTcKeys : t0;
+    int t1 = x.hi > x.lo ? (x.hi + kTcKeys - 1) / kTcKeys : t0;
     if constexpr (kExt) {
-      x.sinks = min(t0, (x.sink_keys + kTcKeys - 1) / kTcKeys);
+      // (listed tokens may end before the window: the sinks are seen all the same)
+      const int sinks = (x.sink_keys + kTcKeys - 1) / kTcKeys;
+      x.sinks = min(t0, sinks);
+      t1 = max(t1, sinks);
       x.skip = t0 - x.sinks;
       const int n = x.sinks + t1 - t0, per = (n + p.splits - 1) / p.splits;
       x.k0 = min(n, x.split * per);

@@ -155,6 +155,32 @@ def test_bad_blocks_of_sinks_in_split_calls(bad, kv):
     check(case, window=2000, sinks=1960, blocked={0: (bad,)}, want_status=K.KVCS_STATUS_BAD_BLOCK_ID)
 
 
+def list_only(case, counts):
+    """Has the table list each request's first blocks alone."""
+    ids = [case.ids[o:o + n] for o, n in zip(case.offsets, counts)]
+    case.values = [v[:, :n * case.bs] for v, n in zip(case.values, counts)]
+    case.ids = torch.cat(ids)
+    case.offsets = [sum(counts[:r]) for r in range(len(counts) + 1)]
+    case.total = case.offsets[-1]
+    case.table[0] = torch.tensor(case.offsets, dtype=torch.int64, device="cuda")
+    case.table[3] = case.ids.to("cuda")
+
+
+@pytest.mark.parametrize("kv,dim", [("bf16", 128), ("fp16", 64), ("fp8", 128), ("int8s", 64), ("fp8s", 128)])
+@pytest.mark.parametrize("new", [[1, 3, 2, 1], [20, 20, 33, 70]], ids=["few", "many"])
+def test_sinks_of_tables_that_end_before_the_window(new, kv, dim):
+    """Where the listed blocks end before the windows start, rows still see the
+    sinks among them: in the first tile of 128 tokens, in the window's own, in
+    whole ones before."""
+    case = make(kv, dim=dim, lengths=[200, 569, 1100, 900], new=new, seed=36)
+    list_only(case, [2, 25, 19, 57])
+    # listed tokens: 32, 400, 304 and 900; the windows start at 81 (100), 450 (468),
+    # 968 (998) and 731 (800) and later
+    for sinks in (8, 130, 400):
+        check(case, window=100, sinks=sinks)
+    check(case, trees_of(new, 17), window=100, sinks=140)
+
+
 # ---------------------------------------------------------------------------
 # drafted trees
 # ---------------------------------------------------------------------------
