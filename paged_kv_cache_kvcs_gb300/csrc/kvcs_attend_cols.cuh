@@ -285,9 +285,9 @@ __device__ __forceinline__ void cols_chunk(const AttnParams &p,
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[0][i] += s2[i];
   }
-  float vsc[2];   // V scales of tokens pg, pg + 8
+  float vsc[2];   // V scales of tokens pg, pg + 8 (an infinite one makes NaN of the row's own maximum)
   if constexpr (kIsScaled<kType>) {
-    const float k0 = lds32f(scales + pg * 4), k1 = lds32f(scales + pg * 4 + 32);
+    const float k0 = finite_or_nan(lds32f(scales + pg * 4)), k1 = finite_or_nan(lds32f(scales + pg * 4 + 32));
     vsc[0] = lds32f(scales + pg * 4 + 64);
     vsc[1] = lds32f(scales + pg * 4 + 96);
 #pragma unroll

@@ -526,7 +526,7 @@ __device__ __forceinline__ bool tc_convert(const TcParams &p, TcShared &sh, TcNo
           if constexpr (kIsScaled<kType>) {
             float f = scale[half][c];
             const bool odd = partly && lane < 16 && !(fabsf(f) < __builtin_huge_valf());
-            if (odd) f = 0.0f;
+            f = odd ? 0.0f : finite_or_nan(f);
             if (half) odd_rows = __ballot_sync(0xffffffffu, odd);
             if (lane < 16)
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + tile % S::kScaleTiles * (8 * kTcKeys) +
@@ -582,8 +582,8 @@ __device__ __noinline__ float noted_weight(const AttnParams &a, int block, int s
            half_bits_to_float(reinterpret_cast<const unsigned short *>(q_row)[e], true);
   if constexpr (kIsScaled<kType>) {
     const long long at = (static_cast<long long>(block) * a.kv_heads + head) * a.map.block_size + slot;
-    dot *= a.k_scales[at];
-    vs = a.v_scales[at];
+    dot *= finite_or_nan(a.k_scales[at]);
+    vs = finite_or_nan(a.v_scales[at]);
   }
   return ex2(score_of(a, dot, 1.0f) - m) * vs;
 }

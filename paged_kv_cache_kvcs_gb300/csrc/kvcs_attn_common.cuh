@@ -339,6 +339,10 @@ __device__ __forceinline__ void scores_of(const AttnParams &p, float (&s)[2][4],
   }
 }
 
+// A token's scale: one that is not finite is NaN (an infinite K scale times a
+// negative product would else be a weight of 0).
+__device__ __forceinline__ float finite_or_nan(float scale) { return fmaf(scale, 0.0f, scale); }
+
 // D += A B, m16n8k16.
 template <bool kBf16>
 __device__ __forceinline__ void mma16816(float (&d)[4], u32 a0, u32 a1, u32 a2, u32 a3, u32 b0,

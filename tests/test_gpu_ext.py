@@ -380,6 +380,28 @@ def test_scales_of_either_sign_and_small():
     check(case)
 
 
+@pytest.mark.parametrize("kv,dim", [("int8s", 128), ("fp8s", 64), ("int8s", 80)])
+@pytest.mark.parametrize("new", [[4, 3], [70, 33]], ids=["few", "many"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("half", [0, 1], ids=["k", "v"])
+@pytest.mark.parametrize("softcap", [0.0, 12.0])
+def test_scales_not_finite_in_sight(softcap, half, value, new, kv, dim):
+    """One makes the rows that see it NaN, whatever the products' signs: here the
+    last tokens' but two, and a cached one of the second request."""
+    case = make(kv, dim=dim, lengths=[150, 300], new=new, seed=37)
+    case.set_scale(0, half, 147, value)
+    case.set_scale(1, half, 40, value)
+    out, lse, status = run(case, max_new=max(new), softcap=softcap)
+    ref = X.attention(case, softcap=softcap)
+    hit = torch.cat([X.sees(case, r)[:, t] for r, t in ((0, 147), (1, 40))])
+    assert status == 0 and hit.any() and not hit.all()
+    assert torch.isnan(out[hit.cuda()]).all()
+    if half == 0:
+        assert torch.isnan(lse[hit.cuda()]).all()
+    A.close(out[~hit.cuda()], ref[0][~hit], ref[2][~hit])
+    A.close(lse[~hit.cuda()], ref[1][~hit], ref[3][~hit])
+
+
 # ---------------------------------------------------------------------------
 # many rows over 8-bit caches
 # ---------------------------------------------------------------------------
