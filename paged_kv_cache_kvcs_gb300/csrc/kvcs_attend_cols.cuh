@@ -857,8 +857,12 @@ __global__ void __launch_bounds__(kAttendThreads, (ColsShape<kType, kDim, kTiles
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) st.l[n][i] += __shfl_xor_sync(0xffffffffu, st.l[n][i], o);
-        if constexpr (kIsScaled<kType>) {   // o relative to m
-          const float f2 = ex2(st.mv[n][i] - st.m[n][i]);   // (of no scores: 1)
+        if constexpr (kIsScaled<kType>) {
+          // o relative to m, both without the products' lift: values have all of 32
+          // bits' range, and a sum of weights 2^13 times larger would leave them 2^97
+          st.l[n][i] *= ex2(-kColsLift<kType>);
+          st.m[n][i] += kColsLift<kType>;
+          const float f2 = ex2(st.mv[n][i] - st.m[n][i]);   // (of no scores: o is 0)
 #pragma unroll
           for (int e = 0; e < kDim / 16; ++e) {
             st.o[n][e][i] *= f2;

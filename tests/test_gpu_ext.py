@@ -402,6 +402,20 @@ def test_scales_not_finite_in_sight(softcap, half, value, new, kv, dim):
     A.close(lse[~hit.cuda()], ref[1][~hit], ref[3][~hit])
 
 
+@pytest.mark.parametrize("kv", ["int8s", "fp8s"])
+@pytest.mark.parametrize("new", [[1, 1], [20, 90]], ids=["one", "many"])
+def test_large_values(kv, new):
+    """V values of some 2^116, as bfloat16 holds them, under scores alike: weights
+    near 1, whose products of random signs add up to some 2^122 before the division
+    by their sum.  (Relative to a weight of 2^-13, as fp16 products are made, that
+    would be past the largest 32-bit number.)"""
+    case = make(kv, dim=128, lengths=[300, 3000], new=new, seed=38, spread=0.5)
+    case.v_scales *= 2.0 ** 116
+    for v in case.values:
+        v[1] *= 2.0 ** 116
+    check(case, scale=0.01)
+
+
 # ---------------------------------------------------------------------------
 # many rows over 8-bit caches
 # ---------------------------------------------------------------------------
