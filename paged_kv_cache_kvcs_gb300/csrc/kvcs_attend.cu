@@ -194,7 +194,7 @@ AttnParams attn_params(const kvcs_cache *cache, int32_t block_size, const kvcs_r
 
 // What a view adds; a tree's arrays come with the workspace.
 void add_ext(AttnParams *p, const kvcs_attention_ext &x) {
-  p->sinks = static_cast<int>(std::min<int64_t>(x.sinks, kMaxRequestTokens));
+  p->sinks = std::min<int64_t>(x.sinks, 1ll << 62);   // (sums with positions stay below 2^63)
   p->k_scales = x.k_scales;
   p->v_scales = x.v_scales;
   if (x.parents) {
@@ -367,8 +367,7 @@ AttendPlan plan_attend(const AttnParams &p, const kvcs_cache &c, const kvcs_atte
     pl.units = units;
     long long key_tiles = p.tab.total_positions * p.map.block_size / std::max(1ll, R) / kTcKeys;
     if (x && p.window > 0)   // (the sinks' tiles, and the window's of a unit's rows)
-      key_tiles = std::min(key_tiles, (static_cast<long long>(p.window) + p.sinks + kTcRows / p.group +
-                                       kTcKeys) / kTcKeys);
+      key_tiles = std::min(key_tiles, (p.window + p.sinks + kTcRows / p.group + kTcKeys) / kTcKeys);
     pl.splits = static_cast<int>(std::max(
         1ll, std::min({sms / std::max(1ll, units), key_tiles / kTcMinTiles,
                        static_cast<long long>(kTcMaxSplits)})));

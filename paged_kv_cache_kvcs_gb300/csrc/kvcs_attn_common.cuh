@@ -191,7 +191,7 @@ struct AttnParams {
   float cap, inv_cap;     // capped scores: cap * log2(e) and scale / cap; 0: none
   float v_scale;
   // extended views
-  int sinks;              // request positions below it stay visible past the window
+  long long sinks;        // request positions below it stay visible past the window
   const int *place;       // trees: each new token's depth, -1 where its request's tree is bad; or null
   const u32 *kin;         // trees: [total_new][kin_words], bit j: the token sees new token j
   int kin_words;

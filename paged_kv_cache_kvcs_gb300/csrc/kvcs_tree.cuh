@@ -27,7 +27,8 @@ struct TreeParams {
   u32 *kin;             // [total_new][kin_words]
   int kin_words;
   int block_size;
-  int window, sinks;
+  int window;
+  long long sinks;
   u32 *tickets;         // zeroed on the way
   int n_tickets;
 };

@@ -181,6 +181,18 @@ def test_sinks_of_tables_that_end_before_the_window(new, kv, dim):
     check(case, trees_of(new, 17), window=100, sinks=140)
 
 
+@pytest.mark.parametrize("new", [[1, 2], [40, 90]], ids=["few", "many"])
+@pytest.mark.parametrize("kv", ["bf16", "int8s"])
+def test_sinks_past_2_to_the_30(new, kv):
+    """Request positions and sinks beyond 2^30 (tables that list the last blocks)."""
+    case = make(kv, dim=128, lengths=[2 ** 31 + 300, 2 ** 30 + 210], new=new,
+                first=[2 ** 27, 2 ** 26], seed=39)
+    check(case, window=40, sinks=2 ** 30 + 20)
+    check(case, window=40, sinks=2 ** 31 + 30)
+    check(case, window=40, sinks=2 ** 62)
+    check(case, trees_of(new, 18, 0.9), window=20, sinks=2 ** 31 + 270)
+
+
 # ---------------------------------------------------------------------------
 # drafted trees
 # ---------------------------------------------------------------------------
