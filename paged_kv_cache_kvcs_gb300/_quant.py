@@ -66,9 +66,11 @@ def _quantisation(caches, block_size, kv_dtype, dtype, k_scales, v_scales, k_sca
     return q
 
 
-def _listed(caches, *given):
+def _listed(where: str, caches, *given):
     """The caches as a list, and what goes with them as lists or None."""
     if isinstance(caches, (list, tuple)):
+        if not caches:
+            raise B.KvcsError(B.KVCS_EINVAL, where)
         for g in given:
             if g is not None and len(g) != len(caches):
                 raise ValueError("keys, values and scales must hold one tensor per cache")
@@ -87,7 +89,8 @@ def write_kv_quantised(caches, block_size: int, keys, values, slot_mapping, posi
     ``v_scales`` (one float32 tensor ``[num_blocks, num_heads, block_size]``
     per cache) get each token's and head's scale; without them ``k_scale`` and
     ``v_scale`` are the scales of all (float8 only)."""
-    caches, keys, values, k_scales, v_scales = _listed(caches, keys, values, k_scales, v_scales)
+    caches, keys, values, k_scales, v_scales = _listed("kvcs_write_kv_quantised", caches, keys, values,
+                                                       k_scales, v_scales)
     n = slot_mapping.numel()
     dev = B._current_device()
     index = dev.index
@@ -130,7 +133,8 @@ def read_kv(caches, block_size: int, pos_offsets, first_position, num_tokens, bl
     Returns ``(keys, values)``: tensors for one cache, lists for a list;
     ``values`` None for latent caches."""
     one = not isinstance(caches, (list, tuple))
-    caches, keys, values, k_scales, v_scales = _listed(caches, keys, values, k_scales, v_scales)
+    caches, keys, values, k_scales, v_scales = _listed("kvcs_read_kv", caches, keys, values, k_scales,
+                                                       v_scales)
     reqs, R, total, index = A._tables(pos_offsets, first_position, num_tokens, block_ids,
                                       total_positions)
     dev = B._current_device()
