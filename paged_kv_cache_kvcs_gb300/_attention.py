@@ -69,6 +69,16 @@ def _checked(name: str, t, dtype, n: int, index: int):
     return t.data_ptr()
 
 
+def _scales(name: str, t, cache, block_size: int, index: int):
+    """The address of a cache's scales.  (As many of them by other three extents,
+    with the heads last say, would be taken for other tokens'.)"""
+    at = _checked(name, t, torch.float32, cache.num_blocks * cache.num_heads * block_size, index)
+    if t.dim() == 3 and t.shape[1:] != (cache.num_heads, block_size):
+        raise ValueError(f"{name} must be [num_blocks, {cache.num_heads}, {block_size}]"
+                         " (heads before slots)")
+    return at
+
+
 def _tables(pos_offsets, first_position, num_tokens, block_ids, total_positions):
     """The checked request table, its request count and position count, and
     the current device's index."""
@@ -247,9 +257,8 @@ def _attend(cache, block_size, pos_offsets, first_position, num_tokens, block_id
         if parents is not None:
             ext.parents = _checked("parents", parents, torch.int32, q.shape[0], index)
         if k_scales is not None:
-            n = cache.num_blocks * cache.num_heads * block_size
-            ext.k_scales = _checked("k_scales", k_scales, torch.float32, n, index)
-            ext.v_scales = _checked("v_scales", v_scales, torch.float32, n, index)
+            ext.k_scales = _scales("k_scales", k_scales, cache, block_size, index)
+            ext.v_scales = _scales("v_scales", v_scales, cache, block_size, index)
     dev = q.device
     if out is not None:
         a.out = _checked("out", out, q.dtype, q.numel(), index)

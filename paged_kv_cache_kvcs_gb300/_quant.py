@@ -60,8 +60,7 @@ def _quantisation(caches, block_size, kv_dtype, dtype, k_scales, v_scales, k_sca
         if given is None:
             continue
         setattr(q, name, (ctypes.c_void_p * len(caches))(*[      # (which keeps it)
-            None if t is None else A._checked(name, t, torch.float32,
-                                              c.num_blocks * c.num_heads * block_size, index)
+            None if t is None else A._scales(name, t, c, block_size, index)
             for c, t in zip(caches, given)]))
     return q
 

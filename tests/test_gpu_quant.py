@@ -494,6 +494,33 @@ def test_torch_refusals():
             read(**bad)
 
 
+def test_scales_with_the_heads_last_are_refused():
+    """As many scales in another order, contiguous: each call says so.  A flat
+    tensor, and one of more blocks, are taken."""
+    case = X.ScaledCase("int8", dim=64, heads=2, bs=16, lengths=[40], new=[2], seed=44)
+    n = case.lengths[0]
+    k = torch.randn(n, 2, 64, device=DEV).bfloat16()
+    slots = case.table[3].long().repeat_interleave(16)[:n] * 16 + torch.arange(n, device=DEV) % 16
+    ends = torch.tensor([0, n], device=DEV)
+
+    def calls(ks, vs):
+        s = dict(kv_dtype=torch.int8, k_scales=ks, v_scales=vs)
+        return (lambda: K.paged_attention(case.cache, 16, *case.table, case.q, case.new_offsets, **s),
+                lambda: K.tree_attention(case.cache, 16, *case.table, case.q, case.new_offsets,
+                                         torch.full((2,), -1, dtype=torch.int32, device=DEV), **s),
+                lambda: K.write_kv_quantised(case.cache, 16, k, k, slots, torch.arange(n, device=DEV), **s),
+                lambda: K.read_kv(case.cache, 16, *case.table, ends, **s))
+    ks, vs = case.k_scales, case.v_scales
+    last = ks.transpose(1, 2).contiguous()
+    for bad in ((last, last), (ks, last), (last, vs)):
+        for call in calls(*bad):
+            with pytest.raises(ValueError, match="heads before slots"):
+                call()
+    for call in calls(ks.reshape(-1), torch.cat([vs, vs])):
+        call()
+    torch.cuda.synchronize()
+
+
 def test_offsets_past_32_bits():
     """Blocks beyond 4 GiB from the pool's base."""
     nb, H, bs, D = 1100000, 4, 16, 64
