@@ -364,6 +364,229 @@ def test_model_catches_roles_that_leave_their_work_behind():
     assert leavings(1500, ends=False) is not None
 
 
+def test_nothing_is_left_behind_whichever_wait_runs_out(monkeypatch):
+    """As above, with the machine told of the wait (``chunk`` makes its machine
+    without)."""
+    gave = 0
+    for trial in range(1500):
+        rnd = random.Random(trial)
+        units, stages = random_units(rnd), rnd.choice([5, 10])
+        who = rnd.choice(["load0", "load1", "products0", "products1", "softmax0.0", "softmax1.1"])
+        machine = Machine(trial, (who, rnd.randint(1, 12)))
+        with monkeypatch.context() as m:
+            m.setattr(f"{__name__}.Machine", lambda seed, machine=machine: machine)
+            chunk(trial, units, stages, gives_up=machine.gives_up)
+        gave += machine.gave_up > 0
+    assert gave > 750
+
+
+# ---------------------------------------------------------------------------
+# Chunks over caches of bytes
+# ---------------------------------------------------------------------------
+
+CONVERT = 2      # converting warps (four on the card)
+
+
+def over_bytes(seed, units, stages, places=None, both_scales=True, all_loaded=True,
+               wait_released=True, gives_up=None, ends=True):
+    """As chunk, over a cache of bytes: no copies, but converting warps that
+    each write their part of a stage, and of the scales of its tile; what they
+    take out of a unit they note, twice over.  units: (query tiles, token tiles).
+    places: tiles whose scales have room, the stages' number by default.
+    both_scales: a tile's scales are there when K's and V's have come.  all_loaded:
+    a unit is loaded when every warp says so.  wait_released: the warps keep one
+    unit ahead of the softmax at most."""
+    m = Machine(seed, gives_up)
+    NS, NP = stages, places or stages
+    full, empty = [Bar(CONVERT) for _ in range(NS)], [Bar(2) for _ in range(NS)]
+    q_full, p_half, p_ready = ([Bar(WARPS), Bar(WARPS)] for _ in range(3))
+    s_full, o_full, turns = ([Bar(1), Bar(1)] for _ in range(3))
+    scales = [Bar((2 if both_scales else 1) * CONVERT) for _ in range(NP)]
+    loaded, released = Bar(CONVERT if all_loaded else 1), Bar(2 * WARPS)
+    ring = [[None] * CONVERT for _ in range(NS)]
+    scale_at = [[[None] * CONVERT for _ in range(2)] for _ in range(NP)]
+    notes = [[None] * CONVERT for _ in range(2)]
+    queries, s_at, o_at = [None, None], [None, None], [None, None]
+    p_at = [[None, None] for _ in range(2)]
+    drain, out = [Bar(1), Bar(1)], {}
+
+    def expect(got, want):
+        if got != want:
+            raise Wrong(f"{got} where {want} is meant")
+
+    def convert(w):
+        tile = 0
+        for n, (_, nk) in enumerate(units):
+            for k in range(nk):
+                for half in (0, 1):
+                    s, turn = (2 * tile + half) % NS, (2 * tile + half) // NS
+                    if turn > 0:
+                        yield empty[s], turn - 1
+                    scale_at[tile % NP][half][w] = (n, k)
+                    yield None
+                    ring[s][w] = (n, half, k)
+                    yield None
+                    if both_scales or half == 0:
+                        scales[tile % NP].arrive()
+                    full[s].arrive()
+                    yield None
+                notes[n & 1][w] = n
+                tile += 1
+            notes[n & 1][w] = n
+            if n > 0 and wait_released:
+                yield released, n - 1
+            if all_loaded or w == 0:
+                loaded.arrive()
+            yield None
+
+    def products(i):
+        q = m.queues[f"T{i}"]
+        it = n_q = n_p = n_t = steps = 0
+
+        def product_s(s, n, k):
+            def run():
+                expect(ring[s], [(n, 0, k)] * CONVERT)
+                expect(queries[i], [n] * WARPS)
+                s_at[i], p_at[i] = (n, k), [None, None]
+            return run
+
+        def product_o(s, n, k, part):
+            def run():
+                expect(ring[s], [(n, 1, k)] * CONVERT)
+                expect(p_at[i][part], [(n, k)] * WARPS)
+                o_at[i] = (n, k, part)
+            return run
+        for n, (tiles, nk) in enumerate(units):
+            if i >= tiles:
+                for _ in range(2 * nk):
+                    yield full[it % NS], it // NS
+                    q.append(empty[it % NS].arrive)
+                    it += 1
+                continue
+            for k in range(nk + 1 if nk else 0):
+                do_o, do_s = k > 0, k < nk
+                vs = it % NS
+                if do_o:
+                    yield full[vs], it // NS
+                    it += 1
+                ks = it % NS
+                if do_s:
+                    yield full[ks], it // NS
+                    it += 1
+                    if k == 0:
+                        yield q_full[i], n_q
+                        n_q += 1
+                if do_o:
+                    yield p_half[i], n_p
+                if tiles == 2 and (i == 1 or steps > 0):
+                    yield turns[i], n_t
+                    n_t += 1
+                if do_o:
+                    q.append(product_o(vs, n, k - 1, 0))
+                    yield p_ready[i], n_p
+                    n_p += 1
+                    q.append(product_o(vs, n, k - 1, 1))
+                    if not do_s:
+                        q.append(o_full[i].arrive)
+                    q.append(empty[vs].arrive)
+                if do_s:
+                    q.append(product_s(ks, n, k))
+                    q.append(s_full[i].arrive)
+                    q.append(empty[ks].arrive)
+                if tiles == 2:
+                    turns[1 - i].arrive()
+                    steps += 1
+                yield None
+
+    def softmax(i, w):
+        n_s = n_o = tile0 = 0
+        for n, (tiles, nk) in enumerate(units):
+            if i < tiles and nk > 0:
+                if queries[i] is None:
+                    queries[i] = [None] * WARPS
+                queries[i][w] = n
+                q_full[i].arrive()
+                for k in range(nk):
+                    yield s_full[i], n_s
+                    n_s += 1
+                    t = tile0 + k
+                    yield scales[t % NP], t // NP
+                    expect(scale_at[t % NP][0], [(n, k)] * CONVERT)    # for the maximum
+                    yield None
+                    for part, bar in ((0, p_half[i]), (1, p_ready[i])):
+                        expect(s_at[i], (n, k))
+                        expect(scale_at[t % NP], [[(n, k)] * CONVERT] * 2)
+                        if p_at[i][part] is None:
+                            p_at[i][part] = [None] * WARPS
+                        p_at[i][part][w] = (n, k)
+                        bar.arrive()
+                        yield None
+                yield o_full[i], n_o
+                n_o += 1
+                expect(o_at[i], (n, nk - 1, 1))
+            yield loaded, n
+            expect(notes[n & 1], [n] * CONVERT)
+            yield None
+            expect(notes[n & 1], [n] * CONVERT)
+            if i < tiles:
+                out[n, i, w] = True
+            tile0 += nk
+            released.arrive()
+
+    def drained(i):
+        m.queues[f"T{i}"].append(drain[i].arrive)
+        return [(drain[i], 0)]
+
+    for w in range(CONVERT):
+        m.add(f"convert{w}", ending(convert(w), list, ends))
+    for i in (0, 1):
+        m.queues[f"T{i}"] = []
+        m.add(f"products{i}", ending(products(i), lambda i=i: drained(i), ends))
+        for w in range(WARPS):
+            m.add(f"softmax{i}.{w}", ending(softmax(i, w), list, ends))
+    m.run()
+    assert gives_up or len(out) == sum(t for t, _ in units) * WARPS
+
+
+def over_bytes_fails(what, trials, gives_up=False, **kw):
+    for trial in range(trials):
+        rnd = random.Random(trial)
+        units = [(rnd.choice([1, 2, 2]), rnd.choice([0, 1, 1, 2, 3, 4, 7]))
+                 for _ in range(rnd.randint(1, 6))]
+        who = rnd.choice(["convert0", "convert1", "products0", "products1", "softmax0.0", "softmax1.1"])
+        try:
+            over_bytes(trial, units, rnd.choice([4, 8]),
+                       gives_up=(who, rnd.randint(1, 12)) if gives_up else None, **kw)
+        except what as e:
+            return trial, e
+    return None
+
+
+def test_bytes_reach_the_products_as_the_tiles_they_are_meant_for():
+    """Stages, scales and notes, under any order of the converting warps."""
+    assert over_bytes_fails((Stall, Wrong), 2000) is None
+
+
+def test_model_catches_scales_that_are_overwritten_or_early():
+    """With room for one tile's scales the next tile's come while the softmax
+    reads; and K's scales alone do not say that V's are there."""
+    assert over_bytes_fails(Wrong, 2000, places=1) is not None
+    assert over_bytes_fails(Wrong, 2000, both_scales=False) is not None
+
+
+def test_model_catches_notes_that_are_read_early_or_overwritten():
+    """One converting warp's word does not go for the others', and without the
+    wait for the softmax its notes of two units before are lost (or a unit's
+    phase passes for the one before)."""
+    assert over_bytes_fails(Wrong, 2000, all_loaded=False) is not None
+    assert over_bytes_fails((Stall, Wrong), 2000, wait_released=False) is not None
+
+
+def test_bytes_leave_no_products_behind_when_a_wait_runs_out():
+    assert over_bytes_fails((Stall, Wrong), 1500, gives_up=True) is None
+    assert over_bytes_fails((Stall, Wrong), 1500, gives_up=True, ends=False) is not None
+
+
 # ---------------------------------------------------------------------------
 # Attention mass of many rows
 # ---------------------------------------------------------------------------
