@@ -73,7 +73,8 @@ def _scales(name: str, t, cache, block_size: int, index: int):
     """The address of a cache's scales.  (As many of them by other three extents,
     with the heads last say, would be taken for other tokens'.)"""
     at = _checked(name, t, torch.float32, cache.num_blocks * cache.num_heads * block_size, index)
-    if t.dim() == 3 and t.shape[1:] != (cache.num_heads, block_size):
+    shape = t.shape
+    if len(shape) == 3 and (shape[2] != block_size or shape[1] != cache.num_heads):
         raise ValueError(f"{name} must be [num_blocks, {cache.num_heads}, {block_size}]"
                          " (heads before slots)")
     return at
@@ -303,7 +304,8 @@ def attention_mass(cache, block_size: int, pos_offsets, first_position, num_toke
     ``[num_blocks, num_heads, block_size]``) the weights that each cached
     token gets from the last ``observe`` new tokens of its request (0: all).
     ``q``, ``new_offsets`` and the score arguments as in ``paged_attention``,
-    ``lse`` as that call returned it.  Returns ``mass``."""
+    ``lse`` as that call returned it, without sinks, scales or a tree (the sums
+    are those of plain views).  Returns ``mass``."""
     B._check_pool(cache, block_size)
     reqs, R, total, index = _tables(pos_offsets, first_position, num_tokens, block_ids,
                                     total_positions)
@@ -338,7 +340,8 @@ def evict(caches: Sequence, block_size: int, pos_offsets, first_position, num_to
     cache), and moves them to the front of the request's blocks, or of
     ``new_block_ids`` (int32, one per position).  ``block_sums`` (one word per
     block) get the filled blocks' checksums.  ``workspace`` is a CUDA uint8
-    tensor of ``eviction_workspace_bytes`` (by default allocated)."""
+    tensor of ``eviction_workspace_bytes`` (by default allocated).  Not for
+    caches with a scale for each token and head: the scales are not moved."""
     if not isinstance(caches, (list, tuple)):
         caches, scores = [caches], [scores]
     if len(scores) != len(caches):
