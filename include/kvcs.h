@@ -592,7 +592,9 @@ typedef struct kvcs_quantisation {
 
 /*
  * kvcs_write_kv_quantised -- kvcs_write_kv, quantising 16-bit keys and values on
- * the way.  The running checksum words are those of the bytes stored.  Caches
+ * the way.  The running checksum words are those of the bytes stored in the
+ * caches; no word covers the scale arrays, so what carries a cache elsewhere has to
+ * guard them itself.  Caches
  * hold one byte an element: head_bytes is the elements of a head, a multiple of
  * 8.  Arguments, padding tokens, status bits and errors as in kvcs_write_kv; keys
  * and values are 16-byte aligned.  A token with a slot past a pool leaves no scale.
@@ -635,7 +637,9 @@ int kvcs_read_kv(const kvcs_cache *caches, int32_t num_caches, int32_t block_siz
  * it gets from the observed new tokens under all query heads of the head:
  *     mass[block][head][slot] += sum_i exp(score_ij - lse_i).
  * q, scores, visibility and errors as in kvcs_paged_attention; lse is that
- * call's (read), out and the workspace are not used.
+ * call's (read), out and the workspace are not used.  Plain views alone: with the
+ * lse of a kvcs_paged_attention_ext call over scales, trees or sinks the sums are
+ * not the weights of that call.
  *   mass  float[num_blocks][num_heads][block_size], zeroed by the caller when
  *         a block is allocated.  Tokens that no observed row sees are not
  *         written.  Where requests share a block, the order in which their
@@ -691,7 +695,9 @@ int kvcs_eviction_workspace(const kvcs_cache *caches, int32_t num_caches, int32_
  * request's blocks, after which the request holds first_position *
  * block_size + B tokens (the caller lowers num_tokens and frees blocks).
  * Slots from B on keep their bytes.  All layouts but STATE; caches and other
- * arguments as in kvcs_block_checksums.
+ * arguments as in kvcs_block_checksums.  Scale arrays (kvcs_attention_ext,
+ * kvcs_quantisation) are not moved: it is not for caches with a scale for each
+ * token and head, whose kept tokens would stand under other tokens' scales.
  *
  * Blocks that the call writes must belong to one request alone (in place:
  * all its blocks), listed once; the caches' pools and scores must not overlap.

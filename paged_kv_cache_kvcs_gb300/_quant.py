@@ -87,7 +87,8 @@ def write_kv_quantised(caches, block_size: int, keys, values, slot_mapping, posi
     ``kv_dtype`` (``torch.int8`` or ``torch.float8_e4m3fn``).  ``k_scales`` and
     ``v_scales`` (one float32 tensor ``[num_blocks, num_heads, block_size]``
     per cache) get each token's and head's scale; without them ``k_scale`` and
-    ``v_scale`` are the scales of all (float8 only)."""
+    ``v_scale`` are the scales of all (float8 only).  ``block_sums`` cover the
+    caches' bytes, not the scales."""
     caches, keys, values, k_scales, v_scales = _listed("kvcs_write_kv_quantised", caches, keys, values,
                                                        k_scales, v_scales)
     n = slot_mapping.numel()
