@@ -52,8 +52,8 @@ struct AttendLaunch {
   static void shape(int dim, int kind, int sms, int *grid, long long *part_floats);
   static cudaError_t attend(const AttnParams &p, int kind, int grid, bool after_zero,
                             cudaStream_t st);
-  // the tensor-memory kernel (16-bit caches, heads of 64 or 128), and the
-  // joining of its parts
+  // the tensor-memory kernel (heads of 64 or 128; 16-bit caches, in extended views
+  // 8-bit ones of bf16 queries as well, without the maps), and the joining of its parts
   static cudaError_t attend_tc(const TcParams &p, const CUtensorMap &k, const CUtensorMap &v,
                                int grid, bool early, cudaStream_t st);
   static cudaError_t mass(const AttnParams &p, int sms, cudaStream_t st);
