@@ -315,7 +315,7 @@ constexpr int kNarrowRows = 16;
 // requests of 2048 tokens 235 and 344 us, 300 and 344, 546 and 346; 16 of 2048 81 and
 // 94, 102 and 94, 169 and 95; one of 32,768 80 and 96, 104 and 96, 146 and 99; one of
 // 1024 29 and 31, 39 and 31, 40 and 34.  Chunks of 2048 at the end of 4 of 8192 tokens
-// 6361 and 1838, over int8 6319 and 1644.
+// 6361 and 1827, over int8 6319 and 1643.
 constexpr int kTcBytesRows = 48;
 // Observed rows the small mass kernel takes, at most (it against the
 // tensor-memory one, 64 requests of 2048 tokens: 16 rows 52 and 107 us, 32

@@ -32,12 +32,15 @@
 // relative to mv_i = max_j (z_ij + log2 |vs_j|) as l is to m_i, and brought back to
 // m_i at the group's end.
 //
-// Bound: by the bytes for 16-bit caches, by conversions and products for 8-bit ones.
-// Measured (32 query heads to 8 KV heads of 128): 64 requests of 512 to 4096 tokens,
-// one token each, int8 with scales, 85 us, 3.7 TB/s; 64 of 600 to 8192 under a
-// window of 1024 with 4 first tokens, bf16, 63 us, 4.2 TB/s; 32 rows (trees of 4,
-// 64 query heads) over 32 requests of 1000 to 4096, e4m3 with scales, 123 us,
-// 1.4 TB/s (read twice, half of the second time from L2).
+// Bound: by the bytes for 16-bit caches; for 8-bit ones by conversions, permutes and
+// products waiting for one another (half of the issue slots are used, by 15 warps an
+// SM; the largest share of their waits are instructions' own latencies).
+// Measured (32 query heads to 8 KV heads of 128; one call after another, a replayed
+// graph, as the comparisons here are, takes some 3 us more): 64 requests of 512 to
+// 4096 tokens, one token each, int8 with scales, 82 us, 3.8 TB/s (replayed 84.5, e4m3 82.5); 64 of 600
+// to 8192 under a window of 1024 with 4 first tokens, bf16, 59 us, 4.5 TB/s; 32 rows
+// (trees of 4, 64 query heads) over 32 requests of 1000 to 4096, e4m3 with scales, 119
+// us, 1.5 TB/s (read twice, half of the second time from L2).
 // The step over int8 took 122 us with kvcs_attend.cuh's orientation, 97 with three
 // CTAs an SM and the copies' places made anew for each.
 #pragma once
@@ -584,7 +587,10 @@ __device__ __forceinline__ void cols_queries(const AttnParams &p, const Request 
 
 // Any chunk; returns its mask of readable tokens.  Tokens outside [lo, hi) but
 // for those below sink_keys, and tokens of bad blocks, become zeros.  `scales`:
-// where the chunk's scales go.
+// where the chunk's scales go.  It takes all chunks of pools without runs of 16 tokens
+// or of other widths: 64 requests under a window of 1024 (above), blocks of 8 and 24
+// slots 92 us and 91 where 16 take 62, heads of 96 92; int8 with scales, heads of 96 and
+// blocks of 24 slots 68.  (X-split pools have runs, whose pieces lie apart: 94.)
 template <int kType, int kDim>
 __device__ __noinline__ u32 cols_load_any(const AttnParams &p, long long pos0, int head, u32 chunk,
                                           int key0, int lo, int hi, int sink_keys, u32 scales) {

@@ -46,7 +46,7 @@
 // some row sees only in part: of a tree those of its new tokens and of the windows'
 // ends.  The trees' masks are made by the kernel before, which this one overlaps
 // until it reads them.  4 requests of 2048 new tokens over 8192 under a window of
-// 2048, 64 first tokens kept (the same heads): 279 us, 985 TFLOP/s, 51% of the
+// 2048, 64 first tokens kept (the same heads): 279 us, 1016 TFLOP/s, 54% of the
 // measured burst rate; what it leaves are 10 us from a unit's last product to the next
 // one's first, of 17 tiles and 1.8 us each.  Trees of 16 tokens of 64 requests over
 // 512 to 4096: 176 us, 3.5 TB/s: units of one query tile, so that neither tile's
@@ -64,8 +64,9 @@
 // taken 64 tokens at a time, once for their maximum and once for the weights, so that
 // four warpgroups have registers enough.  A token with a scale or value that is not
 // finite, where some row may not see it, is taken out and noted, as above.
-// Chunks of 2048 of 4 requests over 8192: int8 1644 us, e4m3 1838 (349 TFLOP/s over all
-// (row, token) pairs; 16-bit values 646; kvcs_attend_cols.cuh's kernel 6319 and 6361).
+// Chunks of 2048 of 4 requests over 8192: int8 1643 us, e4m3 1827 (585 and 527 TFLOP/s
+// over the (row, token) pairs that are seen; 16-bit values 621 us beside them, 1550;
+// kvcs_attend_cols.cuh's kernel 6319 and 6361 us).
 // What bounds it is the conversion, 32,768 values a tile with some five instructions
 // for two of them (without it 1165), then the weights (without both 527).  As four
 // warps for K and four for V over copies in shared memory, which leave room for three
